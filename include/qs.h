@@ -436,6 +436,102 @@ QS_API int qs_top_logprobs(int64_t B, const int32_t* cand_ids, const float* cand
                     int32_t* top_ids, float* top_logprobs, int32_t* row_status,
                     void* stream);
 
+/* Log-probabilities of given tokens under the full tempered, masked softmax of
+ * each row (no top-k, no top-p), with the row's entropy and its most probable
+ * tokens. With L the legal tokens of the row, m = max over L of z and
+ * S = sum over L of exp((z - m) / T):
+ *   log p_t = (z_t - m) / T - ln S,   H = -sum over L of p ln p.
+ *
+ * logits, bitmask   as for qs_filter_mask (dtype float32 or bfloat16)
+ * temperature  [B] float32, optional (NULL: 1); finite and > 0 (0, the greedy
+ *              rows of qs_sample, has no finite log-probabilities here)
+ * tokens       [B][G] int32, 1 <= G <= 1024: the tokens to score, any order,
+ *              repeats allowed; -1 (what qs_sample writes on an error row, and
+ *              the padding of short rows) is an empty slot
+ * logprobs     [B][G] float32 out: log p_t; -inf for a token that is illegal
+ *              or whose logit is -inf; 0 in an empty slot
+ * row_max      [B] float32 out: m
+ * log_sum      [B] float32 out: ln S (the natural log of the normaliser is
+ *              row_max / T + log_sum; kept apart so that no bits are lost)
+ * entropy      [B] float32 out, optional: H in nats
+ * top_n        0 <= top_n <= 64
+ * top_ids      [B][top_n] int32 out (top_n > 0): the largest finite legal
+ *              logits' ids, descending, ties by ascending id; -1 past the last
+ * top_logprobs [B][top_n] float32 out (top_n > 0): their log p; -inf past the
+ *              last
+ * row_status   [B] int32 out: QS_ROW_BAD_PARAM (T, or a token outside
+ *              [-1, V)), then as for qs_filter_mask. An error row gets NaN in
+ *              logprobs (empty slots stay 0), row_max, log_sum and entropy and
+ *              empty top slots.
+ * workspace    qs_token_logprobs_workspace_bytes(B, V, dtype, top_n) bytes of
+ *              device scratch, 256-byte aligned (NULL / 0 when that is 0), as
+ *              for qs_filter_mask: its contents on entry do not matter, calls
+ *              that may overlap in time need different ones.
+ * Sums are held in float32 per lane and joined in a fixed order: the same call
+ * gives the same bits. Logits are read once. */
+QS_API size_t qs_token_logprobs_workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n);
+QS_API int qs_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V,
+                      int64_t row_stride, const float* temperature, const uint32_t* bitmask,
+                      int64_t bitmask_stride, const int32_t* tokens, int64_t G, float* logprobs,
+                      float* row_max, float* log_sum, float* entropy, int64_t top_n,
+                      int32_t* top_ids, float* top_logprobs, int32_t* row_status,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of qs_token_logprobs with respect to the logits. With gl the
+ * gradients of the log-probabilities and gH that of the entropy,
+ *   dz_i = (1/T) [ sum over g of gl_g (1[i = t_g] - p_i) - gH p_i (ln p_i + H) ]
+ * for legal i and 0 for illegal ones. A token named by several slots gets the
+ * sum of theirs, in slot order; empty slots (-1) count for nothing whatever
+ * their gl holds.
+ *
+ * logits, temperature, bitmask, tokens  the forward call's inputs
+ * row_max, log_sum, row_status [B]      the forward call's outputs (inputs here)
+ * grad_logprobs [B][G] float32
+ * entropy, grad_entropy [B] float32, both or neither: the forward call's H, gH
+ * grad_logits  [B][grad_stride] out, in the logits' dtype, every element of
+ *              the first V columns written (0 on rows whose row_status is not
+ *              QS_ROW_OK), columns from V on left as they are; 16-byte aligned,
+ *              grad_stride >= V and grad_stride * element size a multiple of 16.
+ *              It may be the logits' own buffer (same address and stride); any
+ *              other overlap is not allowed.
+ * Computed in float32, rounded once to the dtype (nearest even). Tokens outside
+ * [0, V) are ignored. One kernel launch on `stream`; nothing is allocated. */
+QS_API int qs_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_t V,
+                      int64_t row_stride, const float* temperature, const uint32_t* bitmask,
+                      int64_t bitmask_stride, const int32_t* tokens, int64_t G,
+                      const float* row_max, const float* log_sum, const int32_t* row_status,
+                      const float* grad_logprobs, const float* entropy,
+                      const float* grad_entropy, void* grad_logits, int64_t grad_stride,
+                      void* stream);
+
+/* Logits of hidden states under an output projection held in 4 bits with group
+ * scales, in the layout the calls above read:
+ *   y[b][v] = sum over groups g of scale[v][g] *
+ *             sum over k in g of hidden[b][k] * (code[v][k] - zero[v][g])
+ *
+ * hidden       [B][hidden_stride] bfloat16, 16-byte aligned, hidden_stride a
+ *              multiple of 8 and >= K
+ * codes        [V][codes_stride] bytes, 16-byte aligned, codes_stride a
+ *              multiple of 16 and >= K / 2: two codes 0..15 a byte, the even
+ *              column in the low half
+ * scales       [V][scale_stride] float32 or bfloat16 (scale_dtype), one per
+ *              group of `group` columns; scale_stride >= K / group
+ * zeros        [V][zero_stride] uint8, optional (NULL: 8 everywhere)
+ * group        32, 64 or 128; K a multiple of it, K <= 65536
+ * logits       [B][row_stride] float32 or bfloat16 out (logits_dtype), 16-byte
+ *              aligned, row_stride * element size a multiple of 16, columns
+ *              from V on left as they are
+ * V at most 2^24. Products are exact (a bf16 factor and a code), sums are held
+ * in float32 and each logit is rounded once. A row of `hidden` that holds an
+ * infinity or a NaN gives no finite logit (NaN, or an infinity). Made for
+ * the 1 to 64 rows of a decode step; more rows read the weights once per 64.
+ * One kernel launch on `stream`; nothing is allocated. */
+QS_API int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidden_stride,
+                      const uint8_t* codes, int64_t V, int64_t codes_stride, const void* scales,
+                      int scale_dtype, int64_t scale_stride, const uint8_t* zeros,
+                      int64_t zero_stride, int64_t group, void* logits, int logits_dtype,
+                      int64_t row_stride, void* stream);
+
 /* Library version string (static storage). */
 QS_API const char* qs_version(void);
 

@@ -19,6 +19,8 @@ Modules:
   min(1, p/q), else resample from max(0, p - q)) over candidate lists.
 * ``penalties`` — repetition and presence penalties over each row's history,
   and an additive logit bias list per row.
+* ``scoring``  — log-probabilities of given tokens with entropy and top tokens,
+  their gradient, and the output head with 4-bit weights.
 * ``batch``    — row loops over a whole [B, V] batch with the exact input layout
   the C-ABI uses (fp32 or bf16 bit patterns, packed uint32 bitmask).
 """
@@ -35,3 +37,4 @@ from .batch import decode_logits, filter_batch, sample_batch, argmax_batch  # no
 from .spec import spec_verify_row, spec_verify_batch  # noqa: F401
 from .penalties import (apply_penalties_row, apply_penalties_batch,  # noqa: F401
                         apply_logit_bias_row, apply_logit_bias_batch)
+from .scoring import score_row, grad_row, head_weights  # noqa: F401

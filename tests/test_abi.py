@@ -303,3 +303,83 @@ def test_processed_rejects_bad_arguments(lib):
     need = lib.qs_processors_workspace_bytes(4, 64, 1)
     assert need == 4 * 256
     assert lib.qs_processors_workspace_bytes(4, 155649, 1) == 0
+
+
+def score(lib, **kw):
+    a = dict(logits=A16, dtype=0, B=4, V=64, stride=64, T=None, bm=None, bms=0, tokens=A16, G=2,
+             lp=A16, mx=A16, ls=A16, ent=None, n=0, ids=None, tlp=None, status=A16, ws=WS,
+             wsn=WSN)
+    a.update(kw)
+    return lib.qs_token_logprobs(a["logits"], a["dtype"], a["B"], a["V"], a["stride"], a["T"],
+                                 a["bm"], a["bms"], a["tokens"], a["G"], a["lp"], a["mx"],
+                                 a["ls"], a["ent"], a["n"], a["ids"], a["tlp"], a["status"],
+                                 a["ws"], a["wsn"], None)
+
+
+ODD = ctypes.c_void_p(0x100002)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(logits=None), dict(dtype=2), dict(B=-1), dict(B=1 << 22), dict(V=0), dict(stride=60),
+    dict(stride=65), dict(logits=ODD), dict(T=ODD), dict(bm=A16, bms=1), dict(tokens=None),
+    dict(tokens=ODD), dict(G=0), dict(G=1025), dict(lp=None), dict(mx=None), dict(ls=None),
+    dict(ent=ODD), dict(n=-1), dict(n=65, ids=A16, tlp=A16), dict(n=3), dict(n=3, ids=A16),
+    dict(n=3, ids=A16, tlp=ODD), dict(status=None),
+])
+def test_token_logprobs_rejects_bad_arguments(lib, kw):
+    assert score(lib, **kw) == _lib.QS_ERR_INVALID_ARG
+
+
+def test_token_logprobs_workspace(lib):
+    assert score(lib, B=0) == _lib.QS_OK
+    f = lib.qs_token_logprobs_workspace_bytes
+    for bad in ((0, 64, 0, 0), (-1, 64, 0, 0), (1 << 22, 64, 0, 0), (4, 0, 0, 0),
+                (4, 64, 2, 0), (4, 64, 0, 65), (4, 64, 0, -1)):
+        assert f(*bad) == 0
+    for shape in ((1, 32000, 0, 0), (256, 151936, 1, 20), (2048, 151936, 1, 0), (1, 1 << 30, 0, 64),
+                  ((1 << 22) - 1, 64, 1, 0), (1, 1, 0, 1)):
+        need = f(*shape)
+        assert need <= 1 << 32
+        if need:
+            kw = dict(B=shape[0], V=shape[1], dtype=shape[2], stride=-(-shape[1] // 8) * 8,
+                      n=shape[3], ids=A16, tlp=A16)
+            assert score(lib, **kw, wsn=need - 1) == _lib.QS_ERR_WORKSPACE
+            assert score(lib, **kw, ws=None) == _lib.QS_ERR_WORKSPACE
+            assert score(lib, **kw, ws=ctypes.c_void_p(0x400080)) == _lib.QS_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(logits=None), dict(dtype=3), dict(B=-1), dict(V=0), dict(stride=65), dict(tokens=None),
+    dict(G=0), dict(G=1025), dict(mx=None), dict(ls=None), dict(status=None), dict(g=None),
+    dict(g=ODD), dict(ent=A16), dict(gent=A16), dict(grad=None), dict(grad=ODD), dict(gs=60),
+    dict(gs=65), dict(T=ODD), dict(bm=A16, bms=1), dict(grad=A16, gs=128),
+])
+def test_token_logprobs_backward_rejects_bad_arguments(lib, kw):
+    a = dict(logits=A16, dtype=0, B=4, V=64, stride=64, T=None, bm=None, bms=0, tokens=A16, G=2,
+             mx=A16, ls=A16, status=A16, g=A16, ent=None, gent=None, grad=A8, gs=64)
+    a.update(kw)
+    assert lib.qs_token_logprobs_backward(
+        a["logits"], a["dtype"], a["B"], a["V"], a["stride"], a["T"], a["bm"], a["bms"],
+        a["tokens"], a["G"], a["mx"], a["ls"], a["status"], a["g"], a["ent"], a["gent"],
+        a["grad"], a["gs"], None) == _lib.QS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=None), dict(x=ODD), dict(B=-1), dict(B=1 << 22), dict(K=0), dict(K=48), dict(K=65664),
+    dict(xs=248), dict(xs=260), dict(codes=None), dict(codes=ctypes.c_void_p(0x100008)),
+    dict(V=0), dict(V=(1 << 24) + 1), dict(cs=112), dict(cs=136), dict(s=None), dict(s=ODD),
+    dict(sd=2), dict(ss=3), dict(zeros=A16, zs=3), dict(group=16), dict(group=96),
+    dict(group=256), dict(logits=None), dict(logits=ODD), dict(ld=2), dict(ls=60), dict(ls=66),
+])
+def test_head_logits_rejects_bad_arguments(lib, kw):
+    a = dict(x=A16, B=2, K=256, xs=256, codes=A16, V=64, cs=128, s=A16, sd=0, ss=4, zeros=None,
+             zs=0, group=64, logits=A8, ld=0, ls=64)
+    a.update(kw)
+    assert lib.qs_head_logits(a["x"], a["B"], a["K"], a["xs"], a["codes"], a["V"], a["cs"],
+                              a["s"], a["sd"], a["ss"], a["zeros"], a["zs"], a["group"],
+                              a["logits"], a["ld"], a["ls"], None) == _lib.QS_ERR_INVALID_ARG
+
+
+def test_head_logits_empty_batch(lib):
+    assert lib.qs_head_logits(None, 0, 256, 256, None, 64, 128, None, 0, 4, None, 0, 64, None, 0,
+                              64, None) == _lib.QS_OK

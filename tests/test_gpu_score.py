@@ -1,0 +1,464 @@
+"""qs_token_logprobs and qs_token_logprobs_backward (through the binding) against
+the oracle in fp64.
+
+Tolerances, with u = 2^-24 (half a float32 step) and a_i = (z_i - m) / T:
+- a_i is a difference, a product with a rounded 1 / T (or a quotient) and the
+  rounding of both: at most 4 u |a_i|. A weight exp a_i then carries
+  4 u |a_i| + 4 u relative (the exponential itself good to two units).
+- S is a sum of positive terms along at most `depth` additions: relative
+  depth u + 4 u sum p|a| + 4 u. log S adds 2 u |log S| + 4 u.
+- log p_t = a_t - log S: 4 u |a_t| + error of log S + u |log p_t|.
+- H = log S + sum p|a|, both terms positive: error of log S, plus
+  (2 depth + 16) u sum p|a| + 4 u sum p a^2 for the second.
+- a gradient element: p (..) with p's relative error 4 u |a| + 8 u (the row
+  statistics are inputs), the G slot gradients summed in order, one final
+  rounding of half a step of the output type.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def depth(V):
+    """Additions on a term's way into S: at most 64 in a lane's block, then the
+    blocks of a lane, the lanes, the waves and the parts of a row."""
+    return 128 + V / 2 ** 14
+
+
+@pytest.fixture(scope="module")
+def qs():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import top_sampling_vocabs_amd as qs
+    qs.load()
+    return qs
+
+
+def bf16(x):
+    """float32 values rounded to bf16 by truncation (exact in both types)."""
+    return (np.asarray(x, np.float32).view(np.uint32) & 0xFFFF0000).view(np.float32)
+
+
+def pack(legal):
+    B, V = legal.shape
+    W = -(-V // 32)
+    bits = np.zeros((B, W * 32), np.uint8)
+    bits[:, :V] = legal
+    return np.packbits(bits, axis=1, bitorder="little").view(np.uint32).view(np.int32)
+
+
+def on_gpu(z, dtype, extra=0):
+    """[B, V] on the GPU in padded rows (extra: more padding, filled with a value
+    that would win every row)."""
+    import torch
+    B, V = z.shape
+    step = 4 if dtype == "f32" else 8
+    buf = np.full((B, (-(-V // step) + extra) * step), 3e38, np.float32)
+    buf[:, :V] = z
+    t = torch.from_numpy(buf).cuda()
+    if dtype == "bf16":
+        t = t.to(torch.bfloat16)
+    return t[:, :V]
+
+
+def make(seed, B, V, kind):
+    rng = np.random.default_rng(seed)
+    if kind == "normal":
+        z = rng.normal(0, 3, (B, V))
+    elif kind == "ties":
+        z = rng.integers(-2, 3, (B, V)).astype(float)
+    elif kind == "equal":
+        z = np.full((B, V), -7.25)
+    elif kind == "falling":
+        z = np.broadcast_to(-np.arange(V) * (40.0 / V), (B, V)).copy()
+    elif kind == "rising":
+        z = np.broadcast_to(np.arange(V) * (40.0 / V), (B, V)).copy()
+    elif kind == "stripe":
+        # the largest tokens all belong to one lane's places
+        z = rng.normal(0, 1, (B, V))
+        z[:, np.arange(V) % 512 < 8] += 50.0
+    elif kind == "wide":
+        z = rng.normal(0, 1, (B, V)) * 10.0 ** rng.integers(-3, 5, (B, V))
+    elif kind == "negative":
+        z = -np.abs(rng.normal(0, 3, (B, V))) - 1e4
+    elif kind == "zeros":
+        z = np.where(rng.random((B, V)) < 0.5, 0.0, -0.0)
+    else:
+        raise ValueError(kind)
+    return bf16(z)
+
+
+def tokens_for(rng, B, V, G, pad=True):
+    t = rng.integers(0, V, (B, G)).astype(np.int32)
+    if pad:
+        t[rng.random((B, G)) < 0.15] = -1
+    return t
+
+
+def run(qs, z, dtype, tokens, T=None, legal=None, top_n=0, extra=0, workspace=None):
+    import torch
+    lg = on_gpu(z, dtype, extra)
+    d = dict(temperature=None if T is None else torch.from_numpy(T).cuda(),
+             bitmask=None if legal is None else torch.from_numpy(pack(legal)).cuda())
+    tok = torch.from_numpy(tokens).cuda()
+    out = qs.token_logprobs(lg, tok, entropy=True, top_n=top_n, workspace=workspace, **d)
+    torch.cuda.synchronize()
+    return lg, tok, d, out
+
+
+def check_forward(z, tokens, T, legal, top_n, out):
+    B, V = z.shape
+    o = {k: v.cpu().numpy().astype(np.float64) for k, v in out.items()}
+    lps = o["logprobs"].reshape(B, -1)
+    for r in range(B):
+        w = oracle.score_row(z[r], None if legal is None else legal[r],
+                             1.0 if T is None else T[r], tokens[r], top_n)
+        assert o["status"][r] == w["status"], (r, o["status"][r], w["status"])
+        if w["status"] != oracle.ROW_OK:
+            assert np.array_equal(lps[r], w["logprobs"], equal_nan=True), r
+            for k in ("row_max", "log_sum", "entropy"):
+                assert np.isnan(o[k][r]), (r, k)
+        else:
+            fin = w["p"] > 0
+            X = (w["p"][fin] * -w["a"][fin]).sum()
+            X2 = (w["p"][fin] * w["a"][fin] ** 2).sum()
+            t_S = U * (depth(V) + 4 * X + 2 * abs(w["log_sum"]) + 8)
+            t_H = t_S + U * ((2 * depth(V) + 16) * X + 4 * X2 + 2 * w["entropy"])
+            assert o["row_max"][r] == w["row_max"], r
+            assert abs(o["log_sum"][r] - w["log_sum"]) <= t_S, (r, o["log_sum"][r], w["log_sum"])
+            assert abs(o["entropy"][r] - w["entropy"]) <= t_H, (r, o["entropy"][r], w["entropy"])
+            for got, want in [(lps[r], w["logprobs"])] + (
+                    [(o["top_logprobs"][r], w["top_logprobs"])] if top_n else []):
+                # what lies below the least float32 is -inf in the output's type
+                want = np.where(want < np.finfo(np.float32).min, -np.inf, want)
+                fin = np.isfinite(want)
+                assert np.array_equal(got[~fin], want[~fin]), (r, got, want)
+                tol = t_S + U * (4 * np.abs(want[fin] + w["log_sum"]) + np.abs(want[fin]))
+                assert (np.abs(got[fin] - want[fin]) <= tol).all(), (r, got, want)
+            empty = tokens[r] == -1
+            assert (lps[r][empty] == 0).all(), r
+        if top_n:
+            assert np.array_equal(o["top_ids"][r], w["top_ids"]), \
+                (r, o["top_ids"][r][:8], w["top_ids"][:8])
+            gone = w["top_ids"] < 0
+            assert (o["top_logprobs"][r][gone] == -np.inf).all(), r
+
+
+SIZES = [1, 2, 7, 8, 9, 63, 64, 65, 511, 512, 513, 1000, 2047, 2049, 5003, 8193, 16384, 16385,
+         40003, 131080, 300007]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", SIZES)
+def test_sizes(qs, V, dtype):
+    """Every length class, with mask, temperatures, padded slots, top tokens."""
+    rng = np.random.default_rng(V)
+    B = 5
+    z = make(V, B, V, "normal")
+    legal = rng.random((B, V)) < 0.4
+    legal[0] = True
+    legal[3] = False                       # a row without a legal token
+    legal[4] = False
+    legal[4, V // 2] = True                # and one with a single one
+    z[~legal] = np.array([np.nan, np.inf, 3e38, -np.inf], np.float32)[
+        rng.integers(0, 4, (~legal).sum())]
+    T = rng.uniform(0.3, 2.0, B).astype(np.float32)
+    tokens = tokens_for(rng, B, V, 3)
+    top_n = int(rng.choice([0, 1, 5, 20, 64]))
+    print(f"score V={V} {dtype} top_n={top_n}", flush=True)
+    for n in sorted({0, top_n, 64}):
+        _, _, _, out = run(qs, z, dtype, tokens, T, legal, n, extra=1)
+        check_forward(z, tokens, T, legal, n, out)
+    free = make(V + 1, B, V, "normal")
+    _, _, _, out = run(qs, free, dtype, tokens, None, None, 7)
+    check_forward(free, tokens, None, None, 7, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["ties", "equal", "falling", "rising", "stripe", "wide",
+                                  "negative", "zeros"])
+@pytest.mark.parametrize("V", [700, 9001, 70000])
+def test_values(qs, V, kind, dtype):
+    """Ties, ordered rows, one lane's places on top, wide ranges, all negative."""
+    print(f"score values V={V} {kind} {dtype}", flush=True)
+    B = 3
+    z = make(V, B, V, kind)
+    tokens = tokens_for(np.random.default_rng(V), B, V, 2, pad=False)
+    for n in (1, 20, 64):
+        _, _, _, out = run(qs, z, dtype, tokens, None, None, n)
+        check_forward(z, tokens, None, None, n, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 40, 3001, 50000])
+def test_row_errors(qs, V, dtype):
+    """Every row error beside rows that are fine, and values that are legal."""
+    print(f"score errors V={V} {dtype}", flush=True)
+    rng = np.random.default_rng(V)
+    B = 16
+    z = make(5, B, V, "normal")
+    T = np.ones(B, np.float32)
+    legal = np.ones((B, V), bool)
+    tokens = tokens_for(rng, B, V, 4)
+    z[0, V - 1] = np.nan
+    z[1, 0] = np.inf
+    z[2, :] = -np.inf
+    z[3, :] = -np.inf
+    z[3, V // 2] = np.nan                  # NaN among -inf
+    legal[4] = False
+    z[5, V - 1] = np.nan
+    legal[5, V - 1] = V == 1               # NaN at an illegal place
+    T[6], T[7], T[8], T[9] = 0.0, -1.0, np.nan, np.inf
+    tokens[10, 0] = V
+    tokens[11, 3] = -2
+    z[12, : V // 2] = -np.inf              # legal -inf tokens
+    T[13] = 1e-38
+    T[14] = 3e38
+    tokens[15] = -1
+    _, _, _, out = run(qs, z, dtype, tokens, T, legal, 9)
+    check_forward(z, tokens, T, legal, 9, out)
+
+
+@pytest.mark.parametrize("G", [1, 2, 63, 300, 1024])
+def test_many_tokens(qs, G):
+    """Many given tokens of a row, repeats among them."""
+    print(f"score G={G}", flush=True)
+    rng = np.random.default_rng(G)
+    z = make(G, 4, 6007, "normal")
+    tokens = tokens_for(rng, 4, 6007, G)
+    tokens[1] = tokens[1, 0]
+    _, _, _, out = run(qs, z, "bf16", tokens, None, None, 0)
+    check_forward(z, tokens, None, None, 0, out)
+
+
+@pytest.mark.parametrize("B,V", [(1, 151936), (2, 600), (300, 2000), (1500, 777)])
+def test_batches(qs, B, V):
+    """From one long row (spread over the GPU) to more rows than compute units;
+    the same call twice gives the same bits."""
+    import torch
+    print(f"score batch B={B} V={V}", flush=True)
+    z = make(B, B, V, "normal")
+    tokens = tokens_for(np.random.default_rng(B), B, V, 1)
+    for dtype in ("f32", "bf16"):
+        _, _, _, out = run(qs, z, dtype, tokens, None, None, 20)
+        check_forward(z, tokens, None, None, 20, out)
+        _, _, _, again = run(qs, z, dtype, tokens, None, None, 20)
+        for k in out:
+            assert torch.equal(out[k].view(torch.int32), again[k].view(torch.int32)), k
+
+
+# --------------------------------------------------------------------------
+
+def check_grad(z, dtype, tokens, T, legal, gl, gH, out, grad):
+    B, V = z.shape
+    got = grad.float().cpu().numpy().astype(np.float64)
+    st = {k: v.cpu().numpy() for k, v in out.items()}
+    half = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+    for r in range(B):
+        if st["status"][r] != oracle.ROW_OK:
+            assert (got[r] == 0).all(), r
+            continue
+        Tr = 1.0 if T is None else float(T[r])
+        lg = None if legal is None else legal[r]
+        H = st["entropy"][r]
+        want = oracle.grad_row(z[r], lg, Tr, tokens[r], gl[r], None if gH is None else gH[r],
+                               st["row_max"][r], st["log_sum"][r], H)
+        ok = np.ones(V, bool) if lg is None else lg
+        assert (got[r][~ok] == 0).all(), r
+        with np.errstate(over="ignore", invalid="ignore"):
+            a = np.where(ok, (z[r].astype(np.float64) - st["row_max"][r]) / Tr, 0.0)
+        a = np.maximum(a, -1e4)
+        lp = a - st["log_sum"][r]
+        p = np.exp(lp)
+        live = tokens[r] >= 0
+        g_abs = np.abs(gl[r][live]).sum()
+        gh = 0.0 if gH is None else abs(float(gH[r]))
+        slot = np.zeros(V)
+        for t, g in zip(tokens[r][live], gl[r][live]):
+            slot[t] += abs(g)
+        n = len(tokens[r])
+        tol = U / Tr * (p * ((4 * np.abs(a) + 24 + n) * (g_abs + gh * (np.abs(lp) + abs(H)))
+                             + gh * 8 * np.abs(a)) + (n + 4) * slot)
+        # a p below the least normal float32, 2^-126, may be taken as 0, and so may
+        # an element below it: off by 2^-126 times p's factor, and by 2^-126
+        tol = tol + 2.0 ** -126 * (1 + (g_abs + gh * (np.abs(lp) + abs(H))) / Tr)
+        tol = tol * 1.01 + half * np.abs(want) * 1.01
+        bad = np.abs(got[r] - want) > tol
+        assert not bad.any(), (r, np.nonzero(bad)[0][:4], got[r][bad][:4], want[bad][:4])
+
+
+def run_grad(qs, z, dtype, tokens, T, legal, gl, gH, extra=0, **kw):
+    import torch
+    lg, tok, d, out = run(qs, z, dtype, tokens, T, legal, extra=extra)
+    ent = {} if gH is None else dict(entropy=out["entropy"], grad_entropy=torch.from_numpy(gH).cuda())
+    grad = qs.token_logprobs_backward(lg, tok, out["row_max"], out["log_sum"], out["status"],
+                                      torch.from_numpy(gl).cuda(), **d, **ent, **kw)
+    torch.cuda.synchronize()
+    return lg, out, grad
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", SIZES)
+def test_grad_sizes(qs, V, dtype):
+    print(f"grad V={V} {dtype}", flush=True)
+    rng = np.random.default_rng(V)
+    B = 5
+    z = make(V, B, V, "normal")
+    legal = rng.random((B, V)) < 0.4
+    legal[0] = True
+    legal[3] = False
+    z[~legal] = np.array([np.nan, np.inf, 3e38, -np.inf], np.float32)[
+        rng.integers(0, 4, (~legal).sum())]
+    z[1, legal[1]] = np.where(rng.random(legal[1].sum()) < 0.3, -np.inf, z[1, legal[1]])
+    T = rng.uniform(0.3, 2.0, B).astype(np.float32)
+    tokens = tokens_for(rng, B, V, 3)
+    tokens[2, 1:] = tokens[2, 0]           # one token in several slots
+    gl = rng.normal(0, 1, (B, 3)).astype(np.float32)
+    gl[tokens == -1] = np.nan              # what an empty slot holds is not read into sums
+    gH = rng.normal(0, 0.1, B).astype(np.float32)
+    _, out, grad = run_grad(qs, z, dtype, tokens, T, legal, gl, gH, extra=1)
+    check_grad(z, dtype, tokens, T, legal, gl, gH, out, grad)
+    z = make(V + 1, B, V, "normal")
+    gl = rng.normal(0, 1, (B, 1)).astype(np.float32)
+    t1 = tokens_for(rng, B, V, 1, pad=False)
+    _, out, grad = run_grad(qs, z, dtype, t1, None, None, gl, None)
+    check_grad(z, dtype, t1, None, None, gl, None, out, grad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 2, 9, 300, 1024])
+def test_grad_many_tokens(qs, G, dtype):
+    print(f"grad G={G} {dtype}", flush=True)
+    rng = np.random.default_rng(G)
+    B, V = 4, 9007
+    z = make(G, B, V, "wide")
+    tokens = tokens_for(rng, B, V, G)
+    tokens[1] = V - 1
+    tokens[2] = np.arange(G) % 17
+    gl = rng.normal(0, 1, (B, G)).astype(np.float32)
+    gH = rng.normal(0, 1, B).astype(np.float32)
+    _, out, grad = run_grad(qs, z, dtype, tokens, None, None, gl, gH)
+    check_grad(z, dtype, tokens, None, None, gl, gH, out, grad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_grad_in_place_and_padding(qs, dtype):
+    """In the logits' own buffer, and into a buffer whose padding stays."""
+    import torch
+    print(f"grad in place {dtype}", flush=True)
+    rng = np.random.default_rng(3)
+    B, V = 7, 5003
+    z = make(3, B, V, "normal")
+    tokens = tokens_for(rng, B, V, 2)
+    gl = rng.normal(0, 1, (B, 2)).astype(np.float32)
+    _, out, want = run_grad(qs, z, dtype, tokens, None, None, gl, None)
+    lg, tok, d, _ = run(qs, z, dtype, tokens)
+    got = qs.token_logprobs_backward(lg, tok, out["row_max"], out["log_sum"], out["status"],
+                                     torch.from_numpy(gl).cuda(), out=lg)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == lg.data_ptr() and torch.equal(got, want)
+    buf = torch.full((B, V + 61), 7.0, dtype=want.dtype, device="cuda")
+    lg = on_gpu(z, dtype)
+    qs.token_logprobs_backward(lg, tok, out["row_max"], out["log_sum"], out["status"],
+                               torch.from_numpy(gl).cuda(), out=buf[:, :V])
+    torch.cuda.synchronize()
+    assert torch.equal(buf[:, :V], want) and (buf[:, V:] == 7.0).all()
+
+
+def test_gradient_against_differences(qs):
+    """Central differences of the forward kernel's own outputs. With step h the
+    difference carries 2 t / (2 h) of the forward's error t and h^2 / 6 of the
+    third derivative (at most 1 in size for log-probabilities, and below 4 for
+    the entropy of 12 tokens, where |ln p| < 8)."""
+    import torch
+    rng = np.random.default_rng(11)
+    V, h = 12, 2.0 ** -5
+    z = rng.normal(0, 1, V).astype(np.float32)
+    z = np.round(z * 256) / 256            # z + h is exact
+    T = np.float32(1.25)
+    tokens = np.array([3, 7, 3], np.int32)
+    gl = np.array([0.7, -1.1, 0.4], np.float32)
+    gH = np.float32(0.6)
+    rows = np.stack([z] + [z + s * h * np.eye(V, dtype=np.float32)[i]
+                           for i in range(V) for s in (1, -1)]).astype(np.float32)
+    n = rows.shape[0]
+    _, _, _, out = run(qs, rows, "f32", np.tile(tokens, (n, 1)), np.full(n, T, np.float32))
+    f = (out["logprobs"].double() * torch.from_numpy(gl).cuda().double()).sum(1) \
+        + float(gH) * out["entropy"].double()
+    f = f.cpu().numpy()
+    want = (f[1::2] - f[2::2]) / (2 * h)
+    _, out, grad = run_grad(qs, z[None], "f32", tokens[None], np.array([T]), None, gl[None],
+                            np.array([gH]))
+    weight = np.abs(gl).sum() + abs(gH)
+    tol = weight * (U * 160 * 2 / (2 * h) + 4 * h * h / 6 / float(T) ** 3)
+    assert (np.abs(grad[0].cpu().numpy() - want) <= tol).all(), (grad[0].cpu().numpy(), want, tol)
+
+
+def test_autograd(qs):
+    """backward() through the binding: the same gradients, leaves of padded rows,
+    outputs without a gradient, one loss of both outputs and of each alone."""
+    import torch
+    rng = np.random.default_rng(5)
+    B, V = 6, 1001
+    z = make(5, B, V, "normal")
+    tokens = tokens_for(rng, B, V, 2)
+    T = rng.uniform(0.5, 1.5, B).astype(np.float32)
+    gl = rng.normal(0, 1, (B, 2)).astype(np.float32)
+    gH = rng.normal(0, 1, B).astype(np.float32)
+    tok, Tt = torch.from_numpy(tokens).cuda(), torch.from_numpy(T).cuda()
+    g_l, g_H = torch.from_numpy(gl).cuda(), torch.from_numpy(gH).cuda()
+    for dtype in ("f32", "bf16"):
+        for use in ("both", "logprobs", "entropy"):
+            lg = on_gpu(z, dtype).detach().requires_grad_()
+            out = qs.token_logprobs(lg, tok, temperature=Tt, entropy=True, top_n=3)
+            assert not out["top_logprobs"].requires_grad and not out["row_max"].requires_grad
+            loss = 0
+            if use != "entropy":
+                loss = loss + (out["logprobs"] * g_l).sum()
+            if use != "logprobs":
+                loss = loss + (out["entropy"] * g_H).sum()
+            (grad,) = torch.autograd.grad(loss, lg)
+            torch.cuda.synchronize()
+            check_grad(z, dtype, tokens, T, None, gl if use != "entropy" else 0 * gl,
+                       gH if use != "logprobs" else None, {k: v.detach() for k, v in out.items()},
+                       grad)
+
+
+def test_refusals(qs):
+    import torch
+    lg = torch.zeros(4, 64, device="cuda")
+    tok = torch.zeros(4, dtype=torch.int32, device="cuda")
+    stats = dict(row_max=torch.zeros(4, device="cuda"), log_sum=torch.zeros(4, device="cuda"),
+                 status=tok)
+    g = torch.zeros(4, device="cuda")
+    for kw in (dict(tokens=tok.long()), dict(tokens=tok[:3]), dict(tokens=tok.cpu()),
+               dict(tokens=torch.zeros(4, 2, 2, dtype=torch.int32, device="cuda")),
+               dict(temperature=torch.ones(3, device="cuda")),
+               dict(temperature=torch.ones(4)), dict(logits=lg.half()), dict(logits=lg.cpu()),
+               dict(logits=lg.t()), dict(bitmask=torch.zeros(4, 2, device="cuda"))):
+        a = dict(logits=lg, tokens=tok) | kw
+        with pytest.raises((ValueError, TypeError)):
+            qs.token_logprobs(a.pop("logits"), a.pop("tokens"), **a)
+    for kw in (dict(top_n=65), dict(top_n=-1), dict(bitmask=torch.zeros(4, 1, dtype=torch.int32,
+                                                                        device="cuda"))):
+        with pytest.raises(RuntimeError):
+            qs.token_logprobs(lg, tok, **kw)
+    with pytest.raises(RuntimeError):      # rows that do not start 16-byte aligned
+        qs.token_logprobs(torch.zeros(4, 63, device="cuda"), tok)
+    with pytest.raises(RuntimeError):      # no token to score
+        qs.token_logprobs(lg, torch.zeros(4, 0, dtype=torch.int32, device="cuda"))
+    for kw in (dict(grad_logprobs=g[:3]), dict(grad_logprobs=g.double()), dict(entropy=g),
+               dict(grad_entropy=g), dict(out=lg.bfloat16()), dict(out=lg[:, :32]),
+               dict(out=torch.zeros(4, 64))):
+        a = dict(grad_logprobs=g) | kw
+        with pytest.raises(ValueError):
+            qs.token_logprobs_backward(lg, tok, stats["row_max"], stats["log_sum"],
+                                       stats["status"], a.pop("grad_logprobs"), **a)
+    out = qs.token_logprobs(lg[:0], tok[:0], entropy=True, top_n=2)
+    assert out["logprobs"].shape == (0,) and out["top_ids"].shape == (0, 2)

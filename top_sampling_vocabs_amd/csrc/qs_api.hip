@@ -13,8 +13,10 @@
 
 #include "qs_aux.hpp"
 #include "qs_chunk.hpp"
+#include "qs_head.hpp"
 #include "qs_launch.hpp"
 #include "qs_proc.hpp"
+#include "qs_score.hpp"
 #include "qs_topn.hpp"
 
 namespace {
@@ -470,6 +472,143 @@ int qs_top_logprobs(int64_t B, const int32_t* cand_ids, const float* cand_probs,
   a.out_lp = top_logprobs;
   a.status = row_status;
   hipError_t e = qs::launch_top(a, (int)B, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QS_OK : QS_ERR_HIP;
+}
+
+size_t qs_token_logprobs_workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n) {
+  if (B < 1 || B > kMaxB || V < 1 || V > kMaxV || (dtype != QS_F32 && dtype != QS_BF16) ||
+      top_n < 0 || top_n > qs::score::kTopMax)
+    return 0;
+  return qs::score::workspace_bytes(B, V, dtype, top_n);
+}
+
+int qs_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                      const float* temperature, const uint32_t* bitmask, int64_t bitmask_stride,
+                      const int32_t* tokens, int64_t G, float* logprobs, float* row_max,
+                      float* log_sum, float* entropy, int64_t top_n, int32_t* top_ids,
+                      float* top_logprobs, int32_t* row_status, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = check_input(logits, dtype, B, V, row_stride, bitmask, bitmask_stride);
+  if (rc != QS_OK) return rc;
+  if (B == 0) return QS_OK;
+  if (G < 1 || G > qs::score::kTokensMax || top_n < 0 || top_n > qs::score::kTopMax)
+    return QS_ERR_INVALID_ARG;
+  const void* req4[] = {tokens, logprobs, row_max, log_sum, row_status};
+  for (const void* p : req4)
+    if (!p || !aligned(p, 4)) return QS_ERR_INVALID_ARG;
+  if (!aligned(temperature, 4) || !aligned(entropy, 4)) return QS_ERR_INVALID_ARG;
+  if (top_n > 0 && (!top_ids || !top_logprobs || !aligned(top_ids, 4) || !aligned(top_logprobs, 4)))
+    return QS_ERR_INVALID_ARG;
+  const size_t need = qs::score::workspace_bytes(B, V, dtype, top_n);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+    return QS_ERR_WORKSPACE;
+  qs::score::Args a;
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.row_bytes = row_stride * (dtype == QS_F32 ? 4 : 2);
+  a.V = (int)V;
+  a.T = temperature;
+  a.bitmask = bitmask;
+  a.bm_stride = bitmask_stride;
+  a.tokens = tokens;
+  a.G = (int)G;
+  a.logprobs = logprobs;
+  a.row_max = row_max;
+  a.log_sum = log_sum;
+  a.entropy = entropy;
+  a.top_n = (int)top_n;
+  a.top_ids = top_ids;
+  a.top_lp = top_logprobs;
+  a.status = row_status;
+  hipError_t e =
+      qs::score::launch_score(a, dtype, (int)B, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QS_OK : QS_ERR_HIP;
+}
+
+int qs_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_t V,
+                               int64_t row_stride, const float* temperature,
+                               const uint32_t* bitmask, int64_t bitmask_stride,
+                               const int32_t* tokens, int64_t G, const float* row_max,
+                               const float* log_sum, const int32_t* row_status,
+                               const float* grad_logprobs, const float* entropy,
+                               const float* grad_entropy, void* grad_logits, int64_t grad_stride,
+                               void* stream) {
+  int rc = check_input(logits, dtype, B, V, row_stride, bitmask, bitmask_stride);
+  if (rc != QS_OK) return rc;
+  if (B == 0) return QS_OK;
+  if (G < 1 || G > qs::score::kTokensMax) return QS_ERR_INVALID_ARG;
+  const void* req4[] = {tokens, row_max, log_sum, row_status, grad_logprobs};
+  for (const void* p : req4)
+    if (!p || !aligned(p, 4)) return QS_ERR_INVALID_ARG;
+  if (!aligned(temperature, 4) || !aligned(entropy, 4) || !aligned(grad_entropy, 4) ||
+      (entropy == nullptr) != (grad_entropy == nullptr))
+    return QS_ERR_INVALID_ARG;
+  const int64_t es = dtype == QS_F32 ? 4 : 2;
+  if (!grad_logits || !aligned(grad_logits, 16) || grad_stride < V || (grad_stride * es) % 16 != 0)
+    return QS_ERR_INVALID_ARG;
+  // in place only row for row: otherwise one row's writes meet another's reads
+  if (grad_logits == logits && grad_stride != row_stride) return QS_ERR_INVALID_ARG;
+  qs::score::GradArgs a;
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.row_bytes = row_stride * es;
+  a.V = (int)V;
+  a.T = temperature;
+  a.bitmask = bitmask;
+  a.bm_stride = bitmask_stride;
+  a.tokens = tokens;
+  a.G = (int)G;
+  a.row_max = row_max;
+  a.log_sum = log_sum;
+  a.status = row_status;
+  a.g_lp = grad_logprobs;
+  a.entropy = entropy;
+  a.g_ent = grad_entropy;
+  a.grad = static_cast<uint8_t*>(grad_logits);
+  a.grad_bytes = grad_stride * es;
+  hipError_t e = qs::score::launch_grad(a, dtype, (int)B, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QS_OK : QS_ERR_HIP;
+}
+
+int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidden_stride,
+                   const uint8_t* codes, int64_t V, int64_t codes_stride, const void* scales,
+                   int scale_dtype, int64_t scale_stride, const uint8_t* zeros,
+                   int64_t zero_stride, int64_t group, void* logits, int logits_dtype,
+                   int64_t row_stride, void* stream) {
+  if (B < 0 || B > kMaxB || V < 1 || V > qs::head::kMaxV || K < 1 || K > qs::head::kMaxK)
+    return QS_ERR_INVALID_ARG;
+  if ((group != 32 && group != 64 && group != 128) || K % group != 0) return QS_ERR_INVALID_ARG;
+  if ((scale_dtype != QS_F32 && scale_dtype != QS_BF16) ||
+      (logits_dtype != QS_F32 && logits_dtype != QS_BF16))
+    return QS_ERR_INVALID_ARG;
+  if (B == 0) return QS_OK;
+  const int64_t groups = K / group;
+  if (!hidden || !aligned(hidden, 16) || hidden_stride < K || hidden_stride % 8 != 0)
+    return QS_ERR_INVALID_ARG;
+  if (!codes || !aligned(codes, 16) || codes_stride < K / 2 || codes_stride % 16 != 0)
+    return QS_ERR_INVALID_ARG;
+  if (!scales || !aligned(scales, scale_dtype == QS_F32 ? 4 : 2) || scale_stride < groups)
+    return QS_ERR_INVALID_ARG;
+  if (zeros && zero_stride < groups) return QS_ERR_INVALID_ARG;
+  const int64_t es = logits_dtype == QS_F32 ? 4 : 2;
+  if (!logits || !aligned(logits, 16) || row_stride < V || (row_stride * es) % 16 != 0)
+    return QS_ERR_INVALID_ARG;
+  qs::head::Args a;
+  a.hidden = static_cast<const uint16_t*>(hidden);
+  a.hidden_stride = hidden_stride;
+  a.B = (int)B;
+  a.V = (int)V;
+  a.K = (int)K;
+  a.group = (int)group;
+  a.codes = codes;
+  a.codes_stride = codes_stride;
+  a.scales = scales;
+  a.scale_dtype = scale_dtype;
+  a.scale_stride = scale_stride;
+  a.zeros = zeros;
+  a.zero_stride = zero_stride;
+  a.logits = logits;
+  a.logits_dtype = logits_dtype;
+  a.row_stride = row_stride;
+  hipError_t e = qs::head::launch_head(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QS_OK : QS_ERR_HIP;
 }
 

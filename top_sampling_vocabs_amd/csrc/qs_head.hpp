@@ -1,0 +1,35 @@
+// Argument block and launcher of the output head with 4-bit weights.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qs {
+namespace head {
+
+constexpr int64_t kMaxV = (int64_t)1 << 24;
+constexpr int64_t kMaxK = 65536;
+
+struct Args {
+  const uint16_t* hidden;    // [B][hidden_stride] bf16
+  int64_t hidden_stride;
+  int B;
+  int V;
+  int K;
+  int group;                 // 32, 64 or 128; K is a multiple of it
+  const uint8_t* codes;      // [V][codes_stride] bytes, two codes each
+  int64_t codes_stride;
+  const void* scales;        // [V][scale_stride] bf16 or fp32
+  int scale_dtype;
+  int64_t scale_stride;
+  const uint8_t* zeros;      // [V][zero_stride], optional (NULL: 8)
+  int64_t zero_stride;
+  void* logits;              // [B][row_stride]
+  int logits_dtype;
+  int64_t row_stride;
+};
+
+hipError_t launch_head(const Args& a, hipStream_t st);
+
+}  // namespace head
+}  // namespace qs
