@@ -499,6 +499,7 @@ int qs_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64
   if (!aligned(temperature, 4) || !aligned(entropy, 4)) return QS_ERR_INVALID_ARG;
   if (top_n > 0 && (!top_ids || !top_logprobs || !aligned(top_ids, 4) || !aligned(top_logprobs, 4)))
     return QS_ERR_INVALID_ARG;
+  if (!qs::score::grid_fits(B, V, dtype)) return QS_ERR_INVALID_ARG;
   const size_t need = qs::score::workspace_bytes(B, V, dtype, top_n);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return QS_ERR_WORKSPACE;
@@ -545,6 +546,7 @@ int qs_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_t
   const int64_t es = dtype == QS_F32 ? 4 : 2;
   if (!grad_logits || !aligned(grad_logits, 16) || grad_stride < V || (grad_stride * es) % 16 != 0)
     return QS_ERR_INVALID_ARG;
+  if (!qs::score::grad_grid_fits(B, V, dtype)) return QS_ERR_INVALID_ARG;
   // in place only row for row: otherwise one row's writes meet another's reads
   if (grad_logits == logits && grad_stride != row_stride) return QS_ERR_INVALID_ARG;
   qs::score::GradArgs a;

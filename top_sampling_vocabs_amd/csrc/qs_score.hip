@@ -7,8 +7,28 @@
 // Both terms of H are non-negative, so nothing cancels. The top tokens are
 // those of the largest z, ties by id.
 //
-// One workgroup per row: one pass for the maximum and the row's checks, one
-// for the two sums, and one per top token (the largest key below the last).
+// The logits are read once. A workgroup holds its share of a row in registers
+// (NL 16-byte loads per lane, all requested before the first is used), so the
+// maximum comes first and every exponential is taken once against it: no
+// rescaling. Each wave uses its own maximum and the waves' (m, S, E) triples
+// are joined as
+//   S = sum_w S_w f_w,  E = sum_w f_w (E_w + S_w (m_w - m) / T),
+//   f_w = exp((m_w - m) / T).
+// Weights and E are kept in units of log 2 (one hardware exponential each).
+//
+// Rows of up to kRowBlock * 8 loads go to one workgroup and one launch: a second
+// launch costs more than one compute unit needs for such a row. Longer rows
+// are split into parts of kPartBlock * 16 loads, several of which fit a
+// compute unit at once, so that one part's loads run under another's
+// exponentials; a second launch joins the parts of each row.
+//
+// Top tokens: with t the n-th largest of the maxima of 256 groups of lanes, n
+// tokens (one of each of n groups) reach t, so the n largest tokens lie among
+// those with z >= t. These are few (a little over n unless values repeat);
+// they are collected and ranked. Keys
+// (z's order-preserving bits << 32 | ~id) are distinct. Where more than the
+// list holds reach t (long runs of equal values) the workgroup takes its n
+// largest keys one after another instead.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -21,148 +41,542 @@ namespace qs {
 namespace score {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kBlockWaves = kBlock / 64;
+constexpr int kPartBlock = 256;   // threads of a part's workgroup
+constexpr int kPartLoads = 16;    // 16-byte loads per lane
+constexpr int kRowBlock = 1024;   // threads of a whole row's workgroup
+constexpr int kRowLoads = 8;
+constexpr int kSmallBlock = 256;  // threads of a short row's workgroup
+constexpr int kSmallLoads = 4;
+constexpr int kListCap = 256;     // collected keys per workgroup
+constexpr int kJoinCap = 1024;    // keys of all parts that reach the row's t
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What a part's workgroup leaves for the join.
+struct Part {
+  float m;        // largest legal logit (-FLT_MAX if none is finite)
+  float S;        // sum of 2^((z - m) c), c = log2(e) / T; NaN if a legal z is NaN or +inf
+  float E;        // sum of 2^((z - m) c) (z - m) c
+  uint32_t any;   // a legal token exists
+  uint32_t t;     // threshold: order-preserving key of a lower bound of the n-th largest z
+  int32_t count;  // keys in the part's list
+  uint32_t pad[2];
+};
+static_assert(sizeof(Part) == 32, "two 16-byte stores");
+
+template <int DT> constexpr int kPer = DT == QS_F32 ? 4 : 8;  // tokens per 16-byte load
+
+int64_t parts_for(int64_t V, int dtype) {
+  const int64_t per = dtype == QS_F32 ? 4 : 8;
+  if (V <= per * kRowBlock * kRowLoads) return 1;
+  return (V + per * kPartBlock * kPartLoads - 1) / (per * kPartBlock * kPartLoads);
+}
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// log2(e) / T held to finite, non-zero values: 0 times it is 0, and -inf
+// times it is -inf.
+__device__ __forceinline__ float scale_of(float T) {
+  return fminf(fmaxf(kLog2e / T, 1.17549435e-38f), 3.4e38f);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float readlane_f32(float v, int l) {
+  return __uint_as_float(readlane_u32(__float_as_uint(v), l));
+}
+__device__ __forceinline__ float wave_max_f32(float v) {
+  v = fmaxf(v, dpp_f32<kDppXor1>(v));
+  v = fmaxf(v, dpp_f32<kDppXor2>(v));
+  v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+  v = fmaxf(v, dpp_f32<kDppMirror>(v));
+  return fmaxf(fmaxf(readlane_f32(v, 0), readlane_f32(v, 16)),
+               fmaxf(readlane_f32(v, 32), readlane_f32(v, 48)));
+}
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += dpp_f32<kDppXor1>(v);
+  v += dpp_f32<kDppXor2>(v);
+  v += dpp_f32<kDppHalfMirror>(v);
+  v += dpp_f32<kDppMirror>(v);
+  return (readlane_f32(v, 0) + readlane_f32(v, 16)) + (readlane_f32(v, 32) + readlane_f32(v, 48));
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// f_w of the join; exponents below -200 weigh nothing against the maximum's 1.
+__device__ __forceinline__ float rel(float m, float top, float c) {
+  return fmaxf((m - top) * c, -200.0f);
+}
+
+// Token e (0 .. kPer - 1) of a 16-byte load, as float.
+template <int DT>
+__device__ __forceinline__ float token(const uint4& v, int e) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (DT == QS_F32) return __uint_as_float(w[e]);
+  return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+}
+
+// The same for an index known only at run time.
+template <int DT>
+__device__ __forceinline__ float token_at(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3,
+                                          int e) {
+  const int d = DT == QS_F32 ? e : e >> 1;
+  const uint32_t lo = d & 1 ? w1 : w0, hi = d & 1 ? w3 : w2;
+  const uint32_t w = d & 2 ? hi : lo;
+  if constexpr (DT == QS_F32) return __uint_as_float(w);
+  return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+}
 
 template <int DT>
-__device__ __forceinline__ float load_logit(const uint8_t* row, int i) {
+__device__ __forceinline__ float logit_at(const uint8_t* row, int i) {
   if constexpr (DT == QS_F32) return reinterpret_cast<const float*>(row)[i];
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
 }
 
-__device__ __forceinline__ bool is_legal(const uint32_t* bm, int i) {
-  return bm == nullptr || ((bm[i >> 5] >> (i & 31)) & 1u);
+// Tokens whose bit in `bits` is 0 become -inf.
+template <int DT>
+__device__ __forceinline__ uint4 blank(uint4 v, uint32_t bits) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (DT == QS_F32) {
+      const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)bits, d, 1);
+      w[d] = bfi(keep, w[d], 0xFF800000u);
+    } else {
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe((int)bits, 2 * d, 1);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_sbfe((int)bits, 2 * d + 1, 1);
+      w[d] = bfi(bfi(0xFFFFu, lo, hi), w[d], 0xFF80FF80u);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Keeps the compiler from holding a load's unpacked tokens from one pass over
+// the registers to the next (unpacking again costs less than the registers).
+__device__ __forceinline__ void opaque(uint4& v) {
+  asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+}
+
+// The order-preserving key of a logit and back (fp32 keys for both dtypes).
+__device__ __forceinline__ uint32_t key_of(float z) { return Keys<QS_F32>::of(__float_as_uint(z)); }
+
+// The n-th largest (n <= 64) of the wave's 4 * 64 keys, low 16 bits cleared.
+__device__ __forceinline__ uint32_t wave_nth_high16(const uint4& key, int n) {
+  uint32_t t = 0u;
+#pragma unroll
+  for (int b = 31; b >= 16; --b) {
+    const uint32_t c = t | (1u << b);
+    const int reach = __popcll(ballot(key.x >= c)) + __popcll(ballot(key.y >= c)) +
+                      __popcll(ballot(key.z >= c)) + __popcll(ballot(key.w >= c));
+    if (reach >= n) t = c;
+  }
+  return t;
+}
+
+constexpr int kGroups = 256;
+
+struct Shared {
+  uint64_t list[kListCap];
+  uint4 group[kGroups / 4];  // keys of the groups' maxima
+  float m[kRowBlock / 64], S[kRowBlock / 64], E[kRowBlock / 64];
+  uint32_t any[kRowBlock / 64];
+  uint64_t best[kRowBlock / 64];
+  int count;
+};
+
+// Writes one row's outputs; called by every thread of a workgroup of `threads`,
+// with the row's joined statistics and (top_n > 0) `n_list` distinct keys in
+// LDS that hold its top tokens.
 template <int DT>
-__global__ void __launch_bounds__(kBlock) score_kernel(Args a) {
-  __shared__ uint64_t s_u64[kBlockWaves];
-  __shared__ float s_f[2 * kBlockWaves];
-  __shared__ uint32_t s_flags;
-  const int r = blockIdx.x;
-  const int tid = threadIdx.x;
-  const int w = tid >> 6;
+__device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int threads, float m,
+                                           float S, float E, bool any, float T,
+                                           const uint64_t* list, int n_list) {
   const uint8_t* row = a.logits + (size_t)r * a.row_bytes;
   const uint32_t* bm = a.bitmask ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
   const int32_t* tokens = a.tokens + (size_t)r * a.G;
-  const float T = a.T ? a.T[r] : 1.0f;
-  if (tid == 0) s_flags = 0u;
-  __syncthreads();
-  // bit 0: a legal token, bit 1: NaN or +inf at one, bit 2: a bad token id
-  uint32_t flags = 0u;
-  float m = -INFINITY;
-  for (int i = tid; i < a.V; i += kBlock) {
-    if (!is_legal(bm, i)) continue;
-    const float z = load_logit<DT>(row, i);
-    flags |= (z != z || z == INFINITY) ? 3u : 1u;
-    m = fmaxf(m, z);
-  }
-  for (int g = tid; g < a.G; g += kBlock)
-    if (tokens[g] < -1 || tokens[g] >= a.V) flags |= 4u;
-  if (flags) atomicOr(&s_flags, flags);
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  if (lane_id() == 0) s_f[w] = m;
-  __syncthreads();
-  flags = s_flags;
-  m = s_f[0];
-  for (int k = 1; k < kBlockWaves; ++k) m = fmaxf(m, s_f[k]);
-  __syncthreads();
+  float* const lps = a.logprobs + (size_t)r * a.G;
+  int bad = 0;
+  for (int g = tid; g < a.G; g += threads) bad |= tokens[g] < -1 || tokens[g] >= a.V;
+  if (threads > 64) bad = __syncthreads_or(bad);
+  else bad = ballot(bad) != 0;
   int status = QS_ROW_OK;
-  if (!(T > 0.0f) || T == INFINITY || (flags & 4u)) status = QS_ROW_BAD_PARAM;
-  else if (!(flags & 1u)) status = QS_ROW_EMPTY;
-  else if (flags & 2u) status = QS_ROW_NONFINITE;
-  else if (m == -INFINITY) status = QS_ROW_ALL_NEG_INF;
-  if (tid == 0) a.status[r] = status;
-  if (status != QS_ROW_OK) {
-    for (int g = tid; g < a.G; g += kBlock)
-      a.logprobs[(size_t)r * a.G + g] = tokens[g] == -1 ? 0.0f : NAN;
-    for (int j = tid; j < a.top_n; j += kBlock) {
-      a.top_ids[(size_t)r * a.top_n + j] = -1;
-      a.top_lp[(size_t)r * a.top_n + j] = -INFINITY;
+  if (bad || !(T > 0.0f) || T == INFINITY) status = QS_ROW_BAD_PARAM;
+  else if (!any) status = QS_ROW_EMPTY;
+  else if (S != S) status = QS_ROW_NONFINITE;
+  else if (S == 0.0f) status = QS_ROW_ALL_NEG_INF;
+  const bool ok = status == QS_ROW_OK;
+  const float log_sum = ok ? logf(S) : NAN;
+  if (tid == 0) {
+    a.status[r] = status;
+    a.row_max[r] = ok ? m : NAN;
+    a.log_sum[r] = log_sum;
+    if (a.entropy) a.entropy[r] = ok ? log_sum - kLn2 * (E / S) : NAN;
+  }
+  for (int g = tid; g < a.G; g += threads) {
+    const int t = tokens[g];
+    float lp = ok ? -INFINITY : NAN;
+    if (t == -1) lp = 0.0f;
+    else if (ok && (bm == nullptr || ((bm[t >> 5] >> (t & 31)) & 1u))) {
+      lp = (logit_at<DT>(row, t) - m) / T - log_sum;
     }
-    if (tid == 0) {
-      a.row_max[r] = NAN;
-      a.log_sum[r] = NAN;
-      if (a.entropy) a.entropy[r] = NAN;
+    lps[g] = lp;
+  }
+  if (a.top_n == 0) return;
+  int32_t* const ids = a.top_ids + (size_t)r * a.top_n;
+  float* const tlp = a.top_lp + (size_t)r * a.top_n;
+  if (!ok) n_list = 0;
+  for (int i = tid; i < n_list; i += threads) {
+    const uint64_t key = list[i];
+    int rank = 0;
+    for (int j = 0; j < n_list; ++j) rank += list[j] > key;
+    if (rank < a.top_n) {
+      ids[rank] = (int32_t)~(uint32_t)key;
+      tlp[rank] = (Keys<QS_F32>::value((uint32_t)(key >> 32)) - m) / T - log_sum;
     }
-    return;
   }
-  float S = 0.0f, E = 0.0f;
-  for (int i = tid; i < a.V; i += kBlock) {
-    if (!is_legal(bm, i)) continue;
-    const float d = (load_logit<DT>(row, i) - m) / T;
-    const float e = __expf(d);
-    S += e;
-    if (e > 0.0f) E += e * d;
+  for (int j = n_list + tid; j < a.top_n; j += threads) {
+    ids[j] = -1;
+    tlp[j] = -INFINITY;
   }
-  for (int off = 32; off > 0; off >>= 1) {
-    S += __shfl_xor(S, off, 64);
-    E += __shfl_xor(E, off, 64);
+}
+
+// One workgroup per row (ROW: parts == 1, outputs written here) or per part.
+template <int DT, int THREADS, int NL, bool MASK, bool TOP, bool ROW>
+__global__ void __launch_bounds__(THREADS)
+    score_kernel(Args a, int parts, int part_loads, Part* ws_parts, uint64_t* ws_list) {
+  constexpr int kWavesHere = THREADS / 64;
+  constexpr int P = kPer<DT>;
+  __shared__ Shared s;
+  const int tid = threadIdx.x;
+  const int lane = lane_id();
+  const int w = tid >> 6;
+  const int r = ROW ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)parts);
+  const int part = ROW ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)parts);
+  const int begin = part * part_loads * THREADS * P;  // first token of this workgroup
+  const uint8_t* row = a.logits + (size_t)r * a.row_bytes;
+  const float T = a.T ? a.T[r] : 1.0f;
+  const float c = scale_of(T);
+
+  // requests: 16 bytes per lane and load; loads that begin past the row's end
+  // are left out (a 16-byte chunk that begins inside the row ends inside its
+  // stride)
+  uint4 v[NL];
+  uint32_t legal[NL];
+#pragma unroll
+  for (int u = 0; u < NL; ++u) {
+    const int i = begin + (u * THREADS + tid) * P;
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    legal[u] = 0u;
+    if (u < part_loads && i < a.V) {
+      v[u] = *reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P));
+      legal[u] = 0xFFu;
+      if constexpr (MASK)
+        legal[u] = reinterpret_cast<const uint8_t*>(a.bitmask + (size_t)r * a.bm_stride)[i >> 3];
+    }
   }
-  if (lane_id() == 0) {
-    s_f[2 * w] = S;
-    s_f[2 * w + 1] = E;
+  if (TOP && tid == 0) s.count = 0;
+
+  // largest legal token of the lane; illegal ones become -inf
+  float m = -3.402823466e38f;
+  uint32_t any = 0u;
+#pragma unroll
+  for (int u = 0; u < NL; ++u) {
+    const int i = begin + (u * THREADS + tid) * P;
+    uint32_t bits = legal[u];
+    if constexpr (P == 4) bits = MASK ? bits >> (i & 4) : bits;
+    const int left = a.V - i;
+    bits &= left >= P ? (1u << P) - 1u : left > 0 ? (1u << left) - 1u : 0u;
+    any |= bits;
+    v[u] = blank<DT>(v[u], bits);
+#pragma unroll
+    for (int e = 0; e < P; ++e) m = fmaxf(m, token<DT>(v[u], e));
+  }
+  const float lane_max = m;
+  const float wave_max = wave_max_f32(m);
+  if constexpr (TOP) {
+    static_assert(THREADS == kGroups || THREADS == 4 * kGroups, "groups of 1 or 4 lanes");
+    uint32_t* const group = reinterpret_cast<uint32_t*>(s.group);
+    if constexpr (THREADS == kGroups) {
+      group[tid] = key_of(lane_max);
+    } else {
+      float g = fmaxf(lane_max, dpp_f32<kDppXor1>(lane_max));
+      g = fmaxf(g, dpp_f32<kDppXor2>(g));
+      if ((lane & 3) == 0) group[tid >> 2] = key_of(g);
+    }
+  }
+
+  // the wave's sums against its own maximum
+  float S[2] = {0.0f, 0.0f}, E[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < NL; ++u) {
+    opaque(v[u]);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float d = (token<DT>(v[u], e) - wave_max) * c;
+      const float x = exp2_hw(d);
+      S[e & 1] += x;
+      E[e & 1] += x * fmaxf(d, -200.0f);  // not 0 times -inf
+    }
+  }
+  const float Sw = wave_sum_f32(S[0] + S[1]);
+  const float Ew = wave_sum_f32(E[0] + E[1]);
+  const bool anyw = ballot(any != 0u) != 0;
+  if (lane == 0) {
+    s.m[w] = wave_max;
+    s.S[w] = Sw;
+    s.E[w] = Ew;
+    s.any[w] = anyw;
   }
   __syncthreads();
-  S = E = 0.0f;
-  for (int k = 0; k < kBlockWaves; ++k) {
-    S += s_f[2 * k];
-    E += s_f[2 * k + 1];
+  float top = s.m[0];
+  bool any_all = s.any[0] != 0u;
+#pragma unroll
+  for (int k = 1; k < kWavesHere; ++k) {
+    top = fmaxf(top, s.m[k]);
+    any_all |= s.any[k] != 0u;
   }
-  const float log_sum = logf(S);
-  if (tid == 0) {
-    a.row_max[r] = m;
-    a.log_sum[r] = log_sum;
-    if (a.entropy) a.entropy[r] = log_sum - E / S;
+  float S_all = 0.0f, E_all = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kWavesHere; ++k) {
+    const float d = rel(s.m[k], top, c);
+    const float f = exp2_hw(d);
+    S_all += f * s.S[k];
+    E_all += f * (s.E[k] + d * s.S[k]);
   }
-  for (int g = tid; g < a.G; g += kBlock) {
-    const int t = tokens[g];
-    float lp = 0.0f;
-    if (t >= 0) lp = is_legal(bm, t) ? (load_logit<DT>(row, t) - m) / T - log_sum : -INFINITY;
-    a.logprobs[(size_t)r * a.G + g] = lp;
-  }
-  uint64_t prev = ~0ull;
-  for (int j = 0; j < a.top_n; ++j) {
-    uint64_t best = 0u;
-    for (int i = tid; i < a.V; i += kBlock) {
-      const float z = load_logit<DT>(row, i);
-      if (!is_legal(bm, i) || z == -INFINITY) continue;
-      const uint64_t key =
-          ((uint64_t)Keys<QS_F32>::of(__float_as_uint(z)) << 32) | (uint32_t)~i;
-      if (key < prev && key > best) best = key;
+
+  int n_list = 0;
+  uint32_t t = 0u;
+  if constexpr (TOP) {
+    // finite tokens only: keys above -inf's (groups without one hold the key of
+    // -FLT_MAX, the lowest of those)
+    t = max(wave_nth_high16(s.group[lane], a.top_n), Keys<QS_F32>::kNegInf + 1u);
+    if (key_of(lane_max) >= t) {
+      const float tz = Keys<QS_F32>::value(t);
+      static_for<0, NL>([&](auto U) {
+        constexpr int u = decltype(U)::value;
+        opaque(v[u]);
+        float z = token<DT>(v[u], 0);
+#pragma unroll
+        for (int e = 1; e < P; ++e) z = fmaxf(z, token<DT>(v[u], e));
+        if (z >= tz) {
+#pragma unroll 1
+          for (int e = 0; e < P; ++e) {
+            z = token_at<DT>(v[u].x, v[u].y, v[u].z, v[u].w, e);
+            if (z >= tz) {
+              const int at = atomicAdd(&s.count, 1);
+              const int i = begin + (u * THREADS + tid) * P + e;
+              if (at < kListCap) s.list[at] = ((uint64_t)key_of(z) << 32) | (uint32_t)~i;
+            }
+          }
+        }
+      });
     }
-    for (int off = 32; off > 0; off >>= 1) {
-      const uint64_t o = (uint64_t)__shfl_xor((long long)best, off, 64);
-      best = o > best ? o : best;
+    __syncthreads();
+    n_list = s.count;
+    if (n_list > kListCap) {
+      // too many at or above t: the n largest keys, each below the one before
+      uint64_t prev = ~0ull;
+      n_list = 0;
+      for (int j = 0; j < a.top_n; ++j) {
+        uint64_t best = 0u;
+        const int end = min(a.V, begin + part_loads * THREADS * P);
+        const uint32_t* bm = MASK ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
+        for (int i = begin + tid; i < end; i += THREADS) {
+          const float z = logit_at<DT>(row, i);
+          if ((MASK && !((bm[i >> 5] >> (i & 31)) & 1u)) || z == -INFINITY) continue;
+          const uint64_t key = ((uint64_t)key_of(z) << 32) | (uint32_t)~i;
+          if (key < prev && key > best) best = key;
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+          const uint64_t o = (uint64_t)__shfl_xor((long long)best, off, 64);
+          best = o > best ? o : best;
+        }
+        if (lane == 0) s.best[w] = best;
+        __syncthreads();
+        for (int k = 0; k < kWavesHere; ++k) best = s.best[k] > best ? s.best[k] : best;
+        __syncthreads();
+        if (best == 0u) break;  // the same in every thread
+        if (tid == 0) s.list[j] = best;
+        prev = best;
+        n_list = j + 1;
+      }
+      __syncthreads();
     }
-    if (lane_id() == 0) s_u64[w] = best;
-    __syncthreads();
-    for (int k = 0; k < kBlockWaves; ++k) best = s_u64[k] > best ? s_u64[k] : best;
-    __syncthreads();
+  }
+  if constexpr (ROW) {
+    finish_row<DT>(a, r, tid, THREADS, top, S_all, E_all, any_all, T, s.list, n_list);
+  } else {
+    const size_t p = (size_t)r * parts + part;
     if (tid == 0) {
-      const float z = Keys<QS_F32>::value((uint32_t)(best >> 32));
-      a.top_ids[(size_t)r * a.top_n + j] = best ? (int32_t)~(uint32_t)best : -1;
-      a.top_lp[(size_t)r * a.top_n + j] = best ? (z - m) / T - log_sum : -INFINITY;
+      Part out;
+      out.m = top;
+      out.S = S_all;
+      out.E = E_all;
+      out.any = any_all;
+      out.t = t;
+      out.count = n_list;
+      out.pad[0] = out.pad[1] = 0u;
+      ws_parts[p] = out;
     }
-    if (best) prev = best;
-    else prev = 0u;  // no token left: the later slots stay empty
+    if constexpr (TOP)
+      for (int i = tid; i < n_list; i += THREADS) ws_list[p * kListCap + i] = s.list[i];
   }
+}
+
+// Joins the parts of each row: one workgroup per row (one wave without top
+// tokens).
+template <int DT, bool TOP>
+__global__ void __launch_bounds__(TOP ? 256 : 64)
+    join_kernel(Args a, int parts, const Part* ws_parts, const uint64_t* ws_list) {
+  constexpr int kThreadsHere = TOP ? 256 : 64;
+  __shared__ uint64_t s_list[TOP ? kJoinCap : 1];
+  __shared__ uint64_t s_best[4];
+  __shared__ int s_count;
+  const int r = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int lane = lane_id();
+  const Part* p = ws_parts + (size_t)r * parts;
+  const float T = a.T ? a.T[r] : 1.0f;
+  const float c = scale_of(T);
+  // every wave joins all parts (the same values in every thread)
+  float m = -3.402823466e38f;
+  uint32_t t = 0u, any = 0u;
+  for (int k = lane; k < parts; k += 64) {
+    m = fmaxf(m, p[k].m);
+    t = max(t, p[k].t);
+    any |= p[k].any;
+  }
+  m = wave_max_f32(m);
+  t = wave_reduce<OpMax>(t);
+  const bool any_all = ballot(any != 0u) != 0;
+  float S = 0.0f, E = 0.0f;
+  for (int k = lane; k < parts; k += 64) {
+    const float d = rel(p[k].m, m, c);
+    const float f = exp2_hw(d);
+    S += f * p[k].S;
+    E += f * (p[k].E + d * p[k].S);
+  }
+  S = wave_sum_f32(S);
+  E = wave_sum_f32(E);
+  int n_list = 0;
+  if constexpr (TOP) {
+    // the row's n-th largest token is at or above every part's t
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    const uint64_t* list = ws_list + (size_t)r * parts * kListCap;
+    for (int k = tid >> 6; k < parts; k += kThreadsHere / 64) {
+      const int n = p[k].count;
+      for (int i = lane; i < n; i += 64) {
+        const uint64_t key = list[(size_t)k * kListCap + i];
+        if ((uint32_t)(key >> 32) >= t) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kJoinCap) s_list[at] = key;
+        }
+      }
+    }
+    __syncthreads();
+    n_list = s_count;
+    if (n_list > kJoinCap) {
+      // more than the list holds: the n largest keys, one after another
+      uint64_t prev = ~0ull;
+      n_list = 0;
+      for (int j = 0; j < a.top_n; ++j) {
+        uint64_t best = 0u;
+        for (int k = tid >> 6; k < parts; k += kThreadsHere / 64) {
+          const int n = p[k].count;
+          for (int i = lane; i < n; i += 64) {
+            const uint64_t key = list[(size_t)k * kListCap + i];
+            if (key < prev && key > best) best = key;
+          }
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+          const uint64_t o = (uint64_t)__shfl_xor((long long)best, off, 64);
+          best = o > best ? o : best;
+        }
+        if (lane == 0) s_best[tid >> 6] = best;
+        __syncthreads();
+        for (int k = 0; k < kThreadsHere / 64; ++k) best = s_best[k] > best ? s_best[k] : best;
+        __syncthreads();
+        if (best == 0u) break;
+        if (tid == 0) s_list[j] = best;
+        prev = best;
+        n_list = j + 1;
+      }
+      __syncthreads();
+    }
+  }
+  finish_row<DT>(a, r, tid, kThreadsHere, m, S, E, any_all, T, s_list, n_list);
+}
+
+template <int DT, int THREADS, int NL, bool ROW>
+void launch(const Args& a, int blocks, int parts, int part_loads, Part* wp, uint64_t* wl,
+            hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(THREADS);
+  const bool mask = a.bitmask != nullptr, top = a.top_n > 0;
+  if (mask && top)
+    hipLaunchKernelGGL((score_kernel<DT, THREADS, NL, true, true, ROW>), grid, block, 0, st, a,
+                       parts, part_loads, wp, wl);
+  else if (mask)
+    hipLaunchKernelGGL((score_kernel<DT, THREADS, NL, true, false, ROW>), grid, block, 0, st, a,
+                       parts, part_loads, wp, wl);
+  else if (top)
+    hipLaunchKernelGGL((score_kernel<DT, THREADS, NL, false, true, ROW>), grid, block, 0, st, a,
+                       parts, part_loads, wp, wl);
+  else
+    hipLaunchKernelGGL((score_kernel<DT, THREADS, NL, false, false, ROW>), grid, block, 0, st, a,
+                       parts, part_loads, wp, wl);
+}
+
+template <int DT>
+hipError_t launch_dt(const Args& a, int B, int parts, uint8_t* ws, hipStream_t st) {
+  constexpr int P = kPer<DT>;
+  if (parts == 1) {
+    if (a.V <= kSmallBlock * kSmallLoads * P)
+      launch<DT, kSmallBlock, kSmallLoads, true>(
+          a, B, 1, (a.V + kSmallBlock * P - 1) / (kSmallBlock * P), nullptr, nullptr, st);
+    else
+      launch<DT, kRowBlock, kRowLoads, true>(
+          a, B, 1, (a.V + kRowBlock * P - 1) / (kRowBlock * P), nullptr, nullptr, st);
+    return hipGetLastError();
+  }
+  Part* const wp = reinterpret_cast<Part*>(ws);
+  uint64_t* const wl =
+      reinterpret_cast<uint64_t*>(ws + align256((size_t)B * parts * sizeof(Part)));
+  // parts of equal length, in whole loads
+  const int loads = (a.V + kPartBlock * P - 1) / (kPartBlock * P);
+  launch<DT, kPartBlock, kPartLoads, false>(a, B * parts, parts, (loads + parts - 1) / parts, wp,
+                                            wl, st);
+  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  if (a.top_n > 0)
+    hipLaunchKernelGGL((join_kernel<DT, true>), dim3((unsigned)B), dim3(256), 0, st, a, parts, wp,
+                       wl);
+  else
+    hipLaunchKernelGGL((join_kernel<DT, false>), dim3((unsigned)B), dim3(64), 0, st, a, parts, wp,
+                       wl);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 size_t workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n) {
-  (void)B; (void)V; (void)dtype; (void)top_n;
-  return 0;
+  const int64_t parts = parts_for(V, dtype);
+  if (parts == 1) return 0;
+  const size_t n = (size_t)B * parts;
+  return align256(n * sizeof(Part)) + (top_n > 0 ? n * kListCap * sizeof(uint64_t) : 0);
+}
+
+bool grid_fits(int64_t B, int64_t V, int dtype) {
+  return B * parts_for(V, dtype) * kPartBlock < (int64_t)1 << 32;
 }
 
 hipError_t launch_score(const Args& a, int dtype, int B, void* workspace, hipStream_t st) {
-  (void)workspace;
-  if (dtype == QS_F32)
-    hipLaunchKernelGGL(score_kernel<QS_F32>, dim3((unsigned)B), dim3(kBlock), 0, st, a);
-  else
-    hipLaunchKernelGGL(score_kernel<QS_BF16>, dim3((unsigned)B), dim3(kBlock), 0, st, a);
-  return hipGetLastError();
+  const int parts = (int)parts_for(a.V, dtype);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  return dtype == QS_F32 ? launch_dt<QS_F32>(a, B, parts, ws, st)
+                         : launch_dt<QS_BF16>(a, B, parts, ws, st);
 }
 
 }  // namespace score

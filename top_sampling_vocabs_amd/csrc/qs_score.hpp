@@ -51,6 +51,10 @@ struct GradArgs {
 };
 
 size_t workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n);
+// whether one workgroup per part of every row fits one launch grid (batches
+// past that, over 2^24 parts, are larger than the memory)
+bool grid_fits(int64_t B, int64_t V, int dtype);
+bool grad_grid_fits(int64_t B, int64_t V, int dtype);
 hipError_t launch_score(const Args& a, int dtype, int B, void* workspace, hipStream_t st);
 hipError_t launch_grad(const GradArgs& a, int dtype, int B, hipStream_t st);
 

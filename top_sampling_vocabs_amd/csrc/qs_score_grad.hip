@@ -2,10 +2,17 @@
 // the logits:
 //   dz_i = (1/T) [ sum_g gl_g (1[i = t_g] - p_i) - gH p_i (log p_i + H) ]
 // for legal i, 0 elsewhere, with log p_i = (z_i - m) / T - log S from the
-// forward pass's row maximum and log sum.
+// forward pass's row maximum and log sum. With a_i = log2 p_i, per row
+//   dz_i = p_i (A + B a_i) + hit_i / T,
+//   A = -(sum_g gl_g + gH H) / T,  B = -gH ln 2 / T,
+// so a token costs one exponential and a few operations, and the kernel is
+// bound by reading the logits and writing their gradient once.
 //
-// One thread per token; a token named by several slots gets their sum, added
-// in slot order and rounded once.
+// A workgroup takes kLoads 16-byte loads per lane of one row. Which 16-byte
+// chunks hold a given token is a bitmap in LDS (built from the row's token
+// list; a single token is compared directly), so that only those chunks look
+// at the list. A token named by several slots gets their sum, in slot order,
+// and each element is rounded once.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -19,48 +26,170 @@ namespace score {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kLoads = 4;  // 16-byte loads per lane
 
-template <int DT>
-__global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a) {
-  const int r = blockIdx.x;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+template <int DT> constexpr int kPer = DT == QS_F32 ? 4 : 8;  // tokens per 16-byte load
+
+__device__ __forceinline__ float clamp_to(float x, float most) {
+  return fminf(fmaxf(x, -most), most);
+}
+
+template <int DT, bool MASK, bool ONE>
+__global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
+  constexpr int P = kPer<DT>;
+  __shared__ uint32_t s_hit[kBlock * kLoads / 32];
+  const int tid = threadIdx.x;
+  const int r = (int)(blockIdx.x / (unsigned)chunks);
+  const int begin = (int)(blockIdx.x - (unsigned)r * (unsigned)chunks) * (kBlock * kLoads * P);
   const uint8_t* row = a.logits + (size_t)r * a.row_bytes;
   uint8_t* out = a.grad + (size_t)r * a.grad_bytes;
-  const uint32_t* bm = a.bitmask ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
   const int32_t* tokens = a.tokens + (size_t)r * a.G;
   const float* gl = a.g_lp + (size_t)r * a.G;
   const bool ok = a.status[r] == QS_ROW_OK;
-  const float T = a.T ? a.T[r] : 1.0f;
-  const float m = a.row_max[r], log_sum = a.log_sum[r];
-  const float gH = a.g_ent ? a.g_ent[r] : 0.0f, H = a.g_ent ? a.entropy[r] : 0.0f;
-  float gs = 0.0f;
-  for (int g = 0; g < a.G; ++g)
-    if (tokens[g] >= 0) gs += gl[g];
-  for (int i = threadIdx.x; i < a.V; i += kBlock) {
-    float v = 0.0f;
-    if (ok && (bm == nullptr || ((bm[i >> 5] >> (i & 31)) & 1u))) {
-      float z;
-      if constexpr (DT == QS_F32) z = reinterpret_cast<const float*>(row)[i];
-      else z = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
-      const float lp = (z - m) / T - log_sum;
-      const float p = __expf(lp);
-      v = -p * gs;
-      if (p > 0.0f) v -= gH * p * (lp + H);
-      for (int g = 0; g < a.G; ++g)
-        if (tokens[g] == i) v += gl[g];
-      v /= T;
+
+  uint4 v[kLoads];
+  uint32_t legal[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int i = begin + (u * kBlock + tid) * P;
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    legal[u] = 0u;
+    if (i < a.V && ok) {
+      v[u] = *reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P));
+      legal[u] = 0xFFu;
+      if constexpr (MASK) {
+        legal[u] = reinterpret_cast<const uint8_t*>(a.bitmask + (size_t)r * a.bm_stride)[i >> 3];
+        if constexpr (P == 4) legal[u] >>= i & 4;
+      }
     }
-    if constexpr (DT == QS_F32) reinterpret_cast<float*>(out)[i] = v;
-    else reinterpret_cast<__bf16*>(out)[i] = (__bf16)v;
   }
+
+  const float T = a.T ? a.T[r] : 1.0f;
+  const float inv_T = fminf(1.0f / T, 1e38f);
+  const float c = fminf(fmaxf(1.4426950408889634f / T, 1.17549435e-38f), 3.4e38f);
+  const float m = a.row_max[r];
+  const float ls2 = a.log_sum[r] * 1.4426950408889634f;
+  float gs = 0.0f;
+  int only = -1;
+  if constexpr (ONE) {
+    only = tokens[0];
+    if (only >= 0 && only < a.V) gs = gl[0];
+  } else {
+    for (int k = tid; k < kBlock * kLoads / 32; k += kBlock) s_hit[k] = 0u;
+    __syncthreads();
+    // every wave sums the list (the same order, the same bits)
+    for (int g = lane_id(); g < a.G; g += 64) {
+      const int t = tokens[g];
+      if (t < 0 || t >= a.V) continue;
+      gs += gl[g];
+      const int k = (t - begin) / P;
+      if (t >= begin && k < kBlock * kLoads) atomicOr(&s_hit[k >> 5], 1u << (k & 31));
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) gs += __shfl_xor(gs, off, 64);
+    __syncthreads();
+  }
+  const float gH = a.g_ent ? a.g_ent[r] : 0.0f, H = a.g_ent ? a.entropy[r] : 0.0f;
+  // finite, so that a p of 0 gives 0
+  const float A = clamp_to(-(gs + gH * H) * inv_T, 3e38f);
+  const float Bc = clamp_to(-gH * 0.6931471805599453f * inv_T, 1e36f);
+
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int k = u * kBlock + tid;
+    const int i = begin + k * P;
+    if (i >= a.V) break;
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+    float x[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      float z;
+      if constexpr (DT == QS_F32) z = __uint_as_float(w[e]);
+      else z = __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+      const float l = fmaxf((z - m) * c - ls2, -200.0f);
+      x[e] = __builtin_amdgcn_exp2f(l) * (A + Bc * l);
+    }
+    if constexpr (ONE) {
+      if (only >= i && only < i + P) {
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+          if (only == i + e) x[e] += gs * inv_T;
+      }
+    } else if ((s_hit[k >> 5] >> (k & 31)) & 1u) {
+      float hit[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) hit[e] = 0.0f;
+      for (int g = 0; g < a.G; ++g) {
+        const int t = tokens[g] - i;
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+          if (t == e) hit[e] += gl[g];
+      }
+#pragma unroll
+      for (int e = 0; e < P; ++e) x[e] += hit[e] * inv_T;
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if constexpr (DT == QS_F32) {
+        const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)legal[u], d, 1);
+        o[d] = __float_as_uint(x[d]) & keep;
+      } else {
+        const f32x2 pair = {x[2 * d], x[2 * d + 1]};
+        o[d] = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2));
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe((int)legal[u], 2 * d, 1);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_sbfe((int)legal[u], 2 * d + 1, 1);
+        o[d] &= bfi(0xFFFFu, lo, hi);
+      }
+    }
+    uint8_t* const at = out + (size_t)i * (16 / P);
+    if (a.V - i >= P) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {  // the row's last tokens: what lies behind them stays
+#pragma unroll
+      for (int e = 0; e < P - 1; ++e) {
+        if (i + e < a.V) {
+          if constexpr (DT == QS_F32) reinterpret_cast<uint32_t*>(at)[e] = o[e];
+          else reinterpret_cast<uint16_t*>(at)[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+}
+
+template <int DT>
+void launch(const GradArgs& a, unsigned blocks, int chunks, hipStream_t st) {
+  const dim3 grid(blocks), block(kBlock);
+  const bool mask = a.bitmask != nullptr, one = a.G == 1;
+  if (mask && one)
+    hipLaunchKernelGGL((grad_kernel<DT, true, true>), grid, block, 0, st, a, chunks);
+  else if (mask)
+    hipLaunchKernelGGL((grad_kernel<DT, true, false>), grid, block, 0, st, a, chunks);
+  else if (one)
+    hipLaunchKernelGGL((grad_kernel<DT, false, true>), grid, block, 0, st, a, chunks);
+  else
+    hipLaunchKernelGGL((grad_kernel<DT, false, false>), grid, block, 0, st, a, chunks);
+}
+
+int64_t chunks_for(int64_t V, int dtype) {
+  const int64_t n = (int64_t)kBlock * kLoads * (dtype == QS_F32 ? 4 : 8);
+  return (V + n - 1) / n;
 }
 
 }  // namespace
 
+bool grad_grid_fits(int64_t B, int64_t V, int dtype) {
+  return B * chunks_for(V, dtype) * kBlock < (int64_t)1 << 32;
+}
+
 hipError_t launch_grad(const GradArgs& a, int dtype, int B, hipStream_t st) {
-  if (dtype == QS_F32)
-    hipLaunchKernelGGL(grad_kernel<QS_F32>, dim3((unsigned)B), dim3(kBlock), 0, st, a);
-  else
-    hipLaunchKernelGGL(grad_kernel<QS_BF16>, dim3((unsigned)B), dim3(kBlock), 0, st, a);
+  const int chunks = (int)chunks_for(a.V, dtype);
+  const unsigned blocks = (unsigned)B * (unsigned)chunks;
+  if (dtype == QS_F32) launch<QS_F32>(a, blocks, chunks, st);
+  else launch<QS_BF16>(a, blocks, chunks, st);
   return hipGetLastError();
 }
 
