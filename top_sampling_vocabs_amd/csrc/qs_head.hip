@@ -2,9 +2,25 @@
 //   y[b][v] = sum_g s[v][g] sum_{k in g} x[b][k] (q[v][k] - z[v][g]),
 // q the codes 0..15, s a scale and z a zero point per row and group of k.
 //
-// One wave per vocabulary row and hidden row: each lane takes every 64th
-// dword of the row's codes (8 columns, inside one group), and the wave adds
-// the lanes' sums.
+// The codes are streamed once from memory in the checkpoint's own row order and
+// meet the matrix cores without a table: a nibble shifted to bits 3..6 under
+// the exponent of 16 is the bf16 number 16 + q, so one shift and one and-or
+// make two factors, and
+//   sum x (q - z) = sum x (16 + q) - (16 + z) sum x
+// with exact products and float32 sums; sum x comes from the same fragments
+// against a fragment of ones. The scale is applied to the float32 group sum,
+// never to a factor, so no weight is rounded.
+//
+// A 16x16x32 product takes 16 hidden rows (A) and 16 vocabulary rows (B), 8
+// columns of k per lane on both sides. Which columns those are is free as long
+// as both sides agree and a product stays inside one group: a lane reads 16, 8
+// or 4 bytes of codes in a row (groups of 128, 64, 32) per 128-column step. The
+// nibbles i and i + 4 of a dword share a register, so the hidden values are
+// laid out in the order 0 4 1 5 2 6 3 7 beforehand.
+//
+// Up to 16 hidden rows whose values fit LDS stay there for the whole launch
+// (head_resident_kernel): every wave then walks its own vocabulary tiles with
+// kDepth steps of codes in flight and no barrier.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -16,6 +32,281 @@
 namespace qs {
 namespace head {
 namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kStepK = 128;                // columns per step
+constexpr int kChunks = kStepK / 8;        // 8-column chunks per step
+constexpr uint32_t kOnes = 0x3F803F80u;    // two bf16 ones
+
+// Where an MFMA's 8 columns of lane group kg lie, in chunks of the step.
+template <int G>
+__device__ __forceinline__ int chunk_of(int j, int kg) {
+  if constexpr (G == 128) return kg * 4 + j;
+  if constexpr (G == 64) return (j >> 1) * 8 + kg * 2 + (j & 1);
+  return j * 4 + kg;
+}
+
+// The two constants of a code's bf16 factor, in a scalar and a vector register so
+// that and and or are one instruction.
+struct Pattern {
+  uint32_t mant, exp;
+  __device__ __forceinline__ Pattern() : mant(0x00780078u), exp(0x41804180u) {
+    asm("" : "+s"(mant));
+    asm("" : "+v"(exp));
+  }
+};
+
+// 8 codes as the bf16 numbers 16 + q, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ bf16x8 factors(uint32_t c, const Pattern& k) {
+  u32x4 r;
+  r.x = ((c << 3) & k.mant) | k.exp;
+  r.y = ((c >> 1) & k.mant) | k.exp;
+  r.z = ((c >> 5) & k.mant) | k.exp;
+  r.w = ((c >> 9) & k.mant) | k.exp;
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// 8 hidden values in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 ordered(const uint4& v) {
+  return make_uint4(bfi(0xFFFFu, v.x, v.z << 16), bfi(0xFFFFu, v.x >> 16, v.z),
+                    bfi(0xFFFFu, v.y, v.w << 16), bfi(0xFFFFu, v.y >> 16, v.w));
+}
+
+__device__ __forceinline__ void store_logit(const Args& a, int b, int v, float y) {
+  const size_t o = (size_t)b * a.row_stride + v;
+  if (a.logits_dtype == QS_F32) static_cast<float*>(a.logits)[o] = y;
+  else static_cast<__bf16*>(a.logits)[o] = (__bf16)y;
+}
+
+// ---------------------------------------------------------------------------
+
+constexpr int kThreads8 = 512;          // 8 waves
+// waves per SIMD that the registers are held to
+constexpr int occupancy(int P, int MT) { return P * MT <= 4 ? 4 : 2; }
+
+// The hidden values of one slice of k stay in each wave's registers: the 8
+// waves of a workgroup are KS slices of k by 8 / KS tiles of 16 vocabulary
+// rows, a wave holds P steps of x (16 MT hidden rows), and the workgroup walks
+// the tiles. A wave's codes of a tile are P * 64 consecutive bytes a row: they
+// are read with consecutive lanes on consecutive bytes (lanes in the product's
+// own order, 16 rows apart, cost four times the cache accesses), one tile ahead,
+// and change lanes through the wave's own LDS. The slices' float32 sums meet in
+// LDS (two buffers, one barrier a tile) and are added in slice order.
+template <int P, int MT, int G, int SD, bool ZEROS>
+__global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
+    head_split_kernel(Args a, int steps, int tiles, int ks_log2) {
+  constexpr int kGroups = kStepK / G;      // groups per step
+  constexpr int NG = P * kGroups;          // groups per slice
+  constexpr int CL = 4 * P;                // lanes per row of a code load
+  constexpr int kRows = 64 / CL;           // rows per code load
+  constexpr int kCodeStride = P * 64 + 16; // bytes per row in LDS
+  constexpr int kScaleStride = NG + 4;     // floats per row in LDS
+  constexpr int SL = NG < 4 ? NG : 4;      // lanes per row of a scale load
+  constexpr int EL = NG / SL;              // scales per lane
+  __shared__ f32x4 s_part[2][8][MT][64];
+  __shared__ f32x4 s_sum[8][NG][MT][4];    // sums of x over a slice's groups
+  __shared__ __align__(16) uint8_t s_code[8][16 * kCodeStride];
+  __shared__ __align__(16) float s_scale[8][16 * kScaleStride];
+  __shared__ __align__(16) float s_off[ZEROS ? 8 : 1][ZEROS ? 16 * kScaleStride : 1];
+  const int tid = threadIdx.x;
+  const int w = uni(tid >> 6);
+  const int lane = lane_id();
+  const int n = lane & 15, kg = lane >> 4;
+  const int KS = 1 << ks_log2, TG = 8 >> ks_log2;
+  const int ks = w & (KS - 1), tg = w >> ks_log2;
+  const int per = (steps + KS - 1) >> ks_log2;  // at most P
+  const int s0 = ks * per;
+  const int mine = max(0, min(per, steps - s0));
+  const int k0 = s0 * kStepK;                    // the slice's first column
+  const int cols = max(0, min(mine * kStepK, a.K - k0));
+  const int batches = (tiles + TG - 1) / TG;
+
+  // a tile's codes, scales and zero points, lanes along the rows: a scalar base
+  // per tile and a lane's offset from it, which only the last tile changes
+  const int c_row = lane / CL, c_chunk = lane % CL;
+  const int g_row = min(lane / SL, 15), g_part = (lane % SL) * EL;
+  const bool c_in = c_chunk * 32 < cols;
+  const int groups = cols / G;
+  constexpr int kScaleSize = SD == QS_F32 ? 4 : 2;
+  using Raw = std::conditional_t<SD == QS_F32, float, uint16_t>;
+  u32x4 code[P];
+  Raw scale[EL];
+  uint8_t zero[EL];
+  auto load_tile = [&](int tile) {
+    const int last = min(15, a.V - 1 - tile * 16);  // below 0 past the last tile
+    const int v0 = last < 0 ? a.V - 1 : tile * 16;
+    const int rows = max(last, 0);
+    const uint8_t* const pc = a.codes + (size_t)v0 * a.codes_stride + (k0 >> 1);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const uint32_t at = (uint32_t)min(i * kRows + c_row, rows) * (uint32_t)a.codes_stride +
+                          (uint32_t)c_chunk * 16u;
+      if (c_in) code[i] = *reinterpret_cast<const u32x4*>(pc + at);
+    }
+    const int g = k0 / G;
+    const uint8_t* const ps = static_cast<const uint8_t*>(a.scales) +
+                              ((size_t)v0 * a.scale_stride + g) * kScaleSize;
+    const uint32_t row = (uint32_t)min(g_row, rows);
+    const uint32_t at = (row * (uint32_t)a.scale_stride + (uint32_t)g_part) * kScaleSize;
+    const uint8_t* const pz = ZEROS ? a.zeros + (size_t)v0 * a.zero_stride + g : nullptr;
+    const uint32_t zat = row * (uint32_t)a.zero_stride + (uint32_t)g_part;
+    if (groups == NG) {
+      __builtin_memcpy(scale, ps + at, kScaleSize * EL);
+      if constexpr (ZEROS) __builtin_memcpy(zero, pz + zat, EL);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) {
+        scale[e] = Raw(0);
+        zero[e] = 0;
+        if (g_part + e < groups) {
+          scale[e] = reinterpret_cast<const Raw*>(ps + at)[e];
+          if constexpr (ZEROS) zero[e] = pz[zat + e];
+        }
+      }
+    }
+  };
+  int batch = blockIdx.x;
+  load_tile(batch * TG + tg);
+
+  bf16x8 x[P][4][MT];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int k = k0 + p * kStepK + chunk_of<G>(j, kg) * 8;
+        const int m = min(t * 16 + n, a.B - 1);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (p < mine && k < a.K)
+          v = ordered(*reinterpret_cast<const uint4*>(a.hidden + (size_t)m * a.hidden_stride + k));
+        x[p][j][t] = __builtin_bit_cast(bf16x8, v);
+      }
+    }
+  }
+  {
+    const u32x4 one = {kOnes, kOnes, kOnes, kOnes};
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int jj = 0; jj < G / 32; ++jj) {
+          const int j = g * (G / 32) + jj;
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j / 4][j % 4][t], ones, sum, 0, 0, 0);
+        }
+        // every column holds the same sums: one lane per four rows writes them
+        if (!ZEROS) sum *= -24.0f;
+        if (n == 0) s_sum[w][g][t][kg] = sum;
+      }
+    }
+  }
+  const Pattern pattern;
+
+  int buf = 0;
+  for (; batch < batches; batch += gridDim.x) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      *reinterpret_cast<u32x4*>(&s_code[w][(i * kRows + c_row) * kCodeStride + c_chunk * 16]) =
+          code[i];
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+      float sc;
+      if constexpr (SD == QS_F32) sc = scale[e];
+      else sc = __uint_as_float((uint32_t)scale[e] << 16);
+      s_scale[w][g_row * kScaleStride + g_part + e] = sc;
+      if constexpr (ZEROS) s_off[w][g_row * kScaleStride + g_part + e] = -16.0f - (float)zero[e];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    load_tile((batch + (int)gridDim.x) * TG + tg);
+
+    f32x4 y[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) y[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint8_t* const row = &s_code[w][n * kCodeStride + p * 64];
+      uint32_t q[4];
+      if constexpr (G == 128) {
+        *reinterpret_cast<u32x4*>(q) = *reinterpret_cast<const u32x4*>(row + kg * 16);
+      } else if constexpr (G == 64) {
+        *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(row + kg * 8);
+        *reinterpret_cast<uint2*>(q + 2) = *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          q[j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        constexpr int J = G / 32;
+        const float sc = s_scale[w][n * kScaleStride + p * kGroups + g];
+        f32x4 acc[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          acc[t] = s_sum[w][p * kGroups + g][t][kg];
+          if constexpr (ZEROS) acc[t] *= s_off[w][n * kScaleStride + p * kGroups + g];
+        }
+#pragma unroll
+        for (int jj = 0; jj < J; ++jj) {
+          const int j = g * J + jj;
+          const bf16x8 f = factors(q[j], pattern);
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p][j][t], f, acc[t], 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[t][e] += sc * acc[t][e];
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) s_part[buf][w][t][lane] = y[t];
+    __syncthreads();
+    for (int i = tid; i < TG * MT * 256; i += kThreads8) {
+      const int q = i / (MT * 256), t = (i >> 8) % MT;
+      const int m = (i >> 4) & 15, col = i & 15;
+      const int v = (batch * TG + q) * 16 + col, b = t * 16 + m;
+      if (v < a.V && b < a.B) {
+        float sum = 0.0f;
+        for (int k = 0; k < KS; ++k) sum += s_part[buf][q * KS + k][t][(m >> 2) * 16 + col][m & 3];
+        store_logit(a, b, v, sum);
+      }
+    }
+    buf ^= 1;
+  }
+}
+
+template <int P, int MT, int G, int SD, bool ZEROS>
+hipError_t launch_split(const Args& a, int steps, int ks_log2, hipStream_t st) {
+  const int tiles = (a.V + 15) / 16;
+  const int tg = 8 >> ks_log2;
+  const int grid = min(512, (tiles + tg - 1) / tg);
+  hipLaunchKernelGGL((head_split_kernel<P, MT, G, SD, ZEROS>), dim3((unsigned)grid),
+                     dim3(kThreads8), 0, st, a, steps, tiles, ks_log2);
+  return hipGetLastError();
+}
+
+template <int MT, int G, int SD, bool ZEROS>
+hipError_t pick_steps(const Args& a, hipStream_t st) {
+  const int steps = (a.K + kStepK - 1) / kStepK;
+  // the fewest slices that leave a wave at most 4 steps
+  int ks_log2 = 0;
+  while (ks_log2 < 3 && (steps + (1 << ks_log2) - 1) >> ks_log2 > 4) ++ks_log2;
+  const int per = (steps + (1 << ks_log2) - 1) >> ks_log2;
+  if (per <= 1) return launch_split<1, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  if (per == 2) return launch_split<2, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  if (per <= 4) return launch_split<4, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  return launch_split<8, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+}
 
 constexpr int kBlock = 256;
 
@@ -50,9 +341,23 @@ __global__ void __launch_bounds__(kBlock) head_kernel(Args a) {
   }
 }
 
+template <int G, int SD>
+hipError_t pick_zeros(const Args& a, hipStream_t st) {
+  return a.zeros ? pick_steps<1, G, SD, true>(a, st) : pick_steps<1, G, SD, false>(a, st);
+}
+template <int G>
+hipError_t pick_scale(const Args& a, hipStream_t st) {
+  return a.scale_dtype == QS_F32 ? pick_zeros<G, QS_F32>(a, st) : pick_zeros<G, QS_BF16>(a, st);
+}
+
 }  // namespace
 
 hipError_t launch_head(const Args& a, hipStream_t st) {
+  if (a.B <= 16 && a.K <= 8192) {
+    if (a.group == 128) return pick_scale<128>(a, st);
+    if (a.group == 64) return pick_scale<64>(a, st);
+    return pick_scale<32>(a, st);
+  }
   const unsigned gx = (unsigned)((a.V + kBlock / 64 - 1) / (kBlock / 64));
   const unsigned gy = (unsigned)(a.B < 64 ? a.B : 64);
   hipLaunchKernelGGL(head_kernel, dim3(gx, gy), dim3(kBlock), 0, st, a);
