@@ -29,7 +29,14 @@ struct Args {
   int64_t row_stride;
 };
 
-hipError_t launch_head(const Args& a, hipStream_t st);
+// one translation unit per group size
+hipError_t launch_g32(const Args& a, hipStream_t st);
+hipError_t launch_g64(const Args& a, hipStream_t st);
+hipError_t launch_g128(const Args& a, hipStream_t st);
+
+inline hipError_t launch_head(const Args& a, hipStream_t st) {
+  return a.group == 128 ? launch_g128(a, st) : a.group == 64 ? launch_g64(a, st) : launch_g32(a, st);
+}
 
 }  // namespace head
 }  // namespace qs

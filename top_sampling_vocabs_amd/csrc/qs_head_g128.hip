@@ -1,0 +1,10 @@
+// The 4-bit output head's kernels for groups of 128 columns.
+#include "qs_head_kernels.hpp"
+
+namespace qs {
+namespace head {
+
+hipError_t launch_g128(const Args& a, hipStream_t st) { return pick_scale<128>(a, st); }
+
+}  // namespace head
+}  // namespace qs

@@ -22,6 +22,8 @@
 // (head_resident_kernel): every wave then walks its own vocabulary tiles with
 // kDepth steps of codes in flight and no barrier.
 
+#pragma once
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -224,7 +226,9 @@ __global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_sched_barrier(0);
     load_tile((batch + (int)gridDim.x) * TG + tg);
+    __builtin_amdgcn_sched_barrier(0);
 
     f32x4 y[MT];
 #pragma unroll
@@ -267,6 +271,8 @@ __global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
           for (int e = 0; e < 4; ++e) y[t][e] += sc * acc[t][e];
         }
       }
+      // one step's LDS reads at a time: more in flight spill registers
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) s_part[buf][w][t][lane] = y[t];
@@ -289,7 +295,7 @@ template <int P, int MT, int G, int SD, bool ZEROS>
 hipError_t launch_split(const Args& a, int steps, int ks_log2, hipStream_t st) {
   const int tiles = (a.V + 15) / 16;
   const int tg = 8 >> ks_log2;
-  const int grid = min(512, (tiles + tg - 1) / tg);
+  const int grid = min(occupancy(P, MT) == 4 ? 512 : 256, (tiles + tg - 1) / tg);
   hipLaunchKernelGGL((head_split_kernel<P, MT, G, SD, ZEROS>), dim3((unsigned)grid),
                      dim3(kThreads8), 0, st, a, steps, tiles, ks_log2);
   return hipGetLastError();
@@ -308,42 +314,275 @@ hipError_t pick_steps(const Args& a, hipStream_t st) {
   return launch_split<8, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
 }
 
-constexpr int kBlock = 256;
+// ---------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(kBlock) head_kernel(Args a) {
-  const int v = blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-  if (v >= a.V) return;
+constexpr int kChunkK = 2 * kStepK;      // columns per chunk: 128 bytes of codes a row
+constexpr int kMaxRows = 64;             // hidden rows per launch
+
+// More hidden rows, or rows too long for the registers: x passes through LDS in
+// chunks of 256 columns (two buffers, one barrier a chunk), already in the
+// product's lane order, with the sums of its groups; every wave of the
+// workgroup multiplies the same chunk with up to NT tiles of its own, whose
+// sums stay in registers over all of k. A chunk's codes, scales and hidden
+// values are requested while the chunk before is multiplied. With one
+// workgroup per compute unit the rows of a wave's tiles follow one another, so
+// x is read from L2 once per 8 NT tiles.
+template <int MT, int NT, int G, int SD, bool ZEROS>
+__global__ void __launch_bounds__(kThreads8, 2) head_stream_kernel(Args a, int chunks, int tiles) {
+  constexpr int GC = kChunkK / G;          // groups per chunk
+  constexpr int SL = GC < 4 ? GC : 4;      // lanes per row of a scale load
+  constexpr int EL = GC / SL;              // scales per lane
+  constexpr int kCodeStride = 128 + 16;    // bytes per row in LDS
+  constexpr int kScaleStride = GC + 4;     // floats per row in LDS
+  constexpr int XI = MT;                   // 16-byte items of x per thread
+  constexpr int kScaleSize = SD == QS_F32 ? 4 : 2;
+  using Raw = std::conditional_t<SD == QS_F32, float, uint16_t>;
+  __shared__ uint4 s_x[2][8 * MT * 64];
+  __shared__ float s_sum[2][GC][MT * 16];
+  __shared__ __align__(16) uint8_t s_code[8][2][16 * kCodeStride];
+  __shared__ __align__(16) float s_scale[8][NT][16 * kScaleStride];
+  __shared__ __align__(16) float s_off[ZEROS ? 8 : 1][ZEROS ? NT : 1][ZEROS ? 16 * kScaleStride : 1];
+  const int tid = threadIdx.x;
+  const int w = uni(tid >> 6);
   const int lane = lane_id();
-  const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes + (size_t)v * a.codes_stride);
-  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const uint16_t* x = a.hidden + (size_t)b * a.hidden_stride;
-    float acc = 0.0f;
-    for (int i = lane; i < a.K / 8; i += 64) {
-      const uint32_t c = codes[i];
-      const int g = i * 8 / a.group;
-      const size_t gi = (size_t)v * a.scale_stride + g;
-      const float s = a.scale_dtype == QS_F32
-                          ? static_cast<const float*>(a.scales)[gi]
-                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.scales)[gi] << 16);
-      const float zero = a.zeros ? (float)a.zeros[(size_t)v * a.zero_stride + g] : 8.0f;
-      float t = 0.0f;
+  const int n = lane & 15, kg = lane >> 4;
+  const int row0 = (int)blockIdx.y * kMaxRows;
+  const int rows_x = min(a.B - row0, MT * 16);
+
+  // x: 32 lanes along a row's chunk, 16 rows at a time
+  const int xc = tid & 31, xm = tid >> 5;
+  uint4 xv[XI];
+  auto load_x = [&](int chunk) {
+    const int k = chunk * kChunkK + xc * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        t += __uint_as_float((uint32_t)x[i * 8 + j] << 16) * ((float)((c >> (4 * j)) & 15u) - zero);
-      acc += s * t;
+    for (int i = 0; i < XI; ++i) {
+      const int m = xm + 16 * i;
+      xv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (m < rows_x && k < a.K)
+        xv[i] = *reinterpret_cast<const uint4*>(a.hidden + (size_t)(row0 + m) * a.hidden_stride + k);
     }
-    for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
-    if (lane == 0) {
-      const size_t o = (size_t)b * a.row_stride + v;
-      if (a.logits_dtype == QS_F32) static_cast<float*>(a.logits)[o] = acc;
-      else static_cast<__bf16*>(a.logits)[o] = (__bf16)acc;
+  };
+  // where item c (8 columns) of a chunk goes: step p, product j, lane group g;
+  // within the product's 64 places rows are turned by 4 g + j, so that neither
+  // these writes nor the reads meet in a bank
+  const int xp = xc >> 4, xs = xc & 15;
+  const int xj = G == 128 ? xs & 3 : G == 64 ? (xs >> 3) * 2 + (xs & 1) : xs >> 2;
+  const int xg = G == 128 ? xs >> 2 : G == 64 ? (xs >> 1) & 3 : xs & 3;
+  auto place = [](int p, int j, int t, int g, int m) {
+    return ((p * 4 + j) * MT + t) * 64 + g * 16 + ((m + 4 * g + j) & 15);
+  };
+  auto store_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const uint32_t q[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum += __uint_as_float(q[e] << 16) + __uint_as_float(q[e] & 0xFFFF0000u);
+      sum += __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(sum)));
+      sum += __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(sum)));
+      if constexpr (G >= 64) sum += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(sum)));
+      if constexpr (G == 128) sum += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(sum)));
+      s_x[buf][place(xp, xj, i, xg, xm)] = ordered(xv[i]);
+      if ((xc & (G / 8 - 1)) == 0) s_sum[buf][xc / (G / 8)][xm + 16 * i] = ZEROS ? sum : -24.0f * sum;
+    }
+  };
+
+  const int c_row = lane >> 3, c_part = lane & 7;
+  const int g_row = min(lane / SL, 15), g_part = (lane % SL) * EL;
+  const Pattern pattern;
+
+  for (int round = (int)blockIdx.x * 8 * NT; round < tiles; round += (int)gridDim.x * 8 * NT) {
+    const int first = round + w * NT;
+    u32x4 code[NT][2];
+    Raw scale[NT][EL];
+    uint8_t zero[NT][EL];
+    auto load_weights = [&](int chunk) {
+      const int k0 = chunk * kChunkK;
+      const bool c_in = k0 + c_part * 32 < a.K;
+      const int g = k0 / G, groups = min(GC, a.K / G - g);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        // past the last tile: the last row again, never stored
+        const int v0 = min((first + i) * 16, a.V - 1), rows = min(15, a.V - 1 - v0);
+        const uint8_t* const pc = a.codes + (size_t)v0 * a.codes_stride + (k0 >> 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = (uint32_t)min(h * 8 + c_row, rows) * (uint32_t)a.codes_stride +
+                              (uint32_t)c_part * 16u;
+          if (c_in) code[i][h] = *reinterpret_cast<const u32x4*>(pc + at);
+        }
+        const uint8_t* const ps = static_cast<const uint8_t*>(a.scales) +
+                                  ((size_t)v0 * a.scale_stride + g) * kScaleSize;
+        const uint32_t row = (uint32_t)min(g_row, rows);
+        const uint32_t at = (row * (uint32_t)a.scale_stride + (uint32_t)g_part) * kScaleSize;
+        const uint8_t* const pz = ZEROS ? a.zeros + (size_t)v0 * a.zero_stride + g : nullptr;
+        const uint32_t zat = row * (uint32_t)a.zero_stride + (uint32_t)g_part;
+        if (groups == GC) {
+          __builtin_memcpy(scale[i], ps + at, kScaleSize * EL);
+          if constexpr (ZEROS) __builtin_memcpy(zero[i], pz + zat, EL);
+        } else {
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            scale[i][e] = Raw(0);
+            zero[i][e] = 0;
+            if (g_part + e < groups) {
+              scale[i][e] = reinterpret_cast<const Raw*>(ps + at)[e];
+              if constexpr (ZEROS) zero[i][e] = pz[zat + e];
+            }
+          }
+        }
+      }
+    };
+
+    f32x4 y[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) y[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __syncthreads();  // the round before has read its last chunk
+    load_x(0);
+    load_weights(0);
+    store_x(0);
+    if (chunks > 1) load_x(1);
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      const int buf = chunk & 1;
+      // this chunk's codes through LDS: from lanes along a row to the product's
+      uint32_t q[NT][8];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        uint8_t* const turn = s_code[w][i & 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<u32x4*>(turn + (h * 8 + c_row) * kCodeStride + c_part * 16) = code[i][h];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          float sc;
+          if constexpr (SD == QS_F32) sc = scale[i][e];
+          else sc = __uint_as_float((uint32_t)scale[i][e] << 16);
+          s_scale[w][i][g_row * kScaleStride + g_part + e] = sc;
+          if constexpr (ZEROS)
+            s_off[w][i][g_row * kScaleStride + g_part + e] = -16.0f - (float)zero[i][e];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint8_t* const row = turn + n * kCodeStride + p * 64;
+          if constexpr (G == 128) {
+            *reinterpret_cast<u32x4*>(&q[i][p * 4]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
+          } else if constexpr (G == 64) {
+            *reinterpret_cast<uint2*>(&q[i][p * 4]) = *reinterpret_cast<const uint2*>(row + kg * 8);
+            *reinterpret_cast<uint2*>(&q[i][p * 4 + 2]) =
+                *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              q[i][p * 4 + j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
+          }
+        }
+      }
+      __syncthreads();  // x of this chunk is in place, the other buffer is free
+      if (chunk + 1 < chunks) {
+        store_x(buf ^ 1);
+        load_weights(chunk + 1);
+        if (chunk + 2 < chunks) load_x(chunk + 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int g = 0; g < GC / 2; ++g) {
+          constexpr int J = G / 32;
+          const int gi = p * (GC / 2) + g;
+          f32x4 acc[NT][MT];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_sum[buf][gi][t * 16 + kg * 4]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              acc[i][t] = sum;
+              if constexpr (ZEROS) acc[i][t] *= s_off[w][i][n * kScaleStride + gi];
+            }
+          }
+#pragma unroll
+          for (int jj = 0; jj < J; ++jj) {
+            const int j = g * J + jj;
+            bf16x8 x[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+              x[t] = __builtin_bit_cast(bf16x8, s_x[buf][place(p, j, t, kg, n)]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const bf16x8 f = factors(q[i][p * 4 + j], pattern);
+#pragma unroll
+              for (int t = 0; t < MT; ++t)
+                acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t], f, acc[i][t], 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const float sc = s_scale[w][i][n * kScaleStride + gi];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[i][t][e] += sc * acc[i][t][e];
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int v = (first + i) * 16 + n;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int m = t * 16 + kg * 4 + e;
+          if (v < a.V && m < rows_x) store_logit(a, row0 + m, v, y[i][t][e]);
+        }
+      }
     }
   }
 }
 
+template <int MT, int NT, int G, int SD, bool ZEROS>
+hipError_t launch_stream_nt(const Args& a, int tiles, hipStream_t st) {
+  const int chunks = (a.K + kChunkK - 1) / kChunkK;
+  const int grid = min(256, (tiles + 8 * NT - 1) / (8 * NT));
+  const int blocks = (a.B + kMaxRows - 1) / kMaxRows;
+  hipLaunchKernelGGL((head_stream_kernel<MT, NT, G, SD, ZEROS>),
+                     dim3((unsigned)grid, (unsigned)blocks), dim3(kThreads8), 0, st, a, chunks,
+                     tiles);
+  return hipGetLastError();
+}
+
+template <int MT, int G, int SD, bool ZEROS>
+hipError_t launch_stream(const Args& a, hipStream_t st) {
+  const int tiles = (a.V + 15) / 16;
+  // the fewest rounds of at most 3 tiles a wave over 256 workgroups, evenly
+  const int rounds = (tiles + 256 * 8 * 3 - 1) / (256 * 8 * 3);
+  const int per_wave = (tiles + 256 * 8 * rounds - 1) / (256 * 8 * rounds);
+  if (per_wave <= 1) return launch_stream_nt<MT, 1, G, SD, ZEROS>(a, tiles, st);
+  if (per_wave == 2) return launch_stream_nt<MT, 2, G, SD, ZEROS>(a, tiles, st);
+  return launch_stream_nt<MT, 3, G, SD, ZEROS>(a, tiles, st);
+}
+
+template <int G, int SD, bool ZEROS>
+hipError_t pick(const Args& a, hipStream_t st) {
+  if (a.B <= 16 && a.K <= 8192) return pick_steps<1, G, SD, ZEROS>(a, st);
+  if (a.B <= 16) return launch_stream<1, G, SD, ZEROS>(a, st);
+  if (a.B <= 32) return launch_stream<2, G, SD, ZEROS>(a, st);
+  return launch_stream<4, G, SD, ZEROS>(a, st);
+}
+
 template <int G, int SD>
 hipError_t pick_zeros(const Args& a, hipStream_t st) {
-  return a.zeros ? pick_steps<1, G, SD, true>(a, st) : pick_steps<1, G, SD, false>(a, st);
+  return a.zeros ? pick<G, SD, true>(a, st) : pick<G, SD, false>(a, st);
 }
 template <int G>
 hipError_t pick_scale(const Args& a, hipStream_t st) {
@@ -351,18 +590,5 @@ hipError_t pick_scale(const Args& a, hipStream_t st) {
 }
 
 }  // namespace
-
-hipError_t launch_head(const Args& a, hipStream_t st) {
-  if (a.B <= 16 && a.K <= 8192) {
-    if (a.group == 128) return pick_scale<128>(a, st);
-    if (a.group == 64) return pick_scale<64>(a, st);
-    return pick_scale<32>(a, st);
-  }
-  const unsigned gx = (unsigned)((a.V + kBlock / 64 - 1) / (kBlock / 64));
-  const unsigned gy = (unsigned)(a.B < 64 ? a.B : 64);
-  hipLaunchKernelGGL(head_kernel, dim3(gx, gy), dim3(kBlock), 0, st, a);
-  return hipGetLastError();
-}
-
 }  // namespace head
 }  // namespace qs
