@@ -317,7 +317,8 @@ hipError_t pick_steps(const Args& a, hipStream_t st) {
 // ---------------------------------------------------------------------------
 
 constexpr int kChunkK = 2 * kStepK;      // columns per chunk: 128 bytes of codes a row
-constexpr int kMaxRows = 64;             // hidden rows per launch
+constexpr int kMaxRows = 64;             // hidden rows per workgroup
+constexpr int kStreamTiles = 3;          // most tiles a wave holds at once
 
 // More hidden rows, or rows too long for the registers: x passes through LDS in
 // chunks of 256 columns (two buffers, one barrier a chunk), already in the
@@ -327,21 +328,30 @@ constexpr int kMaxRows = 64;             // hidden rows per launch
 // values are requested while the chunk before is multiplied. With one
 // workgroup per compute unit the rows of a wave's tiles follow one another, so
 // x is read from L2 once per 8 NT tiles.
+template <int MT, int G, bool ZEROS>
+struct StreamLds {
+  static constexpr int GC = kChunkK / G;           // groups per chunk
+  static constexpr int kCodeStride = 128 + 16;     // bytes per row
+  static constexpr int kScaleStride = GC + 4;      // floats per row
+  uint4 x[2][8 * MT * 64];
+  f32x4 sum[2][GC][MT * 4];
+  u32x4 code[8][2][kCodeStride];                   // 16 rows each
+  float scale[8][kStreamTiles][16 * kScaleStride];
+  float off[ZEROS ? 8 : 1][ZEROS ? kStreamTiles : 1][ZEROS ? 16 * kScaleStride : 1];
+};
+
+// NT tiles of every wave, the workgroup's from tile `base` on, over all of k.
 template <int MT, int NT, int G, int SD, bool ZEROS>
-__global__ void __launch_bounds__(kThreads8, 2) head_stream_kernel(Args a, int chunks, int tiles) {
-  constexpr int GC = kChunkK / G;          // groups per chunk
+__device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZEROS>& lds, int chunks,
+                                             int base) {
+  using Lds = StreamLds<MT, G, ZEROS>;
+  constexpr int GC = Lds::GC;
   constexpr int SL = GC < 4 ? GC : 4;      // lanes per row of a scale load
   constexpr int EL = GC / SL;              // scales per lane
-  constexpr int kCodeStride = 128 + 16;    // bytes per row in LDS
-  constexpr int kScaleStride = GC + 4;     // floats per row in LDS
+  constexpr int kCodeStride = Lds::kCodeStride, kScaleStride = Lds::kScaleStride;
   constexpr int XI = MT;                   // 16-byte items of x per thread
   constexpr int kScaleSize = SD == QS_F32 ? 4 : 2;
   using Raw = std::conditional_t<SD == QS_F32, float, uint16_t>;
-  __shared__ uint4 s_x[2][8 * MT * 64];
-  __shared__ float s_sum[2][GC][MT * 16];
-  __shared__ __align__(16) uint8_t s_code[8][2][16 * kCodeStride];
-  __shared__ __align__(16) float s_scale[8][NT][16 * kScaleStride];
-  __shared__ __align__(16) float s_off[ZEROS ? 8 : 1][ZEROS ? NT : 1][ZEROS ? 16 * kScaleStride : 1];
   const int tid = threadIdx.x;
   const int w = uni(tid >> 6);
   const int lane = lane_id();
@@ -383,8 +393,9 @@ __global__ void __launch_bounds__(kThreads8, 2) head_stream_kernel(Args a, int c
       sum += __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(sum)));
       if constexpr (G >= 64) sum += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(sum)));
       if constexpr (G == 128) sum += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(sum)));
-      s_x[buf][place(xp, xj, i, xg, xm)] = ordered(xv[i]);
-      if ((xc & (G / 8 - 1)) == 0) s_sum[buf][xc / (G / 8)][xm + 16 * i] = ZEROS ? sum : -24.0f * sum;
+      lds.x[buf][place(xp, xj, i, xg, xm)] = ordered(xv[i]);
+      if ((xc & (G / 8 - 1)) == 0) reinterpret_cast<float*>(lds.sum[buf][xc / (G / 8)])[xm + 16 * i] =
+            ZEROS ? sum : -24.0f * sum;
     }
   };
 
@@ -392,184 +403,190 @@ __global__ void __launch_bounds__(kThreads8, 2) head_stream_kernel(Args a, int c
   const int g_row = min(lane / SL, 15), g_part = (lane % SL) * EL;
   const Pattern pattern;
 
-  for (int round = (int)blockIdx.x * 8 * NT; round < tiles; round += (int)gridDim.x * 8 * NT) {
-    const int first = round + w * NT;
-    u32x4 code[NT][2];
-    Raw scale[NT][EL];
-    uint8_t zero[NT][EL];
-    auto load_weights = [&](int chunk) {
-      const int k0 = chunk * kChunkK;
-      const bool c_in = k0 + c_part * 32 < a.K;
-      const int g = k0 / G, groups = min(GC, a.K / G - g);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        // past the last tile: the last row again, never stored
-        const int v0 = min((first + i) * 16, a.V - 1), rows = min(15, a.V - 1 - v0);
-        const uint8_t* const pc = a.codes + (size_t)v0 * a.codes_stride + (k0 >> 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = (uint32_t)min(h * 8 + c_row, rows) * (uint32_t)a.codes_stride +
-                              (uint32_t)c_part * 16u;
-          if (c_in) code[i][h] = *reinterpret_cast<const u32x4*>(pc + at);
-        }
-        const uint8_t* const ps = static_cast<const uint8_t*>(a.scales) +
-                                  ((size_t)v0 * a.scale_stride + g) * kScaleSize;
-        const uint32_t row = (uint32_t)min(g_row, rows);
-        const uint32_t at = (row * (uint32_t)a.scale_stride + (uint32_t)g_part) * kScaleSize;
-        const uint8_t* const pz = ZEROS ? a.zeros + (size_t)v0 * a.zero_stride + g : nullptr;
-        const uint32_t zat = row * (uint32_t)a.zero_stride + (uint32_t)g_part;
-        if (groups == GC) {
-          __builtin_memcpy(scale[i], ps + at, kScaleSize * EL);
-          if constexpr (ZEROS) __builtin_memcpy(zero[i], pz + zat, EL);
-        } else {
-#pragma unroll
-          for (int e = 0; e < EL; ++e) {
-            scale[i][e] = Raw(0);
-            zero[i][e] = 0;
-            if (g_part + e < groups) {
-              scale[i][e] = reinterpret_cast<const Raw*>(ps + at)[e];
-              if constexpr (ZEROS) zero[i][e] = pz[zat + e];
-            }
-          }
-        }
-      }
-    };
-
-    f32x4 y[NT][MT];
+  const int first = base + w * NT;
+  u32x4 code[NT][2];
+  Raw scale[NT][EL];
+  uint8_t zero[NT][EL];
+  auto load_weights = [&](int chunk) {
+    const int k0 = chunk * kChunkK;
+    const bool c_in = k0 + c_part * 32 < a.K;
+    const int g = k0 / G, groups = min(GC, a.K / G - g);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
+      // past the last tile: the last row again, never stored
+      const int v0 = min((first + i) * 16, a.V - 1), rows = min(15, a.V - 1 - v0);
+      const uint8_t* const pc = a.codes + (size_t)v0 * a.codes_stride + (k0 >> 1);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) y[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    __syncthreads();  // the round before has read its last chunk
-    load_x(0);
-    load_weights(0);
-    store_x(0);
-    if (chunks > 1) load_x(1);
-    for (int chunk = 0; chunk < chunks; ++chunk) {
-      const int buf = chunk & 1;
-      // this chunk's codes through LDS: from lanes along a row to the product's
-      uint32_t q[NT][8];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        uint8_t* const turn = s_code[w][i & 1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<u32x4*>(turn + (h * 8 + c_row) * kCodeStride + c_part * 16) = code[i][h];
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = (uint32_t)min(h * 8 + c_row, rows) * (uint32_t)a.codes_stride +
+                            (uint32_t)c_part * 16u;
+        if (c_in) code[i][h] = *reinterpret_cast<const u32x4*>(pc + at);
+      }
+      const uint8_t* const ps = static_cast<const uint8_t*>(a.scales) +
+                                ((size_t)v0 * a.scale_stride + g) * kScaleSize;
+      const uint32_t row = (uint32_t)min(g_row, rows);
+      const uint32_t at = (row * (uint32_t)a.scale_stride + (uint32_t)g_part) * kScaleSize;
+      const uint8_t* const pz = ZEROS ? a.zeros + (size_t)v0 * a.zero_stride + g : nullptr;
+      const uint32_t zat = row * (uint32_t)a.zero_stride + (uint32_t)g_part;
+      if (groups == GC) {
+        __builtin_memcpy(scale[i], ps + at, kScaleSize * EL);
+        if constexpr (ZEROS) __builtin_memcpy(zero[i], pz + zat, EL);
+      } else {
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
-          float sc;
-          if constexpr (SD == QS_F32) sc = scale[i][e];
-          else sc = __uint_as_float((uint32_t)scale[i][e] << 16);
-          s_scale[w][i][g_row * kScaleStride + g_part + e] = sc;
-          if constexpr (ZEROS)
-            s_off[w][i][g_row * kScaleStride + g_part + e] = -16.0f - (float)zero[i][e];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint8_t* const row = turn + n * kCodeStride + p * 64;
-          if constexpr (G == 128) {
-            *reinterpret_cast<u32x4*>(&q[i][p * 4]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
-          } else if constexpr (G == 64) {
-            *reinterpret_cast<uint2*>(&q[i][p * 4]) = *reinterpret_cast<const uint2*>(row + kg * 8);
-            *reinterpret_cast<uint2*>(&q[i][p * 4 + 2]) =
-                *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              q[i][p * 4 + j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
+          scale[i][e] = Raw(0);
+          zero[i][e] = 0;
+          if (g_part + e < groups) {
+            scale[i][e] = reinterpret_cast<const Raw*>(ps + at)[e];
+            if constexpr (ZEROS) zero[i][e] = pz[zat + e];
           }
         }
       }
-      __syncthreads();  // x of this chunk is in place, the other buffer is free
-      if (chunk + 1 < chunks) {
-        store_x(buf ^ 1);
-        load_weights(chunk + 1);
-        if (chunk + 2 < chunks) load_x(chunk + 2);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
 
+  f32x4 y[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) y[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  __syncthreads();  // the round before has read its last chunk
+  load_x(0);
+  load_weights(0);
+  store_x(0);
+  if (chunks > 1) load_x(1);
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int buf = chunk & 1;
+    // this chunk's codes through LDS: from lanes along a row to the product's
+    uint32_t q[NT][8];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      uint8_t* const turn = reinterpret_cast<uint8_t*>(lds.code[w][i & 1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4*>(turn + (h * 8 + c_row) * kCodeStride + c_part * 16) = code[i][h];
+#pragma unroll
+      for (int e = 0; e < EL; ++e) {
+        float sc;
+        if constexpr (SD == QS_F32) sc = scale[i][e];
+        else sc = __uint_as_float((uint32_t)scale[i][e] << 16);
+        lds.scale[w][i][g_row * kScaleStride + g_part + e] = sc;
+        if constexpr (ZEROS)
+          lds.off[w][i][g_row * kScaleStride + g_part + e] = -16.0f - (float)zero[i][e];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
+        const uint8_t* const row = turn + n * kCodeStride + p * 64;
+        if constexpr (G == 128) {
+          *reinterpret_cast<u32x4*>(&q[i][p * 4]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
+        } else if constexpr (G == 64) {
+          *reinterpret_cast<uint2*>(&q[i][p * 4]) = *reinterpret_cast<const uint2*>(row + kg * 8);
+          *reinterpret_cast<uint2*>(&q[i][p * 4 + 2]) =
+              *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
+        } else {
 #pragma unroll
-        for (int g = 0; g < GC / 2; ++g) {
-          constexpr int J = G / 32;
-          const int gi = p * (GC / 2) + g;
-          f32x4 acc[NT][MT];
+          for (int j = 0; j < 4; ++j)
+            q[i][p * 4 + j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
+        }
+      }
+    }
+    __syncthreads();  // x of this chunk is in place, the other buffer is free
+    if (chunk + 1 < chunks) {
+      store_x(buf ^ 1);
+      load_weights(chunk + 1);
+      if (chunk + 2 < chunks) load_x(chunk + 2);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+      for (int g = 0; g < GC / 2; ++g) {
+        constexpr int J = G / 32;
+        const int gi = p * (GC / 2) + g;
+        bf16x8 x[J][MT];
+        f32x4 sum[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          sum[t] = lds.sum[buf][gi][t * 4 + kg];
+#pragma unroll
+          for (int jj = 0; jj < J; ++jj)
+            x[jj][t] = __builtin_bit_cast(bf16x8, lds.x[buf][place(p, g * J + jj, t, kg, n)]);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float sc = lds.scale[w][i][n * kScaleStride + gi];
+          f32x4 acc[MT];
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            const f32x4 sum = *reinterpret_cast<const f32x4*>(&s_sum[buf][gi][t * 16 + kg * 4]);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              acc[i][t] = sum;
-              if constexpr (ZEROS) acc[i][t] *= s_off[w][i][n * kScaleStride + gi];
-            }
+            acc[t] = sum[t];
+            if constexpr (ZEROS) acc[t] *= lds.off[w][i][n * kScaleStride + gi];
           }
 #pragma unroll
           for (int jj = 0; jj < J; ++jj) {
-            const int j = g * J + jj;
-            bf16x8 x[MT];
+            const bf16x8 f = factors(q[i][p * 4 + g * J + jj], pattern);
 #pragma unroll
             for (int t = 0; t < MT; ++t)
-              x[t] = __builtin_bit_cast(bf16x8, s_x[buf][place(p, j, t, kg, n)]);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const bf16x8 f = factors(q[i][p * 4 + j], pattern);
-#pragma unroll
-              for (int t = 0; t < MT; ++t)
-                acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t], f, acc[i][t], 0, 0, 0);
-            }
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[jj][t], f, acc[t], 0, 0, 0);
           }
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const float sc = s_scale[w][i][n * kScaleStride + gi];
+          for (int t = 0; t < MT; ++t) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[i][t][e] += sc * acc[i][t][e];
-            }
+            for (int e = 0; e < 4; ++e) y[i][t][e] += sc * acc[t][e];
           }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        if (MT * NT > 6 && (g & 1)) __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
+  }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int v = (first + i) * 16 + n;
+  for (int i = 0; i < NT; ++i) {
+    const int v = (first + i) * 16 + n;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
+    for (int t = 0; t < MT; ++t) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = t * 16 + kg * 4 + e;
-          if (v < a.V && m < rows_x) store_logit(a, row0 + m, v, y[i][t][e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int m = t * 16 + kg * 4 + e;
+        if (v < a.V && m < rows_x) store_logit(a, row0 + m, v, y[i][t][e]);
       }
     }
   }
 }
 
-template <int MT, int NT, int G, int SD, bool ZEROS>
-hipError_t launch_stream_nt(const Args& a, int tiles, hipStream_t st) {
-  const int chunks = (a.K + kChunkK - 1) / kChunkK;
-  const int grid = min(256, (tiles + 8 * NT - 1) / (8 * NT));
-  const int blocks = (a.B + kMaxRows - 1) / kMaxRows;
-  hipLaunchKernelGGL((head_stream_kernel<MT, NT, G, SD, ZEROS>),
-                     dim3((unsigned)grid, (unsigned)blocks), dim3(kThreads8), 0, st, a, chunks,
-                     tiles);
-  return hipGetLastError();
+// A workgroup has `full` * NT + REST tiles for each of its waves.
+template <int MT, int NT, int REST, int G, int SD, bool ZEROS>
+__global__ void __launch_bounds__(kThreads8, 2)
+    head_stream_kernel(Args a, int chunks, int full) {
+  __shared__ StreamLds<MT, G, ZEROS> lds;
+  int base = (int)blockIdx.x * 8 * (full * NT + REST);
+  for (int i = 0; i < full; ++i, base += 8 * NT)
+    stream_tiles<MT, NT, G, SD, ZEROS>(a, lds, chunks, base);
+  if constexpr (REST > 0) stream_tiles<MT, REST, G, SD, ZEROS>(a, lds, chunks, base);
 }
 
 template <int MT, int G, int SD, bool ZEROS>
 hipError_t launch_stream(const Args& a, hipStream_t st) {
+  const int chunks = (a.K + kChunkK - 1) / kChunkK;
   const int tiles = (a.V + 15) / 16;
-  // the fewest rounds of at most 3 tiles a wave over 256 workgroups, evenly
-  const int rounds = (tiles + 256 * 8 * 3 - 1) / (256 * 8 * 3);
-  const int per_wave = (tiles + 256 * 8 * rounds - 1) / (256 * 8 * rounds);
-  if (per_wave <= 1) return launch_stream_nt<MT, 1, G, SD, ZEROS>(a, tiles, st);
-  if (per_wave == 2) return launch_stream_nt<MT, 2, G, SD, ZEROS>(a, tiles, st);
-  return launch_stream_nt<MT, 3, G, SD, ZEROS>(a, tiles, st);
+  // the same number of tiles for every wave of (at most) one workgroup per
+  // compute unit
+  const int per_wave = (tiles + 256 * 8 - 1) / (256 * 8);
+  const int grid = (tiles + 8 * per_wave - 1) / (8 * per_wave);
+  const int blocks = (a.B + kMaxRows - 1) / kMaxRows;
+  auto run = [&](auto* kernel, int full) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid, (unsigned)blocks), dim3(kThreads8), 0, st, a,
+                       chunks, full);
+    return hipGetLastError();
+  };
+  if (per_wave == 1) return run(head_stream_kernel<MT, 1, 0, G, SD, ZEROS>, 1);
+  if (per_wave == 2) return run(head_stream_kernel<MT, 2, 0, G, SD, ZEROS>, 1);
+  if (per_wave % 3 == 0) return run(head_stream_kernel<MT, 3, 0, G, SD, ZEROS>, per_wave / 3);
+  if (per_wave % 3 == 1) return run(head_stream_kernel<MT, 3, 1, G, SD, ZEROS>, per_wave / 3);
+  return run(head_stream_kernel<MT, 3, 2, G, SD, ZEROS>, per_wave / 3);
 }
 
 template <int G, int SD, bool ZEROS>
