@@ -10,10 +10,14 @@
 // The logits are read once. A workgroup holds its share of a row in registers
 // (NL 16-byte loads per lane, all requested before the first is used), so the
 // maximum comes first and every exponential is taken once against it: no
-// rescaling. Each wave uses its own maximum and the waves' (m, S, E) triples
+// rescaling. Each wave uses its own maximum m_w and, for one operation per
+// token, the rounded product k_w = fl(m_w c), c = log2(e) / T, as its reference:
+// with 2^(z c - k_w) from one fused multiply-add the sums are off by the common
+// factor 2^(m_w c - k_w) alone, which one more gives exactly. (Where m_w c leaves
+// float32's comfortable range the difference comes first.) The waves' (m, S, E)
 // are joined as
-//   S = sum_w S_w f_w,  E = sum_w f_w (E_w + S_w (m_w - m) / T),
-//   f_w = exp((m_w - m) / T).
+//   S = sum_w S_w f_w,  E = sum_w f_w (E_w + S_w (m_w - m) c),
+//   f_w = 2^((m_w - m) c).
 // Weights and E are kept in units of log 2 (one hardware exponential each).
 //
 // Rows of up to kRowBlock * 8 loads go to one workgroup and one launch: a second
@@ -25,7 +29,8 @@
 // Top tokens: with t the n-th largest of the maxima of 256 groups of lanes, n
 // tokens (one of each of n groups) reach t, so the n largest tokens lie among
 // those with z >= t. These are few (a little over n unless values repeat);
-// they are collected and ranked. Keys
+// the lanes whose maximum reaches t (again few) are noted, all threads search
+// their tokens, read again from the caches, and what is found is ranked. Keys
 // (z's order-preserving bits << 32 | ~id) are distinct. Where more than the
 // list holds reach t (long runs of equal values) the workgroup takes its n
 // largest keys one after another instead.
@@ -43,6 +48,7 @@ namespace {
 
 constexpr int kPartBlock = 256;   // threads of a part's workgroup
 constexpr int kPartLoads = 16;    // 16-byte loads per lane
+constexpr int kShortLoads = 8;    // the same where parts are few
 constexpr int kRowBlock = 1024;   // threads of a whole row's workgroup
 constexpr int kRowLoads = 8;
 constexpr int kSmallBlock = 256;  // threads of a short row's workgroup
@@ -66,10 +72,19 @@ static_assert(sizeof(Part) == 32, "two 16-byte stores");
 
 template <int DT> constexpr int kPer = DT == QS_F32 ? 4 : 8;  // tokens per 16-byte load
 
-int64_t parts_for(int64_t V, int dtype) {
-  const int64_t per = dtype == QS_F32 ? 4 : 8;
-  if (V <= per * kRowBlock * kRowLoads) return 1;
-  return (V + per * kPartBlock * kPartLoads - 1) / (per * kPartBlock * kPartLoads);
+// Loads per lane of a part: the long parts' workgroups are more than kFewParts
+// (eight per compute unit), or else the row is cut into twice as many.
+constexpr int64_t kFewParts = 2048;
+int64_t parts_of(int64_t V, int dtype, int loads) {
+  const int64_t n = (int64_t)(dtype == QS_F32 ? 4 : 8) * kPartBlock * loads;
+  return (V + n - 1) / n;
+}
+int loads_for(int64_t B, int64_t V, int dtype) {
+  return B * parts_of(V, dtype, kPartLoads) > kFewParts ? kPartLoads : kShortLoads;
+}
+int64_t parts_for(int64_t B, int64_t V, int dtype) {
+  if (V <= (int64_t)(dtype == QS_F32 ? 4 : 8) * kRowBlock * kRowLoads) return 1;
+  return parts_of(V, dtype, loads_for(B, V, dtype));
 }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -117,40 +132,63 @@ __device__ __forceinline__ float token(const uint4& v, int e) {
   return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
 }
 
-// The same for an index known only at run time.
-template <int DT>
-__device__ __forceinline__ float token_at(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3,
-                                          int e) {
-  const int d = DT == QS_F32 ? e : e >> 1;
-  const uint32_t lo = d & 1 ? w1 : w0, hi = d & 1 ? w3 : w2;
-  const uint32_t w = d & 2 ? hi : lo;
-  if constexpr (DT == QS_F32) return __uint_as_float(w);
-  return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
-}
-
 template <int DT>
 __device__ __forceinline__ float logit_at(const uint8_t* row, int i) {
   if constexpr (DT == QS_F32) return reinterpret_cast<const float*>(row)[i];
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
 }
 
-// Tokens whose bit in `bits` is 0 become -inf.
+// Masks of a 16-byte load's registers: all ones where the token's bit is set.
 template <int DT>
-__device__ __forceinline__ uint4 blank(uint4 v, uint32_t bits) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ uint4 masks_of(uint32_t bits) {
+  uint32_t w[4];
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
     if constexpr (DT == QS_F32) {
-      const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)bits, d, 1);
-      w[d] = bfi(keep, w[d], 0xFF800000u);
+      w[d] = (uint32_t)__builtin_amdgcn_sbfe((int)bits, d, 1);
     } else {
       const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe((int)bits, 2 * d, 1);
       const uint32_t hi = (uint32_t)__builtin_amdgcn_sbfe((int)bits, 2 * d + 1, 1);
-      w[d] = bfi(bfi(0xFFFFu, lo, hi), w[d], 0xFF80FF80u);
+      w[d] = bfi(0xFFFFu, lo, hi);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Tokens outside the masks become -inf.
+template <int DT>
+__device__ __forceinline__ uint4 blank(const uint4& v, const uint4& keep) {
+  constexpr uint32_t kFill = DT == QS_F32 ? 0xFF800000u : 0xFF80FF80u;
+  return make_uint4(bfi(keep.x, v.x, kFill), bfi(keep.y, v.y, kFill), bfi(keep.z, v.z, kFill),
+                    bfi(keep.w, v.w, kFill));
+}
+// The largest of the tokens a lane has seen. bf16 tokens are compared two at a
+// time as whole numbers: among those with a clear sign the larger signed number
+// is the larger token, among the others the smaller unsigned one.
+template <int DT> struct Largest;
+template <> struct Largest<QS_F32> {
+  float m = -INFINITY;
+  __device__ __forceinline__ void add(const uint4& v) {
+    m = fmaxf(fmaxf(m, __uint_as_float(v.x)), __uint_as_float(v.y));
+    m = fmaxf(fmaxf(m, __uint_as_float(v.z)), __uint_as_float(v.w));
+  }
+  __device__ __forceinline__ float value() const { return m; }
+};
+template <> struct Largest<QS_BF16> {
+  uint32_t above = 0x80008000u, below = 0xFFFFFFFFu;
+  __device__ __forceinline__ void add(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      above = bits_of(__builtin_elementwise_max(as_s2(above), as_s2(w[d])));
+      below = bits_of(__builtin_elementwise_min(as_u2(below), as_u2(w[d])));
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    const int hi = max((int)above >> 16, (int)(above << 16) >> 16);
+    const uint32_t lo = min(below >> 16, below & 0xFFFFu);
+    return __uint_as_float((hi >= 0 ? (uint32_t)hi : lo) << 16);
+  }
+};
 
 // Keeps the compiler from holding a load's unpacked tokens from one pass over
 // the registers to the next (unpacking again costs less than the registers).
@@ -182,28 +220,50 @@ struct Shared {
   float m[kRowBlock / 64], S[kRowBlock / 64], E[kRowBlock / 64];
   uint32_t any[kRowBlock / 64];
   uint64_t best[kRowBlock / 64];
+  uint16_t lanes[kRowBlock];  // threads whose maximum reaches t
+  int n_lanes;
   int count;
 };
 
+// The given token of slot `tid` and its logit, requested before the row is.
+struct Given {
+  int token;
+  float z;
+  bool legal;
+};
+template <int DT>
+__device__ __forceinline__ Given load_given(const Args& a, int r, int g) {
+  Given v{-1, 0.0f, false};
+  if (g < a.G) {
+    v.token = a.tokens[(size_t)r * a.G + g];
+    if (v.token >= 0 && v.token < a.V) {
+      v.z = logit_at<DT>(a.logits + (size_t)r * a.row_bytes, v.token);
+      v.legal = a.bitmask == nullptr ||
+                ((a.bitmask[(size_t)r * a.bm_stride + (v.token >> 5)] >> (v.token & 31)) & 1u);
+    }
+  }
+  return v;
+}
+
 // Writes one row's outputs; called by every thread of a workgroup of `threads`,
-// with the row's joined statistics and (top_n > 0) `n_list` distinct keys in
-// LDS that hold its top tokens.
+// with the row's joined statistics, the thread's slot, and (top_n > 0) `n_list`
+// distinct keys in LDS that hold its top tokens.
 template <int DT>
 __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int threads, float m,
-                                           float S, float E, bool any, float T,
+                                           float S, float E, bool any, float T, Given given,
                                            const uint64_t* list, int n_list) {
-  const uint8_t* row = a.logits + (size_t)r * a.row_bytes;
-  const uint32_t* bm = a.bitmask ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
-  const int32_t* tokens = a.tokens + (size_t)r * a.G;
   float* const lps = a.logprobs + (size_t)r * a.G;
-  int bad = 0;
-  for (int g = tid; g < a.G; g += threads) bad |= tokens[g] < -1 || tokens[g] >= a.V;
+  int bad = given.token < -1 || given.token >= a.V;
+  for (int g = tid + threads; g < a.G; g += threads) {
+    const int t = a.tokens[(size_t)r * a.G + g];
+    bad |= t < -1 || t >= a.V;
+  }
   if (threads > 64) bad = __syncthreads_or(bad);
   else bad = ballot(bad) != 0;
   int status = QS_ROW_OK;
   if (bad || !(T > 0.0f) || T == INFINITY) status = QS_ROW_BAD_PARAM;
   else if (!any) status = QS_ROW_EMPTY;
-  else if (S != S) status = QS_ROW_NONFINITE;
+  else if (!(S < INFINITY)) status = QS_ROW_NONFINITE;
   else if (S == 0.0f) status = QS_ROW_ALL_NEG_INF;
   const bool ok = status == QS_ROW_OK;
   const float log_sum = ok ? logf(S) : NAN;
@@ -214,12 +274,10 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int th
     if (a.entropy) a.entropy[r] = ok ? log_sum - kLn2 * (E / S) : NAN;
   }
   for (int g = tid; g < a.G; g += threads) {
-    const int t = tokens[g];
+    if (g != tid) given = load_given<DT>(a, r, g);
     float lp = ok ? -INFINITY : NAN;
-    if (t == -1) lp = 0.0f;
-    else if (ok && (bm == nullptr || ((bm[t >> 5] >> (t & 31)) & 1u))) {
-      lp = (logit_at<DT>(row, t) - m) / T - log_sum;
-    }
+    if (given.token == -1) lp = 0.0f;
+    else if (ok && given.legal) lp = (given.z - m) / T - log_sum;
     lps[g] = lp;
   }
   if (a.top_n == 0) return;
@@ -247,7 +305,9 @@ __global__ void __launch_bounds__(THREADS)
     score_kernel(Args a, int parts, int part_loads, Part* ws_parts, uint64_t* ws_list) {
   constexpr int kWavesHere = THREADS / 64;
   constexpr int P = kPer<DT>;
+  constexpr bool kTable = MASK && DT == QS_BF16;
   __shared__ Shared s;
+  __shared__ uint4 s_masks[kTable ? 256 : 1];  // masks_of every byte of legal bits
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int w = tid >> 6;
@@ -255,6 +315,9 @@ __global__ void __launch_bounds__(THREADS)
   const int part = ROW ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)parts);
   const int begin = part * part_loads * THREADS * P;  // first token of this workgroup
   const uint8_t* row = a.logits + (size_t)r * a.row_bytes;
+  const uint8_t* mask_row = reinterpret_cast<const uint8_t*>(a.bitmask + (size_t)r * a.bm_stride);
+  Given given{-1, 0.0f, false};
+  if constexpr (ROW) given = load_given<DT>(a, r, tid);
   const float T = a.T ? a.T[r] : 1.0f;
   const float c = scale_of(T);
 
@@ -271,29 +334,34 @@ __global__ void __launch_bounds__(THREADS)
     if (u < part_loads && i < a.V) {
       v[u] = *reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P));
       legal[u] = 0xFFu;
-      if constexpr (MASK)
-        legal[u] = reinterpret_cast<const uint8_t*>(a.bitmask + (size_t)r * a.bm_stride)[i >> 3];
+      if constexpr (MASK) legal[u] = mask_row[i >> 3];
     }
   }
-  if (TOP && tid == 0) s.count = 0;
+  // a load's legal bits: the bitmask's, none past the row's end
+  auto bits_at = [&](int i, uint32_t bits) {
+    if constexpr (P == 4) bits = MASK ? bits >> (i & 4) : bits;
+    const int left = a.V - i;
+    return bits & (left >= P ? (1u << P) - 1u : left > 0 ? (1u << left) - 1u : 0u);
+  };
+  if (TOP && tid == 0) s.count = s.n_lanes = 0;
+  if constexpr (kTable) {
+    for (int k = tid; k < 256; k += THREADS) s_masks[k] = masks_of<DT>((uint32_t)k);
+    __syncthreads();
+  }
 
   // largest legal token of the lane; illegal ones become -inf
-  float m = -3.402823466e38f;
+  Largest<DT> largest;
   uint32_t any = 0u;
 #pragma unroll
   for (int u = 0; u < NL; ++u) {
-    const int i = begin + (u * THREADS + tid) * P;
-    uint32_t bits = legal[u];
-    if constexpr (P == 4) bits = MASK ? bits >> (i & 4) : bits;
-    const int left = a.V - i;
-    bits &= left >= P ? (1u << P) - 1u : left > 0 ? (1u << left) - 1u : 0u;
+    const uint32_t bits = bits_at(begin + (u * THREADS + tid) * P, legal[u]);
     any |= bits;
-    v[u] = blank<DT>(v[u], bits);
-#pragma unroll
-    for (int e = 0; e < P; ++e) m = fmaxf(m, token<DT>(v[u], e));
+    if constexpr (kTable) v[u] = blank<DT>(v[u], s_masks[bits]);
+    else if (MASK || bits != (1u << P) - 1u) v[u] = blank<DT>(v[u], masks_of<DT>(bits));
+    largest.add(v[u]);
   }
-  const float lane_max = m;
-  const float wave_max = wave_max_f32(m);
+  const float lane_max = fmaxf(largest.value(), -3.402823466e38f);
+  const float wave_max = wave_max_f32(lane_max);
   if constexpr (TOP) {
     static_assert(THREADS == kGroups || THREADS == 4 * kGroups, "groups of 1 or 4 lanes");
     uint32_t* const group = reinterpret_cast<uint32_t*>(s.group);
@@ -308,15 +376,36 @@ __global__ void __launch_bounds__(THREADS)
 
   // the wave's sums against its own maximum
   float S[2] = {0.0f, 0.0f}, E[2] = {0.0f, 0.0f};
+  const float k = wave_max * c;
+  if (fabsf(k) < 1e30f && c < 1e30f) {
 #pragma unroll
-  for (int u = 0; u < NL; ++u) {
-    opaque(v[u]);
+    for (int u = 0; u < NL; ++u) {
+      opaque(v[u]);
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      const float d = (token<DT>(v[u], e) - wave_max) * c;
-      const float x = exp2_hw(d);
-      S[e & 1] += x;
-      E[e & 1] += x * fmaxf(d, -200.0f);  // not 0 times -inf
+      for (int e = 0; e < P; ++e) {
+        const float d = fmaf(token<DT>(v[u], e), c, -k);
+        const float x = exp2_hw(d);
+        S[e & 1] += x;
+        E[e & 1] = fmaf(x, fmaxf(d, -200.0f), E[e & 1]);  // not 0 times -inf
+      }
+    }
+    const float over = fmaf(wave_max, c, -k), f = exp2_hw(-over);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      E[e] = f * (E[e] - over * S[e]);
+      S[e] *= f;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < NL; ++u) {
+      opaque(v[u]);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const float d = (token<DT>(v[u], e) - wave_max) * c;
+        const float x = exp2_hw(d);
+        S[e & 1] += x;
+        E[e & 1] = fmaf(x, fmaxf(d, -200.0f), E[e & 1]);
+      }
     }
   }
   const float Sw = wave_sum_f32(S[0] + S[1]);
@@ -351,26 +440,25 @@ __global__ void __launch_bounds__(THREADS)
     // finite tokens only: keys above -inf's (groups without one hold the key of
     // -FLT_MAX, the lowest of those)
     t = max(wave_nth_high16(s.group[lane], a.top_n), Keys<QS_F32>::kNegInf + 1u);
-    if (key_of(lane_max) >= t) {
-      const float tz = Keys<QS_F32>::value(t);
-      static_for<0, NL>([&](auto U) {
-        constexpr int u = decltype(U)::value;
-        opaque(v[u]);
-        float z = token<DT>(v[u], 0);
+    if (key_of(lane_max) >= t) s.lanes[atomicAdd(&s.n_lanes, 1)] = (uint16_t)tid;
+    __syncthreads();
+    const float tz = Keys<QS_F32>::value(t);
+    const int chunks = s.n_lanes * part_loads;
+    for (int j = tid; j < chunks; j += THREADS) {
+      const int l = (int)((unsigned)j / (unsigned)part_loads), u = j - l * part_loads;
+      const int i = begin + (u * THREADS + s.lanes[l]) * P;
+      if (i >= a.V) continue;
+      const uint32_t bits = bits_at(i, MASK ? mask_row[i >> 3] : 0xFFu);
+      const uint4 q = blank<DT>(*reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P)),
+                                masks_of<DT>(bits));
 #pragma unroll
-        for (int e = 1; e < P; ++e) z = fmaxf(z, token<DT>(v[u], e));
+      for (int e = 0; e < P; ++e) {
+        const float z = token<DT>(q, e);
         if (z >= tz) {
-#pragma unroll 1
-          for (int e = 0; e < P; ++e) {
-            z = token_at<DT>(v[u].x, v[u].y, v[u].z, v[u].w, e);
-            if (z >= tz) {
-              const int at = atomicAdd(&s.count, 1);
-              const int i = begin + (u * THREADS + tid) * P + e;
-              if (at < kListCap) s.list[at] = ((uint64_t)key_of(z) << 32) | (uint32_t)~i;
-            }
-          }
+          const int at = atomicAdd(&s.count, 1);
+          if (at < kListCap) s.list[at] = ((uint64_t)key_of(z) << 32) | (uint32_t)~(i + e);
         }
-      });
+      }
     }
     __syncthreads();
     n_list = s.count;
@@ -406,7 +494,7 @@ __global__ void __launch_bounds__(THREADS)
     }
   }
   if constexpr (ROW) {
-    finish_row<DT>(a, r, tid, THREADS, top, S_all, E_all, any_all, T, s.list, n_list);
+    finish_row<DT>(a, r, tid, THREADS, top, S_all, E_all, any_all, T, given, s.list, n_list);
   } else {
     const size_t p = (size_t)r * parts + part;
     if (tid == 0) {
@@ -438,6 +526,19 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const Part* p = ws_parts + (size_t)r * parts;
+  // requests that need nothing else first: the thread's slot, and the first 64
+  // keys of 4 lists per wave whatever their counts
+  const Given given = load_given<DT>(a, r, tid);
+  const uint64_t* const list = ws_list + (size_t)r * parts * kListCap;
+  constexpr int kAhead = 4;
+  uint64_t ahead[kAhead];
+  if constexpr (TOP) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = (tid >> 6) + j * (kThreadsHere / 64);
+      ahead[j] = k < parts ? list[(size_t)k * kListCap + lane] : 0u;
+    }
+  }
   const float T = a.T ? a.T[r] : 1.0f;
   const float c = scale_of(T);
   // every wave joins all parts (the same values in every thread)
@@ -465,16 +566,20 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
     // the row's n-th largest token is at or above every part's t
     if (tid == 0) s_count = 0;
     __syncthreads();
-    const uint64_t* list = ws_list + (size_t)r * parts * kListCap;
-    for (int k = tid >> 6; k < parts; k += kThreadsHere / 64) {
-      const int n = p[k].count;
-      for (int i = lane; i < n; i += 64) {
-        const uint64_t key = list[(size_t)k * kListCap + i];
-        if ((uint32_t)(key >> 32) >= t) {
-          const int at = atomicAdd(&s_count, 1);
-          if (at < kJoinCap) s_list[at] = key;
-        }
+    auto add = [&](uint64_t key) {
+      if ((uint32_t)(key >> 32) >= t) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kJoinCap) s_list[at] = key;
       }
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = (tid >> 6) + j * (kThreadsHere / 64);
+      if (k < parts && lane < p[k].count) add(ahead[j]);
+    }
+    for (int j = 0, k = tid >> 6; k < parts; ++j, k += kThreadsHere / 64) {
+      const int n = p[k].count;
+      for (int i = lane + (j < kAhead ? 64 : 0); i < n; i += 64) add(list[(size_t)k * kListCap + i]);
     }
     __syncthreads();
     n_list = s_count;
@@ -508,7 +613,7 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
       __syncthreads();
     }
   }
-  finish_row<DT>(a, r, tid, kThreadsHere, m, S, E, any_all, T, s_list, n_list);
+  finish_row<DT>(a, r, tid, kThreadsHere, m, S, E, any_all, T, given, s_list, n_list);
 }
 
 template <int DT, int THREADS, int NL, bool ROW>
@@ -547,8 +652,11 @@ hipError_t launch_dt(const Args& a, int B, int parts, uint8_t* ws, hipStream_t s
       reinterpret_cast<uint64_t*>(ws + align256((size_t)B * parts * sizeof(Part)));
   // parts of equal length, in whole loads
   const int loads = (a.V + kPartBlock * P - 1) / (kPartBlock * P);
-  launch<DT, kPartBlock, kPartLoads, false>(a, B * parts, parts, (loads + parts - 1) / parts, wp,
-                                            wl, st);
+  const int each = (loads + parts - 1) / parts;
+  if (loads_for(B, a.V, DT) == kPartLoads)
+    launch<DT, kPartBlock, kPartLoads, false>(a, B * parts, parts, each, wp, wl, st);
+  else
+    launch<DT, kPartBlock, kShortLoads, false>(a, B * parts, parts, each, wp, wl, st);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (a.top_n > 0)
     hipLaunchKernelGGL((join_kernel<DT, true>), dim3((unsigned)B), dim3(256), 0, st, a, parts, wp,
@@ -562,18 +670,18 @@ hipError_t launch_dt(const Args& a, int B, int parts, uint8_t* ws, hipStream_t s
 }  // namespace
 
 size_t workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n) {
-  const int64_t parts = parts_for(V, dtype);
+  const int64_t parts = parts_for(B, V, dtype);
   if (parts == 1) return 0;
   const size_t n = (size_t)B * parts;
   return align256(n * sizeof(Part)) + (top_n > 0 ? n * kListCap * sizeof(uint64_t) : 0);
 }
 
 bool grid_fits(int64_t B, int64_t V, int dtype) {
-  return B * parts_for(V, dtype) * kPartBlock < (int64_t)1 << 32;
+  return B * parts_for(B, V, dtype) * kPartBlock < (int64_t)1 << 32;
 }
 
 hipError_t launch_score(const Args& a, int dtype, int B, void* workspace, hipStream_t st) {
-  const int parts = (int)parts_for(a.V, dtype);
+  const int parts = (int)parts_for(B, a.V, dtype);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   return dtype == QS_F32 ? launch_dt<QS_F32>(a, B, parts, ws, st)
                          : launch_dt<QS_BF16>(a, B, parts, ws, st);
