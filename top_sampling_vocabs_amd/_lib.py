@@ -6,6 +6,7 @@ sampling runs in the HIP kernels; there is no CPU or torch fallback. If the
 library is missing the first call raises.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -537,36 +538,47 @@ def top_logprobs(cand_ids, cand_probs, cand_count, n):
     return ids, lp, status
 
 
+def _addr(t):
+    """A tensor's address as a C argument (an int; None is NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def _on(device):
     """Context in which `device` is the current one (kernels launch there)."""
-    import contextlib
-
     import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _SAME_DEVICE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
-def _check_same_device(device, **tensors):
-    for name, t in tensors.items():
+def _raw_stream(device):
+    """The handle of the device's current torch stream, without a Stream object."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _check_same_device(device, tensors):
+    for name, t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _check_tokens(tokens, B, device):
-    """tokens as a contiguous [B, G] view."""
+    """The number of slots per row of tokens [B] or [B, G]."""
     import torch
     if tokens.dtype != torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != B \
             or tokens.device != device or not tokens.is_contiguous():
         raise ValueError(f"tokens must be a contiguous int32 tensor [B] or [B, G] on {device}")
-    return tokens if tokens.dim() == 2 else tokens.view(B, 1)
+    return tokens.shape[1] if tokens.dim() == 2 else 1
 
 
 def _padded_rows(B, V, dtype, device):
     """[B, V] uninitialised, rows starting 16 bytes aligned."""
     import torch
-    step = 4 if dtype == torch.float32 else 8
-    return torch.empty((B, -(-V // step) * step), dtype=dtype, device=device)[:, :V]
+    over = -V % (4 if dtype == torch.float32 else 8)
+    t = torch.empty((B, V + over), dtype=dtype, device=device)
+    return t[:, :V] if over else t
 
 
 def token_logprobs_workspace_for(logits, top_n=0):
@@ -593,49 +605,52 @@ def token_logprobs(logits, tokens, *, temperature=None, bitmask=None, entropy=Fa
     only; a second derivative is not available).
     """
     import torch
-    lib = load()
-    if logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor [B, V] with unit column stride")
-    _check_same_device(logits.device, temperature=temperature, bitmask=bitmask,
-                       workspace=workspace)
     B, V = _check_logits(logits, bitmask)
-    _check_tokens(tokens, B, logits.device)
+    dev = logits.device
+    _check_same_device(dev, (("temperature", temperature), ("bitmask", bitmask),
+                             ("workspace", workspace)))
+    G = _check_tokens(tokens, B, dev)
     if temperature is not None:
         _check_rowvec(temperature, B, torch.float32, "temperature")
-    if torch.is_grad_enabled() and logits.requires_grad:
-        keys, *out = _token_logprobs_autograd().apply(logits, tokens, temperature, bitmask,
+    if logits.requires_grad and torch.is_grad_enabled():
+        keys, *out = _token_logprobs_autograd().apply(logits, tokens, temperature, bitmask, G,
                                                       bool(entropy), int(top_n), workspace)
         return dict(zip(keys, out))
-    return _token_logprobs(lib, logits.detach(), tokens, temperature, bitmask, entropy, top_n,
-                           workspace)
+    return _token_logprobs(logits, tokens, temperature, bitmask, G, entropy, top_n, workspace)
 
 
-def _token_logprobs(lib, logits, tokens, temperature, bitmask, entropy, top_n, workspace):
+def _token_logprobs(logits, tokens, temperature, bitmask, G, entropy, top_n, workspace):
     import torch
+    lib = load()
     B, V = logits.shape
     dev = logits.device
-    tok = _check_tokens(tokens, B, dev)
-    out = {"logprobs": torch.empty(tokens.shape, dtype=torch.float32, device=dev),
-           "row_max": torch.empty(B, dtype=torch.float32, device=dev),
-           "log_sum": torch.empty(B, dtype=torch.float32, device=dev),
-           "status": torch.empty(B, dtype=torch.int32, device=dev)}
+    code = _dtype_code(logits)
+    lps = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    # the values per row in one allocation
+    row_max, log_sum, status, *ent = torch.empty((4 if entropy else 3, B), dtype=torch.float32,
+                                                 device=dev).unbind(0)
+    status = status.view(torch.int32)
+    out = {"logprobs": lps, "row_max": row_max, "log_sum": log_sum, "status": status}
     if entropy:
-        out["entropy"] = torch.empty(B, dtype=torch.float32, device=dev)
+        out["entropy"] = ent[0]
+    ids = tops = None
     if top_n:
-        out["top_ids"] = torch.empty((B, top_n), dtype=torch.int32, device=dev)
-        out["top_logprobs"] = torch.empty((B, top_n), dtype=torch.float32, device=dev)
+        out["top_ids"] = ids = torch.empty((B, top_n), dtype=torch.int32, device=dev)
+        out["top_logprobs"] = tops = torch.empty((B, top_n), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = token_logprobs_workspace_for(logits, top_n)
+        n = lib.qs_token_logprobs_workspace_bytes(B, V, code, top_n)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     with _on(dev):
         rc = lib.qs_token_logprobs(
-            _ptr(logits), _dtype_code(logits), B, V, logits.stride(0), _ptr(temperature),
-            _ptr(bitmask), 0 if bitmask is None else bitmask.stride(0), _ptr(tok), tok.shape[1],
-            _ptr(out["logprobs"]), _ptr(out["row_max"]), _ptr(out["log_sum"]),
-            _ptr(out.get("entropy")), int(top_n), _ptr(out.get("top_ids")),
-            _ptr(out.get("top_logprobs")), _ptr(out["status"]), _ptr(workspace),
+            logits.data_ptr(), code, B, V, logits.stride(0), _addr(temperature), _addr(bitmask),
+            0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G, lps.data_ptr(),
+            row_max.data_ptr(), log_sum.data_ptr(), ent[0].data_ptr() if entropy else None,
+            top_n, _addr(ids), _addr(tops), status.data_ptr(), _addr(workspace),
             0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(dev))
-    _status(rc, "qs_token_logprobs")
+            _raw_stream(dev))
+    if rc:
+        _status(rc, "qs_token_logprobs")
     return out
 
 
@@ -652,14 +667,13 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
     """
     import torch
     lib = load()
-    if logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor [B, V] with unit column stride")
-    dev = logits.device
-    _check_same_device(dev, temperature=temperature, bitmask=bitmask, row_max=row_max,
-                       log_sum=log_sum, status=status, grad_logprobs=grad_logprobs,
-                       entropy=entropy, grad_entropy=grad_entropy, out=out)
     B, V = _check_logits(logits, bitmask)
-    tok = _check_tokens(tokens, B, dev)
+    dev = logits.device
+    _check_same_device(dev, (("temperature", temperature), ("bitmask", bitmask),
+                             ("row_max", row_max), ("log_sum", log_sum), ("status", status),
+                             ("grad_logprobs", grad_logprobs), ("entropy", entropy),
+                             ("grad_entropy", grad_entropy), ("out", out)))
+    G = _check_tokens(tokens, B, dev)
     if temperature is not None:
         _check_rowvec(temperature, B, torch.float32, "temperature")
     _check_rowvec(row_max, B, torch.float32, "row_max")
@@ -679,11 +693,12 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
         raise ValueError("out must have the logits' shape and dtype and unit column stride")
     with _on(dev):
         rc = lib.qs_token_logprobs_backward(
-            _ptr(logits), _dtype_code(logits), B, V, logits.stride(0), _ptr(temperature),
-            _ptr(bitmask), 0 if bitmask is None else bitmask.stride(0), _ptr(tok), tok.shape[1],
-            _ptr(row_max), _ptr(log_sum), _ptr(status), _ptr(grad_logprobs), _ptr(entropy),
-            _ptr(grad_entropy), _ptr(out), out.stride(0), _stream(dev))
-    _status(rc, "qs_token_logprobs_backward")
+            logits.data_ptr(), _dtype_code(logits), B, V, logits.stride(0), _addr(temperature),
+            _addr(bitmask), 0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G,
+            row_max.data_ptr(), log_sum.data_ptr(), status.data_ptr(), grad_logprobs.data_ptr(),
+            _addr(entropy), _addr(grad_entropy), out.data_ptr(), out.stride(0), _raw_stream(dev))
+    if rc:
+        _status(rc, "qs_token_logprobs_backward")
     return out
 
 
@@ -700,8 +715,8 @@ def _token_logprobs_autograd():
 
     class TokenLogprobs(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, logits, tokens, temperature, bitmask, entropy, top_n, workspace):
-            out = _token_logprobs(load(), logits, tokens, temperature, bitmask, entropy, top_n,
+        def forward(ctx, logits, tokens, temperature, bitmask, G, entropy, top_n, workspace):
+            out = _token_logprobs(logits, tokens, temperature, bitmask, G, entropy, top_n,
                                   workspace)
             ctx.keys = tuple(out)
             ctx.save_for_backward(logits, tokens, temperature, bitmask, out["row_max"],
@@ -719,7 +734,7 @@ def _token_logprobs_autograd():
             g = dict(zip(ctx.keys, grads))
             g_lp, g_ent = g["logprobs"], g.get("entropy")
             if g_lp is None and g_ent is None:
-                return (None,) * 7
+                return (None,) * 8
             if g_lp is None:
                 g_lp = torch.zeros(tokens.shape, dtype=torch.float32, device=tokens.device)
             grad = token_logprobs_backward(
@@ -727,7 +742,7 @@ def _token_logprobs_autograd():
                 temperature=temperature, bitmask=bitmask,
                 entropy=None if g_ent is None else ent,
                 grad_entropy=None if g_ent is None else g_ent.contiguous())
-            return (grad,) + (None,) * 6
+            return (grad,) + (None,) * 7
 
     _autograd = TokenLogprobs
     return _autograd
@@ -750,7 +765,7 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
             or hidden.stride(1) != 1:
         raise ValueError("hidden must be a bfloat16 CUDA tensor [B, K] with unit column stride")
     dev = hidden.device
-    _check_same_device(dev, codes=codes, scales=scales, zeros=zeros, out=out)
+    _check_same_device(dev, (("codes", codes), ("scales", scales), ("zeros", zeros), ("out", out)))
     B, K = hidden.shape
     if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.shape[1] * 2 != K \
             or codes.stride(1) != 1:
@@ -773,11 +788,12 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
         raise ValueError("out must be [B, V] in the asked dtype with unit column stride")
     with _on(dev):
         rc = lib.qs_head_logits(
-            _ptr(hidden), B, K, hidden.stride(0), _ptr(codes), V, codes.stride(0), _ptr(scales),
-            _dtype_code(scales), scales.stride(0), _ptr(zeros),
-            0 if zeros is None else zeros.stride(0), K // groups, _ptr(out), _dtype_code(out),
-            out.stride(0), _stream(dev))
-    _status(rc, "qs_head_logits")
+            hidden.data_ptr(), B, K, hidden.stride(0), codes.data_ptr(), V, codes.stride(0),
+            scales.data_ptr(), _dtype_code(scales), scales.stride(0), _addr(zeros),
+            0 if zeros is None else zeros.stride(0), K // groups, out.data_ptr(), _dtype_code(out),
+            out.stride(0), _raw_stream(dev))
+    if rc:
+        _status(rc, "qs_head_logits")
     return out
 
 
