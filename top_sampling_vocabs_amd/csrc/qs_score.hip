@@ -223,24 +223,25 @@ struct Shared {
   uint16_t lanes[kRowBlock];  // threads whose maximum reaches t
   int n_lanes;
   int count;
+  uint32_t t;
 };
 
-// The given token of slot `tid` and its logit, requested before the row is.
+// The given token of a slot, and its logit once the token is here.
 struct Given {
   int token;
   float z;
   bool legal;
 };
+__device__ __forceinline__ int given_token(const Args& a, int r, int g) {
+  return g < a.G ? a.tokens[(size_t)r * a.G + g] : -1;
+}
 template <int DT>
-__device__ __forceinline__ Given load_given(const Args& a, int r, int g) {
-  Given v{-1, 0.0f, false};
-  if (g < a.G) {
-    v.token = a.tokens[(size_t)r * a.G + g];
-    if (v.token >= 0 && v.token < a.V) {
-      v.z = logit_at<DT>(a.logits + (size_t)r * a.row_bytes, v.token);
-      v.legal = a.bitmask == nullptr ||
-                ((a.bitmask[(size_t)r * a.bm_stride + (v.token >> 5)] >> (v.token & 31)) & 1u);
-    }
+__device__ __forceinline__ Given load_given(const Args& a, int r, int token) {
+  Given v{token, 0.0f, false};
+  if (token >= 0 && token < a.V) {
+    v.z = logit_at<DT>(a.logits + (size_t)r * a.row_bytes, token);
+    v.legal = a.bitmask == nullptr ||
+              ((a.bitmask[(size_t)r * a.bm_stride + (token >> 5)] >> (token & 31)) & 1u);
   }
   return v;
 }
@@ -274,7 +275,7 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int th
     if (a.entropy) a.entropy[r] = ok ? log_sum - kLn2 * (E / S) : NAN;
   }
   for (int g = tid; g < a.G; g += threads) {
-    if (g != tid) given = load_given<DT>(a, r, g);
+    if (g != tid) given = load_given<DT>(a, r, given_token(a, r, g));
     float lp = ok ? -INFINITY : NAN;
     if (given.token == -1) lp = 0.0f;
     else if (ok && given.legal) lp = (given.z - m) / T - log_sum;
@@ -287,7 +288,12 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int th
   for (int i = tid; i < n_list; i += threads) {
     const uint64_t key = list[i];
     int rank = 0;
-    for (int j = 0; j < n_list; ++j) rank += list[j] > key;
+    int j = 0;
+    for (; j + 8 <= n_list; j += 8) {  // eight LDS reads under way at a time
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rank += list[j + e] > key;
+    }
+    for (; j < n_list; ++j) rank += list[j] > key;
     if (rank < a.top_n) {
       ids[rank] = (int32_t)~(uint32_t)key;
       tlp[rank] = (Keys<QS_F32>::value((uint32_t)(key >> 32)) - m) / T - log_sum;
@@ -316,8 +322,8 @@ __global__ void __launch_bounds__(THREADS)
   const int begin = part * part_loads * THREADS * P;  // first token of this workgroup
   const uint8_t* row = a.logits + (size_t)r * a.row_bytes;
   const uint8_t* mask_row = reinterpret_cast<const uint8_t*>(a.bitmask + (size_t)r * a.bm_stride);
-  Given given{-1, 0.0f, false};
-  if constexpr (ROW) given = load_given<DT>(a, r, tid);
+  int given_id = -1;
+  if constexpr (ROW) given_id = given_token(a, r, tid);
   const float T = a.T ? a.T[r] : 1.0f;
   const float c = scale_of(T);
 
@@ -337,6 +343,8 @@ __global__ void __launch_bounds__(THREADS)
       if constexpr (MASK) legal[u] = mask_row[i >> 3];
     }
   }
+  Given given{-1, 0.0f, false};
+  if constexpr (ROW) given = load_given<DT>(a, r, given_id);
   // a load's legal bits: the bitmask's, none past the row's end
   auto bits_at = [&](int i, uint32_t bits) {
     if constexpr (P == 4) bits = MASK ? bits >> (i & 4) : bits;
@@ -438,8 +446,14 @@ __global__ void __launch_bounds__(THREADS)
   uint32_t t = 0u;
   if constexpr (TOP) {
     // finite tokens only: keys above -inf's (groups without one hold the key of
-    // -FLT_MAX, the lowest of those)
-    t = max(wave_nth_high16(s.group[lane], a.top_n), Keys<QS_F32>::kNegInf + 1u);
+    // -FLT_MAX, the lowest of those). One wave searches: in every wave the search
+    // would cost as much as half a lane's exponentials.
+    if (w == 0) {
+      t = max(wave_nth_high16(s.group[lane], a.top_n), Keys<QS_F32>::kNegInf + 1u);
+      if (lane == 0) s.t = t;
+    }
+    __syncthreads();
+    t = s.t;
     if (key_of(lane_max) >= t) s.lanes[atomicAdd(&s.n_lanes, 1)] = (uint16_t)tid;
     __syncthreads();
     const float tz = Keys<QS_F32>::value(t);
@@ -526,9 +540,11 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const Part* p = ws_parts + (size_t)r * parts;
-  // requests that need nothing else first: the thread's slot, and the first 64
-  // keys of 4 lists per wave whatever their counts
-  const Given given = load_given<DT>(a, r, tid);
+  // requests that need nothing else first: the thread's slot, a part per lane,
+  // and the first 64 keys of 4 lists per wave whatever their counts
+  const int given_id = given_token(a, r, tid);
+  Part mine{-3.402823466e38f, 0.0f, 0.0f, 0u, 0u, 0, {0u, 0u}};
+  if (lane < parts) mine = p[lane];
   const uint64_t* const list = ws_list + (size_t)r * parts * kListCap;
   constexpr int kAhead = 4;
   uint64_t ahead[kAhead];
@@ -541,10 +557,11 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
   }
   const float T = a.T ? a.T[r] : 1.0f;
   const float c = scale_of(T);
+  const Given given = load_given<DT>(a, r, given_id);
   // every wave joins all parts (the same values in every thread)
-  float m = -3.402823466e38f;
-  uint32_t t = 0u, any = 0u;
-  for (int k = lane; k < parts; k += 64) {
+  float m = mine.m;
+  uint32_t t = mine.t, any = mine.any;
+  for (int k = lane + 64; k < parts; k += 64) {
     m = fmaxf(m, p[k].m);
     t = max(t, p[k].t);
     any |= p[k].any;
@@ -552,8 +569,10 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
   m = wave_max_f32(m);
   t = wave_reduce<OpMax>(t);
   const bool any_all = ballot(any != 0u) != 0;
-  float S = 0.0f, E = 0.0f;
-  for (int k = lane; k < parts; k += 64) {
+  const float d0 = rel(mine.m, m, c), f0 = exp2_hw(d0);
+  float S = f0 * mine.S;
+  float E = f0 * (mine.E + d0 * mine.S);
+  for (int k = lane + 64; k < parts; k += 64) {
     const float d = rel(p[k].m, m, c);
     const float f = exp2_hw(d);
     S += f * p[k].S;
@@ -575,10 +594,10 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int k = (tid >> 6) + j * (kThreadsHere / 64);
-      if (k < parts && lane < p[k].count) add(ahead[j]);
+      if (k < parts && lane < __shfl(mine.count, k, 64)) add(ahead[j]);
     }
     for (int j = 0, k = tid >> 6; k < parts; ++j, k += kThreadsHere / 64) {
-      const int n = p[k].count;
+      const int n = k < 64 ? __shfl(mine.count, k, 64) : p[k].count;
       for (int i = lane + (j < kAhead ? 64 : 0); i < n; i += 64) add(list[(size_t)k * kListCap + i]);
     }
     __syncthreads();
