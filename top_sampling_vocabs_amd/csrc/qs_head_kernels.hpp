@@ -335,7 +335,7 @@ struct StreamLds {
   static constexpr int kScaleStride = GC + 4;      // floats per row
   uint4 x[2][8 * MT * 64];
   f32x4 sum[2][GC][MT * 4];
-  u32x4 code[8][2][kCodeStride];                   // 16 rows each
+  u32x4 code[8][kStreamTiles][kCodeStride];        // 16 rows each
   float scale[8][kStreamTiles][16 * kScaleStride];
   float off[ZEROS ? 8 : 1][ZEROS ? kStreamTiles : 1][ZEROS ? 16 * kScaleStride : 1];
 };
@@ -459,10 +459,9 @@ __device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZER
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int buf = chunk & 1;
     // this chunk's codes through LDS: from lanes along a row to the product's
-    uint32_t q[NT][8];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      uint8_t* const turn = reinterpret_cast<uint8_t*>(lds.code[w][i & 1]);
+      uint8_t* const turn = reinterpret_cast<uint8_t*>(lds.code[w][i]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<u32x4*>(turn + (h * 8 + c_row) * kCodeStride + c_part * 16) = code[i][h];
@@ -475,34 +474,35 @@ __device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZER
         if constexpr (ZEROS)
           lds.off[w][i][g_row * kScaleStride + g_part + e] = -16.0f - (float)zero[i][e];
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const uint8_t* const row = turn + n * kCodeStride + p * 64;
-        if constexpr (G == 128) {
-          *reinterpret_cast<u32x4*>(&q[i][p * 4]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
-        } else if constexpr (G == 64) {
-          *reinterpret_cast<uint2*>(&q[i][p * 4]) = *reinterpret_cast<const uint2*>(row + kg * 8);
-          *reinterpret_cast<uint2*>(&q[i][p * 4 + 2]) =
-              *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q[i][p * 4 + j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
-        }
-      }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (chunk + 1 < chunks) load_weights(chunk + 1);
     __syncthreads();  // x of this chunk is in place, the other buffer is free
     if (chunk + 1 < chunks) {
       store_x(buf ^ 1);
-      load_weights(chunk + 1);
       if (chunk + 2 < chunks) load_x(chunk + 2);
     }
     __builtin_amdgcn_sched_barrier(0);
 
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
+      uint32_t q[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint8_t* const row =
+            reinterpret_cast<const uint8_t*>(lds.code[w][i]) + n * kCodeStride + p * 64;
+        if constexpr (G == 128) {
+          *reinterpret_cast<u32x4*>(q[i]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
+        } else if constexpr (G == 64) {
+          *reinterpret_cast<uint2*>(q[i]) = *reinterpret_cast<const uint2*>(row + kg * 8);
+          *reinterpret_cast<uint2*>(q[i] + 2) = *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[i][j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
+        }
+      }
 #pragma unroll
       for (int g = 0; g < GC / 2; ++g) {
         constexpr int J = G / 32;
@@ -527,7 +527,7 @@ __device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZER
           }
 #pragma unroll
           for (int jj = 0; jj < J; ++jj) {
-            const bf16x8 f = factors(q[i][p * 4 + g * J + jj], pattern);
+            const bf16x8 f = factors(q[i][g * J + jj], pattern);
 #pragma unroll
             for (int t = 0; t < MT; ++t)
               acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[jj][t], f, acc[t], 0, 0, 0);
