@@ -6,7 +6,6 @@ sampling runs in the HIP kernels; there is no CPU or torch fallback. If the
 library is missing the first call raises.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -537,272 +536,3 @@ def top_logprobs(cand_ids, cand_probs, cand_count, n):
     _status(rc, "qs_top_logprobs")
     return ids, lp, status
 
-
-def _addr(t):
-    """A tensor's address as a C argument (an int; None is NULL)."""
-    return None if t is None else t.data_ptr()
-
-
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on(device):
-    """Context in which `device` is the current one (kernels launch there)."""
-    import torch
-    return _SAME_DEVICE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
-
-
-def _raw_stream(device):
-    """The handle of the device's current torch stream, without a Stream object."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _check_same_device(device, tensors):
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-
-def _check_tokens(tokens, B, device):
-    """The number of slots per row of tokens [B] or [B, G]."""
-    import torch
-    if tokens.dtype != torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != B \
-            or tokens.device != device or not tokens.is_contiguous():
-        raise ValueError(f"tokens must be a contiguous int32 tensor [B] or [B, G] on {device}")
-    return tokens.shape[1] if tokens.dim() == 2 else 1
-
-
-def _padded_rows(B, V, dtype, device):
-    """[B, V] uninitialised, rows starting 16 bytes aligned."""
-    import torch
-    over = -V % (4 if dtype == torch.float32 else 8)
-    t = torch.empty((B, V + over), dtype=dtype, device=device)
-    return t[:, :V] if over else t
-
-
-def token_logprobs_workspace_for(logits, top_n=0):
-    """A workspace tensor for token_logprobs on these logits, or None when the
-    call needs none. Reuse it across calls on one stream."""
-    import torch
-    n = load().qs_token_logprobs_workspace_bytes(int(logits.shape[0]), int(logits.shape[1]),
-                                                 _dtype_code(logits), int(top_n))
-    return torch.empty(n, dtype=torch.uint8, device=logits.device) if n else None
-
-
-def token_logprobs(logits, tokens, *, temperature=None, bitmask=None, entropy=False, top_n=0,
-                   workspace=None):
-    """Log-probabilities of given tokens under the full tempered, masked softmax.
-
-    logits [B, V] float32 / bfloat16 (CUDA); tokens int32 [B] or [B, G], -1 an
-    empty slot (log-probability 0); temperature float32 [B] (> 0) or None (1);
-    bitmask int32 [B, >= ceil(V/32)] holding uint32 words, or None. Returns a
-    dict of device tensors: logprobs (the shape of tokens), row_max [B],
-    log_sum [B], status [B], and if requested entropy [B] (nats), top_ids and
-    top_logprobs [B, top_n] (top_n <= 64). Enqueued on the current stream.
-
-    If logits require a gradient, logprobs and entropy carry it (to the logits
-    only; a second derivative is not available).
-    """
-    import torch
-    B, V = _check_logits(logits, bitmask)
-    dev = logits.device
-    _check_same_device(dev, (("temperature", temperature), ("bitmask", bitmask),
-                             ("workspace", workspace)))
-    G = _check_tokens(tokens, B, dev)
-    if temperature is not None:
-        _check_rowvec(temperature, B, torch.float32, "temperature")
-    if logits.requires_grad and torch.is_grad_enabled():
-        keys, *out = _token_logprobs_autograd().apply(logits, tokens, temperature, bitmask, G,
-                                                      bool(entropy), int(top_n), workspace)
-        return dict(zip(keys, out))
-    return _token_logprobs(logits, tokens, temperature, bitmask, G, entropy, top_n, workspace)
-
-
-def _token_logprobs(logits, tokens, temperature, bitmask, G, entropy, top_n, workspace):
-    import torch
-    lib = load()
-    B, V = logits.shape
-    dev = logits.device
-    code = _dtype_code(logits)
-    lps = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    # the values per row in one allocation
-    row_max, log_sum, status, *ent = torch.empty((4 if entropy else 3, B), dtype=torch.float32,
-                                                 device=dev).unbind(0)
-    status = status.view(torch.int32)
-    out = {"logprobs": lps, "row_max": row_max, "log_sum": log_sum, "status": status}
-    if entropy:
-        out["entropy"] = ent[0]
-    ids = tops = None
-    if top_n:
-        out["top_ids"] = ids = torch.empty((B, top_n), dtype=torch.int32, device=dev)
-        out["top_logprobs"] = tops = torch.empty((B, top_n), dtype=torch.float32, device=dev)
-    if workspace is None:
-        n = lib.qs_token_logprobs_workspace_bytes(B, V, code, top_n)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = lib.qs_token_logprobs(
-            logits.data_ptr(), code, B, V, logits.stride(0), _addr(temperature), _addr(bitmask),
-            0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G, lps.data_ptr(),
-            row_max.data_ptr(), log_sum.data_ptr(), ent[0].data_ptr() if entropy else None,
-            top_n, _addr(ids), _addr(tops), status.data_ptr(), _addr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _raw_stream(dev))
-    if rc:
-        _status(rc, "qs_token_logprobs")
-    return out
-
-
-def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logprobs, *,
-                            temperature=None, bitmask=None, entropy=None, grad_entropy=None,
-                            out=None):
-    """Gradient of token_logprobs with respect to the logits.
-
-    logits, tokens, temperature, bitmask: the forward call's inputs; row_max,
-    log_sum, status (and entropy): its outputs; grad_logprobs float32 in the
-    shape of tokens; grad_entropy float32 [B], together with entropy, or None.
-    Returns grad_logits [B, V] in the logits' dtype (0 on rows whose status is
-    not ROW_OK); out: where to write it (it may be logits itself).
-    """
-    import torch
-    lib = load()
-    B, V = _check_logits(logits, bitmask)
-    dev = logits.device
-    _check_same_device(dev, (("temperature", temperature), ("bitmask", bitmask),
-                             ("row_max", row_max), ("log_sum", log_sum), ("status", status),
-                             ("grad_logprobs", grad_logprobs), ("entropy", entropy),
-                             ("grad_entropy", grad_entropy), ("out", out)))
-    G = _check_tokens(tokens, B, dev)
-    if temperature is not None:
-        _check_rowvec(temperature, B, torch.float32, "temperature")
-    _check_rowvec(row_max, B, torch.float32, "row_max")
-    _check_rowvec(log_sum, B, torch.float32, "log_sum")
-    _check_rowvec(status, B, torch.int32, "status")
-    if grad_logprobs.shape != tokens.shape or grad_logprobs.dtype != torch.float32 \
-            or not grad_logprobs.is_contiguous():
-        raise ValueError("grad_logprobs must be a contiguous float32 tensor in the shape of tokens")
-    if (entropy is None) != (grad_entropy is None):
-        raise ValueError("entropy and grad_entropy go together")
-    if entropy is not None:
-        _check_rowvec(entropy, B, torch.float32, "entropy")
-        _check_rowvec(grad_entropy, B, torch.float32, "grad_entropy")
-    if out is None:
-        out = _padded_rows(B, V, logits.dtype, dev)
-    elif out.shape != logits.shape or out.dtype != logits.dtype or out.stride(1) != 1:
-        raise ValueError("out must have the logits' shape and dtype and unit column stride")
-    with _on(dev):
-        rc = lib.qs_token_logprobs_backward(
-            logits.data_ptr(), _dtype_code(logits), B, V, logits.stride(0), _addr(temperature),
-            _addr(bitmask), 0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G,
-            row_max.data_ptr(), log_sum.data_ptr(), status.data_ptr(), grad_logprobs.data_ptr(),
-            _addr(entropy), _addr(grad_entropy), out.data_ptr(), out.stride(0), _raw_stream(dev))
-    if rc:
-        _status(rc, "qs_token_logprobs_backward")
-    return out
-
-
-_autograd = None
-
-
-def _token_logprobs_autograd():
-    """The torch.autograd.Function around token_logprobs (made on first use:
-    importing this module does not import torch)."""
-    global _autograd
-    if _autograd is not None:
-        return _autograd
-    import torch
-
-    class TokenLogprobs(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, logits, tokens, temperature, bitmask, G, entropy, top_n, workspace):
-            out = _token_logprobs(logits, tokens, temperature, bitmask, G, entropy, top_n,
-                                  workspace)
-            ctx.keys = tuple(out)
-            ctx.save_for_backward(logits, tokens, temperature, bitmask, out["row_max"],
-                                  out["log_sum"], out["status"], out.get("entropy"))
-            ctx.mark_non_differentiable(*(v for k, v in out.items()
-                                          if k not in ("logprobs", "entropy")))
-            ctx.set_materialize_grads(False)
-            return (ctx.keys, *out.values())
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, _keys, *grads):
-            logits, tokens, temperature, bitmask, row_max, log_sum, status, ent = \
-                ctx.saved_tensors
-            g = dict(zip(ctx.keys, grads))
-            g_lp, g_ent = g["logprobs"], g.get("entropy")
-            if g_lp is None and g_ent is None:
-                return (None,) * 8
-            if g_lp is None:
-                g_lp = torch.zeros(tokens.shape, dtype=torch.float32, device=tokens.device)
-            grad = token_logprobs_backward(
-                logits, tokens, row_max, log_sum, status, g_lp.contiguous(),
-                temperature=temperature, bitmask=bitmask,
-                entropy=None if g_ent is None else ent,
-                grad_entropy=None if g_ent is None else g_ent.contiguous())
-            return (grad,) + (None,) * 7
-
-    _autograd = TokenLogprobs
-    return _autograd
-
-
-def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
-    """Logits of hidden states under an output projection held in 4 bits.
-
-    hidden bfloat16 [B, K]; codes uint8 [V, K/2], two codes a byte, the even
-    column in the low half; scales float32 / bfloat16 [V, K/group], group 32, 64
-    or 128; zeros uint8 [V, K/group] or None (8). Weight [v, k] is
-    (code - zero) * scale. Returns logits [B, V] in `dtype` (bfloat16 unless
-    given) with rows laid out as the selection reads them; out: where to write
-    them. Enqueued on the current stream. Inference only: tensors that require
-    a gradient are refused.
-    """
-    import torch
-    lib = load()
-    if hidden.dim() != 2 or not hidden.is_cuda or hidden.dtype != torch.bfloat16 \
-            or hidden.stride(1) != 1:
-        raise ValueError("hidden must be a bfloat16 CUDA tensor [B, K] with unit column stride")
-    dev = hidden.device
-    _check_same_device(dev, (("codes", codes), ("scales", scales), ("zeros", zeros), ("out", out)))
-    B, K = hidden.shape
-    if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.shape[1] * 2 != K \
-            or codes.stride(1) != 1:
-        raise ValueError("codes must be a uint8 tensor [V, K/2] with unit column stride")
-    V = codes.shape[0]
-    groups = scales.shape[1] if scales.dim() == 2 else 0
-    if groups < 1 or scales.shape[0] != V or K % groups or K // groups not in (32, 64, 128) \
-            or scales.stride(1) != 1:
-        raise ValueError("scales must be [V, K/group] with group 32, 64 or 128 "
-                         "and unit column stride")
-    if zeros is not None and (zeros.shape != scales.shape or zeros.dtype != torch.uint8
-                              or zeros.stride(1) != 1):
-        raise ValueError("zeros must be a uint8 tensor in the shape of scales")
-    if torch.is_grad_enabled() and (hidden.requires_grad or scales.requires_grad):
-        raise ValueError("head_logits has no gradient: call it under torch.no_grad() "
-                         "or on detached tensors")
-    if out is None:
-        out = _padded_rows(B, V, dtype or torch.bfloat16, dev)
-    elif out.shape != (B, V) or out.stride(1) != 1 or (dtype is not None and out.dtype != dtype):
-        raise ValueError("out must be [B, V] in the asked dtype with unit column stride")
-    with _on(dev):
-        rc = lib.qs_head_logits(
-            hidden.data_ptr(), B, K, hidden.stride(0), codes.data_ptr(), V, codes.stride(0),
-            scales.data_ptr(), _dtype_code(scales), scales.stride(0), _addr(zeros),
-            0 if zeros is None else zeros.stride(0), K // groups, out.data_ptr(), _dtype_code(out),
-            out.stride(0), _raw_stream(dev))
-    if rc:
-        _status(rc, "qs_head_logits")
-    return out
-
-
-def sample_hidden(hidden, codes, scales, zeros, temperature, top_k, top_p, bitmask=None, *,
-                  dtype=None, logits=None, **options):
-    """sample() from hidden states: head_logits into `logits` (a buffer [B, V];
-    made per call when omitted), then the selection, on the current stream.
-    options: sample()'s keyword arguments. The result holds the logits too."""
-    z = head_logits(hidden, codes, scales, zeros, dtype=dtype, out=logits)
-    out = sample(z, temperature, top_k, top_p, bitmask, **options)
-    out["logits"] = z
-    return out
