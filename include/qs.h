@@ -468,7 +468,9 @@ QS_API int qs_top_logprobs(int64_t B, const int32_t* cand_ids, const float* cand
  *              for qs_filter_mask: its contents on entry do not matter, calls
  *              that may overlap in time need different ones.
  * Sums are held in float32 per lane and joined in a fixed order: the same call
- * gives the same bits. Logits are read once. */
+ * gives the same bits. Logits are read once, and the few pieces of 16 bytes that
+ * hold top tokens again. One kernel launch on `stream` for rows of at most 32768
+ * float32 or 65536 bfloat16 tokens, two for longer ones; nothing is allocated. */
 QS_API size_t qs_token_logprobs_workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n);
 QS_API int qs_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V,
                       int64_t row_stride, const float* temperature, const uint32_t* bitmask,
@@ -509,11 +511,12 @@ QS_API int qs_token_logprobs_backward(const void* logits, int dtype, int64_t B, 
  *   y[b][v] = sum over groups g of scale[v][g] *
  *             sum over k in g of hidden[b][k] * (code[v][k] - zero[v][g])
  *
- * hidden       [B][hidden_stride] bfloat16, 16-byte aligned, hidden_stride a
- *              multiple of 8 and >= K
+ * hidden       [B][hidden_stride] bfloat16, B at most 2^20, 16-byte aligned,
+ *              hidden_stride a multiple of 8 and >= K
  * codes        [V][codes_stride] bytes, 16-byte aligned, codes_stride a
  *              multiple of 16 and >= K / 2: two codes 0..15 a byte, the even
- *              column in the low half
+ *              column in the low half; codes_stride, scale_stride and
+ *              zero_stride at most 2^26
  * scales       [V][scale_stride] float32 or bfloat16 (scale_dtype), one per
  *              group of `group` columns; scale_stride >= K / group
  * zeros        [V][zero_stride] uint8, optional (NULL: 8 everywhere)
@@ -521,10 +524,14 @@ QS_API int qs_token_logprobs_backward(const void* logits, int dtype, int64_t B, 
  * logits       [B][row_stride] float32 or bfloat16 out (logits_dtype), 16-byte
  *              aligned, row_stride * element size a multiple of 16, columns
  *              from V on left as they are
- * V at most 2^24. Products are exact (a bf16 factor and a code), sums are held
- * in float32 and each logit is rounded once. A row of `hidden` that holds an
- * infinity or a NaN gives no finite logit (NaN, or an infinity). Made for
- * the 1 to 64 rows of a decode step; more rows read the weights once per 64.
+ * V at most 2^24. A group's sum is that of hidden * (16 + code) less (16 +
+ * zero) times that of hidden: products are exact, sums are held in float32 (so
+ * their rounding is relative to these two sums, and both have to stay below
+ * float32's largest value), the scale meets the group's sum and each logit is
+ * rounded once. A row of `hidden` that holds an infinity or a NaN gives no
+ * finite logit (NaN, or an infinity). Made for the 1 to 64 rows of a decode
+ * step; more rows read the weights once per 64. The same call gives the same
+ * bits; a row's bits may depend on B, which chooses the order of the sums.
  * One kernel launch on `stream`; nothing is allocated. */
 QS_API int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidden_stride,
                       const uint8_t* codes, int64_t V, int64_t codes_stride, const void* scales,

@@ -370,6 +370,8 @@ def test_token_logprobs_backward_rejects_bad_arguments(lib, kw):
     dict(V=0), dict(V=(1 << 24) + 1), dict(cs=112), dict(cs=136), dict(s=None), dict(s=ODD),
     dict(sd=2), dict(ss=3), dict(zeros=A16, zs=3), dict(group=16), dict(group=96),
     dict(group=256), dict(logits=None), dict(logits=ODD), dict(ld=2), dict(ls=60), dict(ls=66),
+    dict(B=(1 << 20) + 1), dict(cs=(1 << 26) + 16), dict(ss=(1 << 26) + 1),
+    dict(zeros=A16, zs=(1 << 26) + 1),
 ])
 def test_head_logits_rejects_bad_arguments(lib, kw):
     a = dict(x=A16, B=2, K=256, xs=256, codes=A16, V=64, cs=128, s=A16, sd=0, ss=4, zeros=None,

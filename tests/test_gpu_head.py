@@ -84,6 +84,13 @@ CASES = [
     (20, 40, 32800, 32, False, "bf16", "f32"),
     (4, 70001, 256, 64, True, "bf16", "f32"),
     (1, 40000, 1024, 32, True, "bf16", "bf16"),
+    # 17 to 32 rows in registers (one, two and four steps a slice) and through LDS
+    (32, 300, 96, 32, True, "bf16", "f32"),
+    (31, 33000, 2176, 64, False, "bf16", "f32"),
+    (18, 9001, 1280, 128, True, "f32", "bf16"),
+    (29, 4003, 3968, 128, False, "bf16", "f32"),
+    (24, 20001, 1024, 64, True, "bf16", "f32"),
+    (16, 2100, 8192, 32, True, "bf16", "f32"),
 ]
 
 
@@ -124,6 +131,22 @@ def test_strides_and_padding(qs, B):
     plain = qs.head_logits(x.cuda(), codes.cuda(), s.cuda(), z.cuda(), dtype=torch.float32)
     torch.cuda.synchronize()
     assert torch.equal(plain, out)
+
+
+@pytest.mark.parametrize("B", [2, 20, 40])
+def test_offsets_past_32_bits(qs, B):
+    """Rows of codes and logits that lie 2^32 bytes and more into their buffers,
+    in every kernel, at strides that a row of 4-bit weights can have."""
+    import torch
+    print(f"head offsets B={B}", flush=True)
+    V, K, group, stride = 70003, 128, 64, 65536
+    x, codes, s, z = make(B, B, V, K, group, True, "f32")
+    cs = torch.empty((V, stride), dtype=torch.uint8, device="cuda")[:, :K // 2]
+    cs.copy_(codes)
+    rows = torch.empty((B, 1 << 29), dtype=torch.float32, device="cuda")[:, :V]
+    got = qs.head_logits(x.cuda(), cs, s.cuda(), z.cuda(), out=rows)
+    torch.cuda.synchronize()
+    check(x, codes, s, z, group, got, "f32")
 
 
 @pytest.mark.parametrize("B", [1, 16, 64])

@@ -15,6 +15,8 @@ Tolerances, with u = 2^-24 (half a float32 step) and a_i = (z_i - m) / T:
   rounding of half a step of the output type.
 """
 
+import math
+
 import numpy as np
 import pytest
 
@@ -462,3 +464,63 @@ def test_refusals(qs):
                                        stats["status"], a.pop("grad_logprobs"), **a)
     out = qs.token_logprobs(lg[:0], tok[:0], entropy=True, top_n=2)
     assert out["logprobs"].shape == (0,) and out["top_ids"].shape == (0, 2)
+
+
+def test_offsets_past_32_bits(qs):
+    """Rows 4 GiB apart, forward and in-place backward: the compact rows' bits."""
+    import torch
+    print("offsets past 32 bits", flush=True)
+    rng = np.random.default_rng(12)
+    for V in (5001, 40003):
+        z = torch.from_numpy(rng.normal(0, 3, (3, V)).astype(np.float32)).cuda()
+        flat = torch.empty((3, -(-V // 8) * 8), device="cuda")[:, :V]
+        flat.copy_(z)
+        far = torch.empty((3, 1 << 30), device="cuda")[:, :V]
+        far.copy_(z)
+        tok = torch.from_numpy(rng.integers(0, V, (3, 2)).astype(np.int32)).cuda()
+        a = qs.token_logprobs(flat, tok, entropy=True, top_n=5)
+        b = qs.token_logprobs(far, tok, entropy=True, top_n=5)
+        torch.cuda.synchronize()
+        for k in a:
+            assert torch.equal(a[k], b[k]), k
+        g = torch.ones(3, 2, device="cuda")
+        want = qs.token_logprobs_backward(flat, tok, a["row_max"], a["log_sum"], a["status"], g)
+        got = qs.token_logprobs_backward(far, tok, b["row_max"], b["log_sum"], b["status"], g,
+                                         out=far)
+        torch.cuda.synchronize()
+        assert torch.equal(want, got)
+        del far, got, b
+
+
+def test_longest_row(qs):
+    """2^30 tokens, the most a row may have. All logits are 0 but three, so that
+    S = V - 3 + e^1 + e^2 + e^3 before the maximum is taken out. Its terms pass at
+    most 64 additions in a lane, 6 + 4 in a workgroup, 2^15 / 64 and 6 in the join:
+    log S is off by at most 600 * 2^-24 = 3.6e-5, its own rounding to float32
+    (2^-24 * 18) within that."""
+    import torch
+    print("longest row", flush=True)
+    V = 1 << 30
+    z = torch.zeros((1, V), dtype=torch.bfloat16, device="cuda")
+    at = [V - 1, 12345678, (1 << 29) + 7]
+    for k, i in enumerate(at):
+        z[0, i] = float(3 - k)
+    tok = torch.tensor([[V - 1, 0, at[2], -1]], dtype=torch.int32, device="cuda")
+    out = qs.token_logprobs(z, tok, top_n=3)
+    torch.cuda.synchronize()
+    S = V - 3 + sum(math.exp(k) for k in (1, 2, 3))
+    assert out["status"].item() == 0 and out["row_max"].item() == 3.0
+    assert abs(out["log_sum"].item() - (math.log(S) - 3)) <= 3.6e-5
+    assert out["top_ids"].tolist() == [[V - 1, at[1], at[2]]]
+    lp = out["logprobs"][0].tolist()
+    for got, zv in zip(lp, (3.0, 0.0, 1.0)):
+        assert abs(got - (zv - math.log(S))) <= 3.6e-5 + 2 ** -20
+    assert lp[3] == 0.0
+    g = torch.ones_like(tok, dtype=torch.float32)
+    grad = qs.token_logprobs_backward(z, tok, out["row_max"], out["log_sum"], out["status"], g,
+                                      out=z)
+    torch.cuda.synchronize()
+    # three slots: 1 - 3 p at a given token, -3 p elsewhere, p below 2e-8
+    assert grad[0, V - 1].item() == 1.0 and grad[0, at[2]].item() == 1.0
+    p = 3 * math.exp(2) / S
+    assert abs(grad[0, at[1]].item() + p) <= p * 2 ** -7

@@ -84,7 +84,9 @@ def token_logprobs(logits, tokens, *, temperature=None, bitmask=None, entropy=Fa
     top_logprobs [B, top_n] (top_n <= 64). Enqueued on the current stream.
 
     If logits require a gradient, logprobs and entropy carry it (to the logits
-    only; a second derivative is not available).
+    only; a second derivative is not available). To capture a training step in a
+    graph, drop every eager autograd graph of the same leaves first, as torch
+    asks for all backward passes, or capture token_logprobs_backward itself.
     """
     B, V, G = _check_row_inputs(logits, tokens, temperature, bitmask)
     if workspace is not None:
@@ -243,7 +245,7 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
                          f"on {dev}")
     with _on(dev):
         rc = load().qs_head_logits(
-            hidden.data_ptr(), B, K, hidden.stride(0), codes.data_ptr(), V, codes.stride(0),
+            hidden.data_ptr(), B, K, hidden.stride(0) if B > 1 else K, codes.data_ptr(), V, codes.stride(0),
             scales.data_ptr(), _code(scales, "scales"), scales.stride(0), _addr(zeros),
             0 if zeros is None else zeros.stride(0), K // groups, out.data_ptr(),
             _code(out, "out"), out.stride(0), _stream(dev))

@@ -575,7 +575,7 @@ int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidden_stri
                    int scale_dtype, int64_t scale_stride, const uint8_t* zeros,
                    int64_t zero_stride, int64_t group, void* logits, int logits_dtype,
                    int64_t row_stride, void* stream) {
-  if (B < 0 || B > kMaxB || V < 1 || V > qs::head::kMaxV || K < 1 || K > qs::head::kMaxK)
+  if (B < 0 || B > qs::head::kMaxB || V < 1 || V > qs::head::kMaxV || K < 1 || K > qs::head::kMaxK)
     return QS_ERR_INVALID_ARG;
   if ((group != 32 && group != 64 && group != 128) || K % group != 0) return QS_ERR_INVALID_ARG;
   if ((scale_dtype != QS_F32 && scale_dtype != QS_BF16) ||
@@ -585,11 +585,13 @@ int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidden_stri
   const int64_t groups = K / group;
   if (!hidden || !aligned(hidden, 16) || hidden_stride < K || hidden_stride % 8 != 0)
     return QS_ERR_INVALID_ARG;
-  if (!codes || !aligned(codes, 16) || codes_stride < K / 2 || codes_stride % 16 != 0)
+  if (!codes || !aligned(codes, 16) || codes_stride < K / 2 || codes_stride % 16 != 0 ||
+      codes_stride > qs::head::kMaxWeightStride)
     return QS_ERR_INVALID_ARG;
-  if (!scales || !aligned(scales, scale_dtype == QS_F32 ? 4 : 2) || scale_stride < groups)
+  if (!scales || !aligned(scales, scale_dtype == QS_F32 ? 4 : 2) || scale_stride < groups ||
+      scale_stride > qs::head::kMaxWeightStride)
     return QS_ERR_INVALID_ARG;
-  if (zeros && zero_stride < groups) return QS_ERR_INVALID_ARG;
+  if (zeros && (zero_stride < groups || zero_stride > qs::head::kMaxWeightStride)) return QS_ERR_INVALID_ARG;
   const int64_t es = logits_dtype == QS_F32 ? 4 : 2;
   if (!logits || !aligned(logits, 16) || row_stride < V || (row_stride * es) % 16 != 0)
     return QS_ERR_INVALID_ARG;

@@ -7,8 +7,12 @@
 namespace qs {
 namespace head {
 
+constexpr int64_t kMaxB = (int64_t)1 << 20;  // 64 rows a block of the grid's y
 constexpr int64_t kMaxV = (int64_t)1 << 24;
 constexpr int64_t kMaxK = 65536;
+// 15 rows of codes, scales (4 bytes) or zero points are reached with a lane's
+// unsigned 32-bit offset from the first of 16
+constexpr int64_t kMaxWeightStride = (int64_t)1 << 26;
 
 struct Args {
   const uint16_t* hidden;    // [B][hidden_stride] bf16

@@ -7,20 +7,23 @@
 // the exponent of 16 is the bf16 number 16 + q, so one shift and one and-or
 // make two factors, and
 //   sum x (q - z) = sum x (16 + q) - (16 + z) sum x
-// with exact products and float32 sums; sum x comes from the same fragments
-// against a fragment of ones. The scale is applied to the float32 group sum,
-// never to a factor, so no weight is rounded.
+// with exact products and float32 sums; sum x is added up once per launch or per
+// chunk and starts the group's sum. The scale is applied to the float32 group
+// sum, never to a factor, so no weight is rounded; the logit's own rounding to
+// bf16, where that is asked for, is the only one to fewer bits.
 //
 // A 16x16x32 product takes 16 hidden rows (A) and 16 vocabulary rows (B), 8
 // columns of k per lane on both sides. Which columns those are is free as long
-// as both sides agree and a product stays inside one group: a lane reads 16, 8
+// as both sides agree and a product stays inside one group: a lane takes 16, 8
 // or 4 bytes of codes in a row (groups of 128, 64, 32) per 128-column step. The
 // nibbles i and i + 4 of a dword share a register, so the hidden values are
 // laid out in the order 0 4 1 5 2 6 3 7 beforehand.
 //
-// Up to 16 hidden rows whose values fit LDS stay there for the whole launch
-// (head_resident_kernel): every wave then walks its own vocabulary tiles with
-// kDepth steps of codes in flight and no barrier.
+// Two kernels. Few rows: the codes' bytes bound the call, and the hidden values
+// stay in registers for the whole launch (head_split_kernel). More rows, or
+// rows too long for the registers: making factors and multiplying costs as much
+// as the bytes, and one set of factors meets up to 64 hidden rows, which pass
+// through LDS (head_stream_kernel).
 
 #pragma once
 
@@ -40,7 +43,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = 128;                // columns per step
-constexpr int kChunks = kStepK / 8;        // 8-column chunks per step
 constexpr uint32_t kOnes = 0x3F803F80u;    // two bf16 ones
 
 // Where an MFMA's 8 columns of lane group kg lie, in chunks of the step.
@@ -96,7 +98,14 @@ constexpr int occupancy(int P, int MT) { return P * MT <= 4 ? 4 : 2; }
 // are read with consecutive lanes on consecutive bytes (lanes in the product's
 // own order, 16 rows apart, cost four times the cache accesses), one tile ahead,
 // and change lanes through the wave's own LDS. The slices' float32 sums meet in
-// LDS (two buffers, one barrier a tile) and are added in slice order.
+// LDS (two buffers, one barrier a tile) and are added in slice order, so the
+// result does not depend on which wave is first.
+//
+// Measured: 1 row, 151936 x 4096 in groups of 128, 59 us (5.5 TB/s of codes and
+// scales, where a large copy reaches 4.8 and a large sum 4.0); 1 row, 32000 x
+// 2048, 11.3 us; 16 rows, 128256 x 4096 in groups of 64 with zero points and
+// float32 logits, 74 us (3.9 TB/s: the factors and the offsets, five vector
+// instructions for every product, take over from the bytes).
 template <int P, int MT, int G, int SD, bool ZEROS>
 __global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
     head_split_kernel(Args a, int steps, int tiles, int ks_log2) {
@@ -307,11 +316,18 @@ hipError_t pick_steps(const Args& a, hipStream_t st) {
   // the fewest slices that leave a wave at most 4 steps
   int ks_log2 = 0;
   while (ks_log2 < 3 && (steps + (1 << ks_log2) - 1) >> ks_log2 > 4) ++ks_log2;
+  // few tiles: more slices of each, so that more workgroups share them (2
+  // rows, 10000 x 2048: 8.7 us against 12.8 without; 32000 x 2048, the first size
+  // past the rule's reach: 12.5 us either way)
+  const int tiles = (a.V + 15) / 16;
+  while (ks_log2 < 3 && (steps >> ks_log2) > 1 && tiles < (512 << (3 - ks_log2))) ++ks_log2;
   const int per = (steps + (1 << ks_log2) - 1) >> ks_log2;
   if (per <= 1) return launch_split<1, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
   if (per == 2) return launch_split<2, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
-  if (per <= 4) return launch_split<4, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
-  return launch_split<8, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  if constexpr (MT == 1) {
+    if (per > 4) return launch_split<8, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  }
+  return launch_split<4, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -325,9 +341,16 @@ constexpr int kStreamTiles = 3;          // most tiles a wave holds at once
 // product's lane order, with the sums of its groups; every wave of the
 // workgroup multiplies the same chunk with up to NT tiles of its own, whose
 // sums stay in registers over all of k. A chunk's codes, scales and hidden
-// values are requested while the chunk before is multiplied. With one
-// workgroup per compute unit the rows of a wave's tiles follow one another, so
-// x is read from L2 once per 8 NT tiles.
+// values are requested while the chunk before is multiplied. x is read from L2
+// once per 8 NT tiles.
+//
+// Measured: 64 rows, 151936 x 8192 in groups of 128, 289 us (550 TFLOP/s); in
+// groups of 32 with float32 scales, 311 us. With the products alone on codes
+// already in LDS the second takes 205 to 250 us, with the loads alone 200 to 220:
+// both sides are near their own limits and overlap imperfectly, since 8 waves a
+// compute unit are all that the registers of 3 tiles by 64 rows allow. Fewer
+// waves with more columns, or the columns of a chunk split over the waves, were
+// slower (355 and 328 us).
 template <int MT, int G, bool ZEROS>
 struct StreamLds {
   static constexpr int GC = kChunkK / G;           // groups per chunk
@@ -394,7 +417,8 @@ __device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZER
       if constexpr (G >= 64) sum += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(sum)));
       if constexpr (G == 128) sum += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(sum)));
       lds.x[buf][place(xp, xj, i, xg, xm)] = ordered(xv[i]);
-      if ((xc & (G / 8 - 1)) == 0) reinterpret_cast<float*>(lds.sum[buf][xc / (G / 8)])[xm + 16 * i] =
+      if ((xc & (G / 8 - 1)) == 0)
+        reinterpret_cast<float*>(lds.sum[buf][xc / (G / 8)])[xm + 16 * i] =
             ZEROS ? sum : -24.0f * sum;
     }
   };
@@ -593,6 +617,12 @@ template <int G, int SD, bool ZEROS>
 hipError_t pick(const Args& a, hipStream_t st) {
   if (a.B <= 16 && a.K <= 8192) return pick_steps<1, G, SD, ZEROS>(a, st);
   if (a.B <= 16) return launch_stream<1, G, SD, ZEROS>(a, st);
+  // 17 to 32 rows: in registers up to 4096 columns (32 rows, 151936 x 4096: 85 to
+  // 90 us against 92 to 94; 5000 x 4096: 17 against 23). Short rows of a large
+  // vocabulary are a draw (24 rows, 151936 x 2048: 52 us either way) and stay with
+  // the kernel that keeps x in LDS.
+  if (a.B <= 32 && a.K <= 4096 && (a.K > 2048 || a.V < 16384))
+    return pick_steps<2, G, SD, ZEROS>(a, st);
   if (a.B <= 32) return launch_stream<2, G, SD, ZEROS>(a, st);
   return launch_stream<4, G, SD, ZEROS>(a, st);
 }

