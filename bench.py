@@ -67,6 +67,11 @@ def parse():
     ap.add_argument("--penalties", action="store_true",
                     help="instead of the headline line, time qs_apply_penalties (2048-token "
                          "histories) on the headline batch, alone and followed by qs_sample")
+    ap.add_argument("--hidden", type=int, default=0, metavar="B",
+                    help="instead of the headline line, time a decode step of B rows from "
+                         "hidden states (V=151936, K=4096, 4-bit output head): head, "
+                         "selection, log-probabilities of the drawn tokens with 20 "
+                         "alternatives, and the gradient a training step adds")
     ap.add_argument("--ablation", action="store_true",
                     help="instead of the headline line, print one line timing the path "
                          "switches (the Qrita page's ablation runs) on the headline "
@@ -536,6 +541,80 @@ def toplp_bench(args, lib, stream):
     print(json.dumps(line), flush=True)
 
 
+def hidden_bench(args):
+    """A decode step from hidden states, and the scores' gradient, as one graph of
+    K steps over rotating weights and as each call alone."""
+    import torch
+    import top_sampling_vocabs_amd as qs
+    B, V, K, group, top_n = args.hidden, 151936, 4096, 128, 20
+    gen = torch.Generator(device="cuda").manual_seed(workloads.BASE_SEED)
+    full = lambda v, d: torch.full((B,), v, dtype=d, device="cuda")  # noqa: E731
+
+    class Step:
+        def __init__(self):
+            rand = lambda *s: torch.rand(*s, device="cuda", generator=gen)  # noqa: E731
+            self.x = torch.randn(B, K, device="cuda", generator=gen).bfloat16()
+            self.codes = torch.randint(0, 256, (V, K // 2), dtype=torch.uint8, device="cuda",
+                                       generator=gen)
+            self.scales = ((0.5 + rand(V, K // group)) * (3 / (4.6 * K ** 0.5))).bfloat16()
+            self.T, self.p = full(1.0, torch.float32), full(0.9, torch.float32)
+            self.k = full(50, torch.int32)
+            self.seed = torch.arange(B, device="cuda")
+            self.offset = torch.zeros(B, dtype=torch.int64, device="cuda")
+            self.g = full(1.0 / B, torch.float32)
+            self.logits = torch.empty(B, V, dtype=torch.bfloat16, device="cuda")
+            self.part = "all"
+            self.call()
+
+        def call(self, stream=None, flags=None):
+            part = self.part
+            if part in ("head", "step", "all"):
+                qs.head_logits(self.x, self.codes, self.scales, out=self.logits)
+            if part in ("sample", "step", "all"):
+                self.tokens = qs.sample(self.logits, self.T, self.k, self.p, seed=self.seed,
+                                        offset=self.offset)["tokens"]
+            if part in ("score", "step", "all"):
+                self.out = qs.token_logprobs(self.logits, self.tokens, temperature=self.T,
+                                             top_n=top_n)
+            if part in ("gradient", "all"):
+                out = self.out
+                self.grad = qs.token_logprobs_backward(
+                    self.logits, self.tokens, out["row_max"], out["log_sum"], out["status"],
+                    self.g, temperature=self.T)
+
+    steps = [Step() for _ in range(args.sets)]
+    ms = {}
+    for part in ("head", "sample", "score", "gradient", "step", "all"):
+        for s in steps:
+            s.part = part
+        for i in range(args.warmup):
+            steps[i % len(steps)].call()
+        torch.cuda.synchronize()
+        t, graph, _ = time_graph(steps, args.steps)
+        ms[part] = t / args.steps
+        for s in steps:
+            assert bool((s.out["status"] == 0).all()) and bool((s.tokens >= 0).all())
+        del graph
+    weights = V * (K // 2 + 2 * (K // group))
+    nbytes = weights + 2 * B * K + 3 * 2 * B * V  # weights, x; logits written, read twice
+    per = ms["step"]
+    print(json.dumps({
+        "metric": f"decode steps from hidden states, rows/sec, B={B} V={V} K={K}",
+        "value": round(B / (per * 1e-3), 1), "unit": "rows/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(per, 5), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": f"4-bit head in groups of {group}, top-k 50 and top-p 0.9 draw, "
+                               f"log-probabilities with {top_n} alternatives",
+                   "head_ms": round(ms["head"], 5), "sample_ms": round(ms["sample"], 5),
+                   "score_ms": round(ms["score"], 5), "gradient_ms": round(ms["gradient"], 5),
+                   "step_and_gradient_ms": round(ms["all"], 5), "launch": "graph"},
+        "roofline": {"bound": "hbm", "achieved": round(nbytes / (per * 1e-3) / 1e9, 1),
+                     "peak": HBM_PEAK_GBS, "unit": "GB/s",
+                     "frac": round(nbytes / (per * 1e-3) / 1e9 / HBM_PEAK_GBS, 5),
+                     "traffic": None, "bytes_per_step": int(nbytes)},
+    }), flush=True)
+
+
 class PenaltyPrepared:
     """A 2048-token history per row (uniform ids, so about 2,030 distinct),
     repetition 1.2 and presence 0.3, and the ctypes tuple of qs_apply_penalties
@@ -845,6 +924,9 @@ def main():
         return
     if args.toplp:
         toplp_bench(args, lib, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        return
+    if args.hidden:
+        hidden_bench(args)
         return
     if args.spec:
         spec_bench(args, lib, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))

@@ -432,6 +432,33 @@ def test_autograd(qs):
                        grad)
 
 
+def test_autograd_outputs_in_place(qs):
+    """The log-probabilities may be changed in place (a masked sum does so). The
+    entropy, which the gradient reads, may not: torch reports it."""
+    import torch
+    z = torch.randn(4, 512, device="cuda")
+    tok = torch.tensor([1, 500, -1, 3], dtype=torch.int32, device="cuda")
+    keep = (tok >= 0).float()
+    grads = []
+    for in_place in (False, True):
+        lg = z.clone().requires_grad_()
+        out = qs.token_logprobs(lg, tok, entropy=True)
+        lp, ent = out["logprobs"], out["entropy"]
+        if in_place:
+            lp *= keep
+        else:
+            lp = lp * keep
+        ent = ent * keep
+        (lp.sum() + 0.5 * ent.sum()).backward()
+        torch.cuda.synchronize()
+        grads.append(lg.grad)
+    assert torch.equal(*grads) and bool(grads[0].any())
+    with pytest.raises(RuntimeError):
+        out = qs.token_logprobs(z.clone().requires_grad_(), tok, entropy=True)
+        out["entropy"].mul_(keep)
+        out["entropy"].sum().backward()
+
+
 def test_refusals(qs):
     import torch
     lg = torch.zeros(4, 64, device="cuda")

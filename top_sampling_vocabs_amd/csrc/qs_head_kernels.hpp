@@ -317,8 +317,8 @@ hipError_t pick_steps(const Args& a, hipStream_t st) {
   int ks_log2 = 0;
   while (ks_log2 < 3 && (steps + (1 << ks_log2) - 1) >> ks_log2 > 4) ++ks_log2;
   // few tiles: more slices of each, so that more workgroups share them (2
-  // rows, 10000 x 2048: 8.7 us against 12.8 without; 32000 x 2048, the first size
-  // past the rule's reach: 12.5 us either way)
+  // rows, 10000 x 2048: 8.7 us against 12.8 without; 1 row, 32000 x 2048, past
+  // the rule's reach: 12.5 us)
   const int tiles = (a.V + 15) / 16;
   while (ks_log2 < 3 && (steps >> ks_log2) > 1 && tiles < (512 << (3 - ks_log2))) ++ks_log2;
   const int per = (steps + (1 << ks_log2) - 1) >> ks_log2;
