@@ -334,47 +334,63 @@ hipError_t pick_steps(const Args& a, hipStream_t st) {
 
 constexpr int kChunkK = 2 * kStepK;      // columns per chunk: 128 bytes of codes a row
 constexpr int kMaxRows = 64;             // hidden rows per workgroup
-constexpr int kStreamTiles = 3;          // most tiles a wave holds at once
+constexpr int kMaxTiles = 5;             // tiles a wave holds at once
 
 // More hidden rows, or rows too long for the registers: x passes through LDS in
-// chunks of 256 columns (two buffers, one barrier a chunk), already in the
-// product's lane order, with the sums of its groups; every wave of the
-// workgroup multiplies the same chunk with up to NT tiles of its own, whose
-// sums stay in registers over all of k. A chunk's codes, scales and hidden
-// values are requested while the chunk before is multiplied. x is read from L2
-// once per 8 NT tiles.
+// steps of 128 columns (two steps a buffer where LDS has room; two buffers, one
+// barrier each), already in the product's lane order, with the sums of its
+// groups; every wave of the workgroup multiplies the same x with up to NT tiles
+// of its own, whose sums stay in registers over all of k. x is read from L2 once
+// per 8 NT tiles and from LDS once per NT, so NT is as large as the registers
+// allow.
 //
-// Measured: 64 rows, 151936 x 8192 in groups of 128, 289 us (550 TFLOP/s); in
-// groups of 32 with float32 scales, 311 us. With the products alone on codes
-// already in LDS the second takes 205 to 250 us, with the loads alone 200 to 220:
-// both sides are near their own limits and overlap imperfectly, since 8 waves a
-// compute unit are all that the registers of 3 tiles by 64 rows allow. Fewer
-// waves with more columns, or the columns of a chunk split over the waves, were
-// slower (355 and 328 us).
-template <int MT, int G, bool ZEROS>
+// What the weights' loads look like decides the rest. The workgroups of an XCD
+// hold 8 NT * 16 rows each at a time, more cache lines than its L2, so a line
+// read in pieces at different times comes from behind L2 each time: a row's
+// codes are read 128 bytes at once (a chunk of 256 columns), its scales as many
+// at a time as a lane can keep (4 lanes a row, 8 or 16 bytes each, for 2 to 8
+// chunks). A chunk's codes are requested while the one before is multiplied, and
+// pass through the wave's own LDS from lanes along a row to the product's.
+//
+// Measured: 64 rows, 151936 x 8192 in groups of 128, 240 us (660 TFLOP/s, 2.8
+// TB/s; 288 with 3 tiles a wave and scales read per chunk); in groups of 32 with
+// float32 scales, 297 us (317); 48 rows, 100003 x 4096 in groups of 32 with zero
+// points, 140 us (187). With all loads but the first taken out the products of
+// the first two take 167 and 220 us (the factors and, at small groups, the
+// scaling cost as many vector instructions as products); the loads alone 225 to
+// 250. 8 waves a compute unit are all that the registers of 5 tiles by 64 rows
+// allow, so the two overlap imperfectly. Fewer waves with more columns, or a
+// chunk's columns split over the waves, were slower (355 and 328 us).
+template <int MT, int NT, int G, bool ZEROS>
 struct StreamLds {
   static constexpr int GC = kChunkK / G;           // groups per chunk
-  static constexpr int kCodeStride = 128 + 16;     // bytes per row
-  static constexpr int kScaleStride = GC + 4;      // floats per row
-  uint4 x[2][8 * MT * 64];
-  f32x4 sum[2][GC][MT * 4];
-  u32x4 code[8][kStreamTiles][kCodeStride];        // 16 rows each
-  float scale[8][kStreamTiles][16 * kScaleStride];
-  float off[ZEROS ? 8 : 1][ZEROS ? kStreamTiles : 1][ZEROS ? 16 * kScaleStride : 1];
+  // columns whose sum is scaled at once: half a group of 128 where the registers
+  // of many tiles leave no room for more of x
+  static constexpr int C = NT > 2 && G == 128 ? 64 : G;
+  static constexpr int XS = NT > 3 ? 1 : 2;        // steps of x per buffer
+  static constexpr int kCodeStride = kChunkK / 2 + 16;  // bytes per row
+  static constexpr int kScaleStride = GC + 1;      // floats per row
+  static constexpr int kZeroStride = GC < 4 ? 4 : GC + 4;  // bytes per row
+  uint4 x[2][XS][4 * MT * 64];
+  f32x4 sum[2][XS][kStepK / C][MT * 4];
+  u32x4 code[8][NT][kCodeStride];                  // 16 rows each
+  float scale[8][NT][16 * kScaleStride];
+  uint8_t zero[ZEROS ? 8 : 1][ZEROS ? NT : 1][ZEROS ? 16 * kZeroStride : 1];
 };
 
-// NT tiles of every wave, the workgroup's from tile `base` on, over all of k.
 template <int MT, int NT, int G, int SD, bool ZEROS>
-__device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZEROS>& lds, int chunks,
-                                             int base) {
-  using Lds = StreamLds<MT, G, ZEROS>;
-  constexpr int GC = Lds::GC;
-  constexpr int SL = GC < 4 ? GC : 4;      // lanes per row of a scale load
-  constexpr int EL = GC / SL;              // scales per lane
+__global__ void __launch_bounds__(kThreads8, 2) head_stream_kernel(Args a, int chunks, int tiles) {
+  using Lds = StreamLds<MT, NT, G, ZEROS>;
+  __shared__ Lds lds;
+  constexpr int GC = Lds::GC, XS = Lds::XS, C = Lds::C;
   constexpr int kCodeStride = Lds::kCodeStride, kScaleStride = Lds::kScaleStride;
-  constexpr int XI = MT;                   // 16-byte items of x per thread
+  constexpr int kZeroStride = Lds::kZeroStride;
+  constexpr int XI = (MT + 1) / 2;         // 16-byte items of x per thread and step
   constexpr int kScaleSize = SD == QS_F32 ? 4 : 2;
-  using Raw = std::conditional_t<SD == QS_F32, float, uint16_t>;
+  constexpr int EL = (G == 32 ? 16 : 8) / kScaleSize;  // scales per lane: 4 lanes a row
+  constexpr int R = 4 * EL / GC;           // chunks that a block of scales lasts
+  constexpr int SW = EL * kScaleSize / 4, ZW = (EL + 3) / 4;  // their registers
+  using Raw = std::conditional_t<SD == QS_F32, uint32_t, uint16_t>;
   const int tid = threadIdx.x;
   const int w = uni(tid >> 6);
   const int lane = lane_id();
@@ -382,247 +398,286 @@ __device__ __forceinline__ void stream_tiles(const Args& a, StreamLds<MT, G, ZER
   const int row0 = (int)blockIdx.y * kMaxRows;
   const int rows_x = min(a.B - row0, MT * 16);
 
-  // x: 32 lanes along a row's chunk, 16 rows at a time
-  const int xc = tid & 31, xm = tid >> 5;
-  uint4 xv[XI];
-  auto load_x = [&](int chunk) {
-    const int k = chunk * kChunkK + xc * 8;
+  // x: 16 lanes along a row's step, 32 rows at a time
+  const int xc = tid & 15, xm = tid >> 4;
+  uint4 xv[XS][XI];
+  auto load_x = [&](int step) {
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const int m = xm + 16 * i;
-      xv[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (m < rows_x && k < a.K)
-        xv[i] = *reinterpret_cast<const uint4*>(a.hidden + (size_t)(row0 + m) * a.hidden_stride + k);
+    for (int s = 0; s < XS; ++s) {
+      const int k = (step + s) * kStepK + xc * 8;
+#pragma unroll
+      for (int i = 0; i < XI; ++i) {
+        const int m = xm + 32 * i;
+        xv[s][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (m < rows_x && k < a.K)
+          xv[s][i] =
+              *reinterpret_cast<const uint4*>(a.hidden + (size_t)(row0 + m) * a.hidden_stride + k);
+      }
     }
   };
-  // where item c (8 columns) of a chunk goes: step p, product j, lane group g;
-  // within the product's 64 places rows are turned by 4 g + j, so that neither
-  // these writes nor the reads meet in a bank
-  const int xp = xc >> 4, xs = xc & 15;
-  const int xj = G == 128 ? xs & 3 : G == 64 ? (xs >> 3) * 2 + (xs & 1) : xs >> 2;
-  const int xg = G == 128 ? xs >> 2 : G == 64 ? (xs >> 1) & 3 : xs & 3;
-  auto place = [](int p, int j, int t, int g, int m) {
-    return ((p * 4 + j) * MT + t) * 64 + g * 16 + ((m + 4 * g + j) & 15);
+  // where item c (8 columns) of a step goes: product j, lane group g; within the
+  // product's 64 places rows are turned by 4 g + j, so that neither these writes
+  // nor the reads meet in a bank
+  const int xj = C == 128 ? xc & 3 : C == 64 ? (xc >> 3) * 2 + (xc & 1) : xc >> 2;
+  const int xg = C == 128 ? xc >> 2 : C == 64 ? (xc >> 1) & 3 : xc & 3;
+  auto place = [](int j, int t, int g, int m) {
+    return (j * MT + t) * 64 + g * 16 + ((m + 4 * g + j) & 15);
   };
   auto store_x = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const uint32_t q[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
-      float sum = 0.0f;
+    for (int s = 0; s < XS; ++s) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sum += __uint_as_float(q[e] << 16) + __uint_as_float(q[e] & 0xFFFF0000u);
-      sum += __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(sum)));
-      sum += __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(sum)));
-      if constexpr (G >= 64) sum += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(sum)));
-      if constexpr (G == 128) sum += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(sum)));
-      lds.x[buf][place(xp, xj, i, xg, xm)] = ordered(xv[i]);
-      if ((xc & (G / 8 - 1)) == 0)
-        reinterpret_cast<float*>(lds.sum[buf][xc / (G / 8)])[xm + 16 * i] =
-            ZEROS ? sum : -24.0f * sum;
+      for (int i = 0; i < XI; ++i) {
+        const int m = xm + 32 * i;
+        const uint32_t q[4] = {xv[s][i].x, xv[s][i].y, xv[s][i].z, xv[s][i].w};
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum += __uint_as_float(q[e] << 16) + __uint_as_float(q[e] & 0xFFFF0000u);
+        sum += __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(sum)));
+        sum += __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(sum)));
+        if constexpr (C >= 64)
+          sum += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(sum)));
+        if constexpr (C == 128) sum += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(sum)));
+        if (MT > 1 || m < 16) {
+          lds.x[buf][s][place(xj, m >> 4, xg, m & 15)] = ordered(xv[s][i]);
+          if ((xc & (C / 8 - 1)) == 0)
+            reinterpret_cast<float*>(lds.sum[buf][s][xc / (C / 8)])[m] =
+                ZEROS ? sum : -24.0f * sum;
+        }
+      }
     }
   };
 
+  // codes: 8 lanes along the 128 bytes of a row, 8 rows a load; scales and zero
+  // points: 4 lanes a row
   const int c_row = lane >> 3, c_part = lane & 7;
-  const int g_row = min(lane / SL, 15), g_part = (lane % SL) * EL;
+  const int g_row = lane >> 2, g_part = (lane & 3) * EL;
   const Pattern pattern;
-
-  const int first = base + w * NT;
+  int first = 0;
   u32x4 code[NT][2];
-  Raw scale[NT][EL];
-  uint8_t zero[NT][EL];
-  auto load_weights = [&](int chunk) {
-    const int k0 = chunk * kChunkK;
-    const bool c_in = k0 + c_part * 32 < a.K;
-    const int g = k0 / G, groups = min(GC, a.K / G - g);
+  uint32_t scale[NT][SW];
+  uint32_t zero[NT][ZW];
+  // past the last tile: the last row again, never stored
+  auto load_codes = [&](int chunk) {
+    // past the row's end: its last bytes again, against hidden values of 0
+    const uint32_t col = (uint32_t)min(chunk * (kChunkK / 2) + c_part * 16, a.K / 2 - 16);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      // past the last tile: the last row again, never stored
       const int v0 = min((first + i) * 16, a.V - 1), rows = min(15, a.V - 1 - v0);
-      const uint8_t* const pc = a.codes + (size_t)v0 * a.codes_stride + (k0 >> 1);
+      const uint8_t* const pc = a.codes + (size_t)v0 * a.codes_stride;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t at = (uint32_t)min(h * 8 + c_row, rows) * (uint32_t)a.codes_stride +
-                            (uint32_t)c_part * 16u;
-        if (c_in) code[i][h] = *reinterpret_cast<const u32x4*>(pc + at);
+        const uint32_t at =
+            (uint32_t)min(h * 8 + c_row, rows) * (uint32_t)a.codes_stride + col;
+        code[i][h] = *reinterpret_cast<const u32x4*>(pc + at);
       }
-      const uint8_t* const ps = static_cast<const uint8_t*>(a.scales) +
-                                ((size_t)v0 * a.scale_stride + g) * kScaleSize;
+    }
+  };
+  int g_first = 0;  // the first group a lane holds
+  auto load_scales = [&](int chunk) {
+    const int groups = a.K / G;
+    g_first = max(min(chunk * GC + g_part, groups - EL), 0);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int v0 = min((first + i) * 16, a.V - 1), rows = min(15, a.V - 1 - v0);
+      const uint8_t* const ps =
+          static_cast<const uint8_t*>(a.scales) + (size_t)v0 * a.scale_stride * kScaleSize;
       const uint32_t row = (uint32_t)min(g_row, rows);
-      const uint32_t at = (row * (uint32_t)a.scale_stride + (uint32_t)g_part) * kScaleSize;
-      const uint8_t* const pz = ZEROS ? a.zeros + (size_t)v0 * a.zero_stride + g : nullptr;
-      const uint32_t zat = row * (uint32_t)a.zero_stride + (uint32_t)g_part;
-      if (groups == GC) {
-        __builtin_memcpy(scale[i], ps + at, kScaleSize * EL);
-        if constexpr (ZEROS) __builtin_memcpy(zero[i], pz + zat, EL);
-      } else {
+      const uint32_t at = (row * (uint32_t)a.scale_stride + (uint32_t)g_first) * kScaleSize;
+      const uint8_t* const pz = ZEROS ? a.zeros + (size_t)v0 * a.zero_stride : nullptr;
+      const uint32_t zat = row * (uint32_t)a.zero_stride + (uint32_t)g_first;
+      if (groups >= EL) {
+        __builtin_memcpy(scale[i], ps + at, 4 * SW);
+        if constexpr (ZEROS && EL == 2) {
+          uint16_t z;
+          __builtin_memcpy(&z, pz + zat, 2);
+          zero[i][0] = z;
+        } else if constexpr (ZEROS) {
+          __builtin_memcpy(zero[i], pz + zat, EL);
+        }
+      } else {  // fewer groups than a lane holds: the last one again
+#pragma unroll
+        for (int k = 0; k < SW; ++k) scale[i][k] = 0u;
+#pragma unroll
+        for (int k = 0; k < ZW; ++k) zero[i][k] = 0u;
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
-          scale[i][e] = Raw(0);
-          zero[i][e] = 0;
-          if (g_part + e < groups) {
-            scale[i][e] = reinterpret_cast<const Raw*>(ps + at)[e];
-            if constexpr (ZEROS) zero[i][e] = pz[zat + e];
-          }
+          const int k = min(e, groups - 1);
+          const uint32_t sc = *reinterpret_cast<const Raw*>(ps + k * kScaleSize + at);
+          scale[i][e * kScaleSize / 4] |= SD == QS_F32 ? sc : sc << (16 * (e & 1));
+          if constexpr (ZEROS) zero[i][e / 4] |= (uint32_t)*(pz + k + zat) << (8 * (e & 3));
         }
       }
     }
   };
 
-  f32x4 y[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-#pragma unroll
-    for (int t = 0; t < MT; ++t) y[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  __syncthreads();  // the round before has read its last chunk
-  load_x(0);
-  load_weights(0);
-  store_x(0);
-  if (chunks > 1) load_x(1);
-  for (int chunk = 0; chunk < chunks; ++chunk) {
-    const int buf = chunk & 1;
-    // this chunk's codes through LDS: from lanes along a row to the product's
+  for (int base = (int)blockIdx.x * 8 * NT; base < tiles; base += (int)gridDim.x * 8 * NT) {
+    first = base + w * NT;
+    f32x4 y[NT][MT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      uint8_t* const turn = reinterpret_cast<uint8_t*>(lds.code[w][i]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4*>(turn + (h * 8 + c_row) * kCodeStride + c_part * 16) = code[i][h];
-#pragma unroll
-      for (int e = 0; e < EL; ++e) {
-        float sc;
-        if constexpr (SD == QS_F32) sc = scale[i][e];
-        else sc = __uint_as_float((uint32_t)scale[i][e] << 16);
-        lds.scale[w][i][g_row * kScaleStride + g_part + e] = sc;
-        if constexpr (ZEROS)
-          lds.off[w][i][g_row * kScaleStride + g_part + e] = -16.0f - (float)zero[i][e];
-      }
+      for (int t = 0; t < MT; ++t) y[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (chunk + 1 < chunks) load_weights(chunk + 1);
-    __syncthreads();  // x of this chunk is in place, the other buffer is free
-    if (chunk + 1 < chunks) {
-      store_x(buf ^ 1);
-      if (chunk + 2 < chunks) load_x(chunk + 2);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      uint32_t q[NT][4];
+    load_x(0);
+    load_scales(0);
+    load_codes(0);
+    __syncthreads();  // the round before has read its last step
+    store_x(0);
+    load_x(XS);
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      // this chunk's codes, scales and zero points through LDS: from lanes along a
+      // row to the product's
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const uint8_t* const row =
-            reinterpret_cast<const uint8_t*>(lds.code[w][i]) + n * kCodeStride + p * 64;
-        if constexpr (G == 128) {
-          *reinterpret_cast<u32x4*>(q[i]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
-        } else if constexpr (G == 64) {
-          *reinterpret_cast<uint2*>(q[i]) = *reinterpret_cast<const uint2*>(row + kg * 8);
-          *reinterpret_cast<uint2*>(q[i] + 2) = *reinterpret_cast<const uint2*>(row + 32 + kg * 8);
-        } else {
+        uint8_t* const turn = reinterpret_cast<uint8_t*>(lds.code[w][i]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q[i][j] = *reinterpret_cast<const uint32_t*>(row + j * 16 + kg * 4);
-        }
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<u32x4*>(turn + (h * 8 + c_row) * kCodeStride + c_part * 16) =
+              code[i][h];
       }
 #pragma unroll
-      for (int g = 0; g < GC / 2; ++g) {
-        constexpr int J = G / 32;
-        const int gi = p * (GC / 2) + g;
-        bf16x8 x[J][MT];
-        f32x4 sum[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          sum[t] = lds.sum[buf][gi][t * 4 + kg];
-#pragma unroll
-          for (int jj = 0; jj < J; ++jj)
-            x[jj][t] = __builtin_bit_cast(bf16x8, lds.x[buf][place(p, g * J + jj, t, kg, n)]);
-        }
+      for (int e = 0; e < EL; ++e) {
+        // groups of other chunks go to the row's spare place
+        const uint32_t part = min((uint32_t)(g_first + e - chunk * GC), (uint32_t)GC);
+        const uint32_t to = (uint32_t)g_row * kScaleStride + part;
+        const uint32_t zto = (uint32_t)g_row * kZeroStride + part;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const float sc = lds.scale[w][i][n * kScaleStride + gi];
-          f32x4 acc[MT];
+          uint32_t sc = scale[i][e * kScaleSize / 4];
+          if constexpr (SD != QS_F32) sc = (e & 1) ? sc & 0xFFFF0000u : sc << 16;
+          lds.scale[w][i][to] = __uint_as_float(sc);
+          if constexpr (ZEROS) lds.zero[w][i][zto] = (uint8_t)(zero[i][e / 4] >> (8 * (e & 3)));
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      load_codes(chunk + 1);
+      if ((chunk + 1) % R == 0) load_scales(chunk + 1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int buf = XS == 1 ? p : chunk & 1;
+        if (p % XS == 0) {
+          __syncthreads();  // x of this step is in place, the other buffer is free
+          store_x(buf ^ 1);
+          load_x(chunk * 2 + p + 2 * XS);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        constexpr int J = C / 32;
+        // a tile's codes of a group, its scale and its offset, one tile ahead
+        uint32_t q[2][J];
+        float sc[2], off[2];
+        auto read = [&](int at, int g, int i) {
+          const uint8_t* const row =
+              reinterpret_cast<const uint8_t*>(lds.code[w][i]) + n * kCodeStride + p * 64;
+          if constexpr (C == 128) {
+            *reinterpret_cast<u32x4*>(q[at]) = *reinterpret_cast<const u32x4*>(row + kg * 16);
+          } else if constexpr (C == 64) {
+            *reinterpret_cast<uint2*>(q[at]) =
+                *reinterpret_cast<const uint2*>(row + g * 32 + kg * 8);
+          } else {
+            q[at][0] = *reinterpret_cast<const uint32_t*>(row + g * 16 + kg * 4);
+          }
+          sc[at] = lds.scale[w][i][n * kScaleStride + (p * kStepK + g * C) / G];
+          if constexpr (ZEROS)
+            off[at] = -16.0f - (float)lds.zero[w][i][n * kZeroStride + (p * kStepK + g * C) / G];
+        };
+        read(0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < kStepK / C; ++g) {
+          bf16x8 x[J][MT];
+          f32x4 sum[MT];
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            acc[t] = sum[t];
-            if constexpr (ZEROS) acc[t] *= lds.off[w][i][n * kScaleStride + gi];
+            sum[t] = lds.sum[buf][p % XS][g][t * 4 + kg];
+#pragma unroll
+            for (int jj = 0; jj < J; ++jj)
+              x[jj][t] =
+                  __builtin_bit_cast(bf16x8, lds.x[buf][p % XS][place(g * J + jj, t, kg, n)]);
           }
 #pragma unroll
-          for (int jj = 0; jj < J; ++jj) {
-            const bf16x8 f = factors(q[i][g * J + jj], pattern);
+          for (int i = 0; i < NT; ++i) {
+            const int at = (g * NT + i) & 1;
+            if (i + 1 < NT) read(at ^ 1, g, i + 1);
+            else if (g + 1 < kStepK / C) read(at ^ 1, g + 1, 0);
+            f32x4 acc[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[jj][t], f, acc[t], 0, 0, 0);
-          }
+            for (int t = 0; t < MT; ++t) {
+              acc[t] = sum[t];
+              if constexpr (ZEROS) acc[t] *= off[at];
+            }
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
+            for (int jj = 0; jj < J; ++jj) {
+              const bf16x8 f = factors(q[at][jj], pattern);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[i][t][e] += sc * acc[t][e];
+              for (int t = 0; t < MT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[jj][t], f, acc[t], 0, 0, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[i][t][e] += sc[at] * acc[t][e];
+              asm volatile("" : "+v"(y[i][t]));  // added here, not when all products are done
+            }
+            if (MT * NT > 6) __builtin_amdgcn_sched_barrier(0);
           }
         }
-        if (MT * NT > 6 && (g & 1)) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int v = (first + i) * 16 + n;
+    int m0 = kg * 4;
+    asm volatile("" : "+v"(m0));  // the rows' addresses are not kept over the loop
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int m = t * 16 + kg * 4 + e;
-        if (v < a.V && m < rows_x) store_logit(a, row0 + m, v, y[i][t][e]);
+        const int m = t * 16 + m0 + e;
+        if (m < rows_x) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const int v = (first + i) * 16 + n;
+            if (v < a.V) store_logit(a, row0 + m, v, y[i][t][e]);
+          }
+        }
       }
     }
   }
-}
-
-// A workgroup has `full` * NT + REST tiles for each of its waves.
-template <int MT, int NT, int REST, int G, int SD, bool ZEROS>
-__global__ void __launch_bounds__(kThreads8, 2)
-    head_stream_kernel(Args a, int chunks, int full) {
-  __shared__ StreamLds<MT, G, ZEROS> lds;
-  int base = (int)blockIdx.x * 8 * (full * NT + REST);
-  for (int i = 0; i < full; ++i, base += 8 * NT)
-    stream_tiles<MT, NT, G, SD, ZEROS>(a, lds, chunks, base);
-  if constexpr (REST > 0) stream_tiles<MT, REST, G, SD, ZEROS>(a, lds, chunks, base);
 }
 
 template <int MT, int G, int SD, bool ZEROS>
 hipError_t launch_stream(const Args& a, hipStream_t st) {
   const int chunks = (a.K + kChunkK - 1) / kChunkK;
   const int tiles = (a.V + 15) / 16;
-  // the same number of tiles for every wave of (at most) one workgroup per
-  // compute unit
-  const int per_wave = (tiles + 256 * 8 - 1) / (256 * 8);
-  const int grid = (tiles + 8 * per_wave - 1) / (8 * per_wave);
   const int blocks = (a.B + kMaxRows - 1) / kMaxRows;
-  auto run = [&](auto* kernel, int full) {
+  // tiles per wave: the fewest rounds of (at most) one workgroup per compute
+  // unit, a round taking as long as its tiles and one more
+  int nt = 1;
+  auto rounds = [&](int t) { return (tiles + 256 * 8 * t - 1) / (256 * 8 * t); };
+  for (int t = 2; t <= kMaxTiles; ++t)
+    if (rounds(t) * (t + 1) < rounds(nt) * (nt + 1)) nt = t;
+  const int grid = min(256, (tiles + 8 * nt - 1) / (8 * nt));
+  auto run = [&](auto* kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid, (unsigned)blocks), dim3(kThreads8), 0, st, a,
-                       chunks, full);
+                       chunks, tiles);
     return hipGetLastError();
   };
-  if (per_wave == 1) return run(head_stream_kernel<MT, 1, 0, G, SD, ZEROS>, 1);
-  if (per_wave == 2) return run(head_stream_kernel<MT, 2, 0, G, SD, ZEROS>, 1);
-  if (per_wave % 3 == 0) return run(head_stream_kernel<MT, 3, 0, G, SD, ZEROS>, per_wave / 3);
-  if (per_wave % 3 == 1) return run(head_stream_kernel<MT, 3, 1, G, SD, ZEROS>, per_wave / 3);
-  return run(head_stream_kernel<MT, 3, 2, G, SD, ZEROS>, per_wave / 3);
+  if (nt == 1) return run(head_stream_kernel<MT, 1, G, SD, ZEROS>);
+  if (nt == 2) return run(head_stream_kernel<MT, 2, G, SD, ZEROS>);
+  if (nt == 3) return run(head_stream_kernel<MT, 3, G, SD, ZEROS>);
+  if (nt == 4) return run(head_stream_kernel<MT, 4, G, SD, ZEROS>);
+  return run(head_stream_kernel<MT, 5, G, SD, ZEROS>);
 }
 
 template <int G, int SD, bool ZEROS>
 hipError_t pick(const Args& a, hipStream_t st) {
   if (a.B <= 16 && a.K <= 8192) return pick_steps<1, G, SD, ZEROS>(a, st);
   if (a.B <= 16) return launch_stream<1, G, SD, ZEROS>(a, st);
-  // 17 to 32 rows: in registers up to 4096 columns (32 rows, 151936 x 4096: 85 to
-  // 90 us against 92 to 94; 5000 x 4096: 17 against 23). Short rows of a large
-  // vocabulary are a draw (24 rows, 151936 x 2048: 52 us either way) and stay with
-  // the kernel that keeps x in LDS.
-  if (a.B <= 32 && a.K <= 4096 && (a.K > 2048 || a.V < 16384))
-    return pick_steps<2, G, SD, ZEROS>(a, st);
+  // 17 to 32 rows: in registers up to 4096 columns where tiles are few and the
+  // slices of k fill the chip (32 rows, 5000 x 4096: 17 us against 21; 20 rows,
+  // 12000 x 2048: 14 against 16). Large vocabularies are a draw or worse (151936 x
+  // 4096: 97 us either way; in groups of 32 with zero points 162 against 139).
+  if (a.B <= 32 && a.K <= 4096 && a.V < 16384) return pick_steps<2, G, SD, ZEROS>(a, st);
   if (a.B <= 32) return launch_stream<2, G, SD, ZEROS>(a, st);
   return launch_stream<4, G, SD, ZEROS>(a, st);
 }
