@@ -91,6 +91,22 @@ CASES = [
     (29, 4003, 3968, 128, False, "bf16", "f32"),
     (24, 20001, 1024, 64, True, "bf16", "f32"),
     (16, 2100, 8192, 32, True, "bf16", "f32"),
+    # 6 to 16 rows through LDS; one to five tiles a wave; fewer groups than a lane
+    # of scales holds, and groups that end inside a block of them
+    (6, 20489, 384, 64, True, "bf16", "f32"),
+    (16, 24001, 1056, 32, True, "f32", "f32"),
+    (13, 70003, 640, 128, False, "bf16", "bf16"),
+    (64, 100001, 160, 32, True, "bf16", "f32"),
+    (40, 131077, 384, 128, True, "f32", "bf16"),
+    (33, 163841, 320, 64, False, "bf16", "bf16"),
+    (50, 150000, 96, 32, False, "f32", "f32"),
+    (20, 140001, 128, 128, True, "bf16", "f32"),
+    (64, 170003, 32, 32, True, "f32", "f32"),
+    (17, 40003, 832, 32, True, "bf16", "f32"),
+    (64, 17000, 4480, 128, True, "bf16", "f32"),
+    (34, 50001, 704, 64, True, "f32", "bf16"),
+    (64, 3, 32, 32, True, "bf16", "f32"),
+    (40, 1, 64, 64, True, "f32", "f32"),
 ]
 
 

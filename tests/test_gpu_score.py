@@ -551,3 +551,38 @@ def test_longest_row(qs):
     assert grad[0, V - 1].item() == 1.0 and grad[0, at[2]].item() == 1.0
     p = 3 * math.exp(2) / S
     assert abs(grad[0, at[1]].item() + p) <= p * 2 ** -7
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [9, 1000, 32003, 151937])
+def test_peaked_rows(qs, V, dtype):
+    """Rows that one token nearly wins alone keep relative precision: with q the
+    mass beside the largest token, log S = -ln(1 - q) has the relative error of
+    the sum of the other weights, U (depth + 8) q + 4 U X as in check_forward
+    with the one left out, and that of log1p (2 steps)."""
+    import torch
+    print(f"peaked V={V} {dtype}", flush=True)
+    rng = np.random.default_rng(V)
+    up = np.array([12.0, 16.0, 20.0, 26.0, 34.0])
+    z = rng.normal(0, 2, (5, V))
+    at = rng.integers(0, V, 5)
+    z[np.arange(5), at] = up
+    z = bf16(z)
+    tokens = np.stack((at, (at + 1) % V), 1).astype(np.int32)
+    T = np.array([1.0, 1.0, 0.7, 1.3, 1.0], np.float32)
+    _, _, _, out = run(qs, z, dtype, tokens, T=T, top_n=1)
+    o = {k: v.cpu().numpy().astype(np.float64) for k, v in out.items()}
+    for r in range(5):
+        w = oracle.score_row(z[r], None, T[r], tokens[r], 1)
+        fin = w["p"] > 0
+        X = (w["p"][fin] * -w["a"][fin]).sum()
+        X2 = (w["p"][fin] * w["a"][fin] ** 2).sum()
+        rest = np.delete(w["p"], at[r]).sum()
+        logS = np.log1p(rest / (1 - rest)) if rest < 0.5 else w["log_sum"]
+        tol = U * ((depth(V) + 8) * rest + 4 * X + 4 * logS) + 1e-37
+        assert abs(o["log_sum"][r] - logS) <= tol, (r, o["log_sum"][r], logS)
+        assert abs(o["logprobs"][r][0] + logS) <= tol
+        assert o["top_logprobs"][r][0] == o["logprobs"][r][0]
+        H = logS + X
+        t_H = tol + U * ((2 * depth(V) + 16) * X + 4 * X2 + 2 * H) + 1e-37
+        assert abs(o["entropy"][r] - H) <= t_H, (r, o["entropy"][r], H)

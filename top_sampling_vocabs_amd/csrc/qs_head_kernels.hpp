@@ -671,7 +671,15 @@ hipError_t launch_stream(const Args& a, hipStream_t st) {
 
 template <int G, int SD, bool ZEROS>
 hipError_t pick(const Args& a, hipStream_t st) {
-  if (a.B <= 16 && a.K <= 8192) return pick_steps<1, G, SD, ZEROS>(a, st);
+  // Up to 16 rows: in registers, but for 6 rows and more where a wave of the
+  // streaming kernel has one to three tiles and nearly all waves have one. There
+  // the registers' way pays for x, read by every workgroup, over few tiles (16
+  // rows, 65000 x 4096: 42 us against 33.5; 8 rows, 32000 x 2048: 15.8 against 12.1;
+  // beside it 4 rows, 56000 x 4096: 28.3 against 29.0, 16 rows, 128256 x 4096 in
+  // groups of 64: 79 against 83, 8 rows, 17000 x 4096: 16.2 against 19.1).
+  const int tiles = (a.V + 15) / 16;
+  const bool few = a.B < 6 || tiles < 1280 || tiles > 3 * 2048;
+  if (a.B <= 16 && a.K <= 8192 && few) return pick_steps<1, G, SD, ZEROS>(a, st);
   if (a.B <= 16) return launch_stream<1, G, SD, ZEROS>(a, st);
   // 17 to 32 rows: in registers up to 4096 columns where tiles are few and the
   // slices of k fill the chip (32 rows, 5000 x 4096: 17 us against 21; 20 rows,

@@ -20,6 +20,15 @@
 //   f_w = 2^((m_w - m) c).
 // Weights and E are kept in units of log 2 (one hardware exponential each).
 //
+// One maximum's own weight, exactly 1, is left out of every sum: R = S - 1 is what
+// a wave, a part and a row hold, and log S = log1p(R). The log-probability of a
+// token that is almost certain then keeps float32's relative precision (added to
+// 1, the other weights would keep 2^-24 absolutely). A wave whose S is 4 or more
+// loses nothing by the subtraction; the others take the lane of their maximum,
+// whose tokens go through LDS to as many lanes and are weighed again there
+// without the one. (2048 rows of 151936 bf16: 115 us; 119 if every wave did it,
+// 110 with the plain sum.)
+//
 // Rows of up to kRowBlock * kRowLoads loads go to one workgroup and one launch:
 // a second launch costs more than one compute unit needs for such a row. Longer
 // rows are split into parts of kPartBlock * kPartLoads loads, several of which
@@ -27,9 +36,9 @@
 // exponentials; a second launch joins the parts of each row. Where that gives
 // at most kFewParts parts they are halved, so that the chip fills evenly.
 //
-// Measured: 2048 rows of 151936 bf16, 106 us (5.9 TB/s, where a large copy
+// Measured: 2048 rows of 151936 bf16, 115 us (5.4 TB/s, where a large copy
 // reaches 4.8: bound by the reads); 256 such rows with a mask and 20 top tokens,
-// 25 us and 5.8 us for the join (3.3 TB/s: bound by the vector instructions, two
+// 28 us and 6 us for the join (2.6 TB/s: bound by the vector instructions, two
 // passes of about a dozen a token, and by the top tokens' LDS lists); one row of
 // 32000, 6 us, its latency and its launch. A workgroup per row that walks the row
 // in a loop, with one launch, was slower in every form tried (28 us against
@@ -70,12 +79,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 // What a part's workgroup leaves for the join.
 struct Part {
   float m;        // largest legal logit (-FLT_MAX if none is finite)
-  float S;        // sum of 2^((z - m) c), c = log2(e) / T; NaN if a legal z is NaN or +inf
+  float R;        // sum of 2^((z - m) c), c = log2(e) / T, without one z = m; NaN if a
+                  // legal z is NaN or +inf
   float E;        // sum of 2^((z - m) c) (z - m) c
   uint32_t any;   // a legal token exists
   uint32_t t;     // threshold: order-preserving key of a lower bound of the n-th largest z
   int32_t count;  // keys in the part's list
-  uint32_t pad[2];
+  uint32_t has;   // a legal z = m exists
+  uint32_t pad;
 };
 static_assert(sizeof(Part) == 32, "two 16-byte stores");
 
@@ -226,8 +237,8 @@ constexpr int kGroups = 256;
 struct Shared {
   uint64_t list[kListCap];
   uint4 group[kGroups / 4];  // keys of the groups' maxima
-  float m[kRowBlock / 64], S[kRowBlock / 64], E[kRowBlock / 64];
-  uint32_t any[kRowBlock / 64];
+  float m[kRowBlock / 64], R[kRowBlock / 64], E[kRowBlock / 64];
+  uint32_t any[kRowBlock / 64], has[kRowBlock / 64];
   uint64_t best[kRowBlock / 64];
   uint16_t lanes[kRowBlock];  // threads whose maximum reaches t
   int n_lanes;
@@ -256,12 +267,12 @@ __device__ __forceinline__ Given load_given(const Args& a, int r, int token) {
 }
 
 // Writes one row's outputs; called by every thread of a workgroup of `threads`,
-// with the row's joined statistics, the thread's slot, and (top_n > 0) `n_list`
-// distinct keys in LDS that hold its top tokens.
+// with the row's joined statistics (has: a finite maximum), the thread's slot, and
+// (top_n > 0) `n_list` distinct keys in LDS that hold its top tokens.
 template <int DT>
 __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int threads, float m,
-                                           float S, float E, bool any, float T, Given given,
-                                           const uint64_t* list, int n_list) {
+                                           float R, bool has, float E, bool any, float T,
+                                           Given given, const uint64_t* list, int n_list) {
   float* const lps = a.logprobs + (size_t)r * a.G;
   int bad = given.token < -1 || given.token >= a.V;
   for (int g = tid + threads; g < a.G; g += threads) {
@@ -273,15 +284,15 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, int th
   int status = QS_ROW_OK;
   if (bad || !(T > 0.0f) || T == INFINITY) status = QS_ROW_BAD_PARAM;
   else if (!any) status = QS_ROW_EMPTY;
-  else if (!(S < INFINITY)) status = QS_ROW_NONFINITE;
-  else if (S == 0.0f) status = QS_ROW_ALL_NEG_INF;
+  else if (!(R < INFINITY)) status = QS_ROW_NONFINITE;
+  else if (!has) status = QS_ROW_ALL_NEG_INF;
   const bool ok = status == QS_ROW_OK;
-  const float log_sum = ok ? logf(S) : NAN;
+  const float log_sum = ok ? log1pf(R) : NAN;
   if (tid == 0) {
     a.status[r] = status;
     a.row_max[r] = ok ? m : NAN;
     a.log_sum[r] = log_sum;
-    if (a.entropy) a.entropy[r] = ok ? log_sum - kLn2 * (E / S) : NAN;
+    if (a.entropy) a.entropy[r] = ok ? log_sum - kLn2 * (E / (1.0f + R)) : NAN;
   }
   for (int g = tid; g < a.G; g += threads) {
     if (g != tid) given = load_given<DT>(a, r, given_token(a, r, g));
@@ -323,6 +334,7 @@ __global__ void __launch_bounds__(THREADS)
   constexpr bool kTable = MASK && DT == QS_BF16;
   __shared__ Shared s;
   __shared__ uint4 s_masks[kTable ? 256 : 1];  // masks_of every byte of legal bits
+  __shared__ uint4 s_peak[kWavesHere][NL];     // tokens of the lane of a wave's maximum
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int w = tid >> 6;
@@ -425,30 +437,68 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
-  const float Sw = wave_sum_f32(S[0] + S[1]);
-  const float Ew = wave_sum_f32(E[0] + E[1]);
+  float Rw = wave_sum_f32(S[0] + S[1]), Ew = wave_sum_f32(E[0] + E[1]);
+  bool has = true;
+  if (Rw >= 4.0f || Rw != Rw) {
+    Rw -= 1.0f;
+  } else {
+    // the maximum's lane again, a load to each of the first lanes, without the one
+    const int peak = __builtin_ctzll(ballot(lane_max == wave_max));
+    if (lane == peak) {
+#pragma unroll
+      for (int u = 0; u < NL; ++u) s_peak[w][u] = v[u];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    uint4 q = masks_of<DT>(0u);
+    q = blank<DT>(q, q);  // -inf
+    if (lane < NL) q = s_peak[w][lane];
+    bool is_max = false;
+#pragma unroll
+    for (int e = 0; e < P; ++e) is_max |= token<DT>(q, e) == wave_max;
+    const uint64_t holders = ballot(is_max);
+    has = holders != 0u;
+    bool out = !has || lane != __builtin_ctzll(holders);  // the one is not here
+    float R = 0.0f, ER = 0.0f;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const float z = token<DT>(q, e), d = (z - wave_max) * c;
+      const bool one = !out && z == wave_max;
+      const float x = one ? 0.0f : exp2_hw(d);
+      R += x;
+      ER = fmaf(x, fmaxf(d, -200.0f), ER);
+      out |= one;
+    }
+    Rw = wave_sum_f32(lane == peak ? R : R + (S[0] + S[1]));
+    Ew = wave_sum_f32(lane == peak ? ER : ER + (E[0] + E[1]));
+  }
   const bool anyw = ballot(any != 0u) != 0;
   if (lane == 0) {
     s.m[w] = wave_max;
-    s.S[w] = Sw;
+    s.R[w] = Rw;
     s.E[w] = Ew;
     s.any[w] = anyw;
+    s.has[w] = has;
   }
   __syncthreads();
   float top = s.m[0];
-  bool any_all = s.any[0] != 0u;
+  bool any_all = s.any[0] != 0u, has_all = s.has[0] != 0u;
 #pragma unroll
   for (int k = 1; k < kWavesHere; ++k) {
     top = fmaxf(top, s.m[k]);
     any_all |= s.any[k] != 0u;
+    has_all |= s.has[k] != 0u;
   }
-  float S_all = 0.0f, E_all = 0.0f;
+  float R_all = 0.0f, E_all = 0.0f;
+  bool left_out = false;  // the one of the first wave that holds the top
 #pragma unroll
   for (int k = 0; k < kWavesHere; ++k) {
     const float d = rel(s.m[k], top, c);
-    const float f = exp2_hw(d);
-    S_all += f * s.S[k];
-    E_all += f * (s.E[k] + d * s.S[k]);
+    const float fk = exp2_hw(d), one = s.has[k] ? 1.0f : 0.0f;
+    const bool here = !left_out && s.has[k] && s.m[k] == top;
+    R_all += fk * (here ? s.R[k] : s.R[k] + one);
+    E_all += fk * (s.E[k] + d * (s.R[k] + one));
+    left_out |= here;
   }
 
   int n_list = 0;
@@ -517,18 +567,20 @@ __global__ void __launch_bounds__(THREADS)
     }
   }
   if constexpr (ROW) {
-    finish_row<DT>(a, r, tid, THREADS, top, S_all, E_all, any_all, T, given, s.list, n_list);
+    finish_row<DT>(a, r, tid, THREADS, top, R_all, has_all, E_all, any_all, T, given, s.list,
+                   n_list);
   } else {
     const size_t p = (size_t)r * parts + part;
     if (tid == 0) {
       Part out;
       out.m = top;
-      out.S = S_all;
+      out.R = R_all;
       out.E = E_all;
       out.any = any_all;
       out.t = t;
       out.count = n_list;
-      out.pad[0] = out.pad[1] = 0u;
+      out.has = has_all;
+      out.pad = 0u;
       ws_parts[p] = out;
     }
     if constexpr (TOP)
@@ -552,7 +604,7 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
   // requests that need nothing else first: the thread's slot, a part per lane,
   // and the first 64 keys of 4 lists per wave whatever their counts
   const int given_id = given_token(a, r, tid);
-  Part mine{-3.402823466e38f, 0.0f, 0.0f, 0u, 0u, 0, {0u, 0u}};
+  Part mine{-3.402823466e38f, 0.0f, 0.0f, 0u, 0u, 0, 0u, 0u};
   if (lane < parts) mine = p[lane];
   const uint64_t* const list = ws_list + (size_t)r * parts * kListCap;
   constexpr int kAhead = 4;
@@ -578,16 +630,22 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
   m = wave_max_f32(m);
   t = wave_reduce<OpMax>(t);
   const bool any_all = ballot(any != 0u) != 0;
-  const float d0 = rel(mine.m, m, c), f0 = exp2_hw(d0);
-  float S = f0 * mine.S;
-  float E = f0 * (mine.E + d0 * mine.S);
+  // a part's maximum counts 1, but for the first part's that holds the row's
+  uint32_t first = mine.has && mine.m == m ? ~(uint32_t)lane : 0u;
+  for (int k = lane + 64; k < parts; k += 64)
+    if (p[k].has && p[k].m == m) first = max(first, ~(uint32_t)k);
+  first = ~wave_reduce<OpMax>(first);
+  const bool has_all = first != ~0u;
+  const float d0 = rel(mine.m, m, c), f0 = exp2_hw(d0), one0 = mine.has ? 1.0f : 0.0f;
+  float R = f0 * ((uint32_t)lane == first ? mine.R : mine.R + one0);
+  float E = f0 * (mine.E + d0 * (mine.R + one0));
   for (int k = lane + 64; k < parts; k += 64) {
     const float d = rel(p[k].m, m, c);
-    const float f = exp2_hw(d);
-    S += f * p[k].S;
-    E += f * (p[k].E + d * p[k].S);
+    const float f = exp2_hw(d), one = p[k].has ? 1.0f : 0.0f;
+    R += f * ((uint32_t)k == first ? p[k].R : p[k].R + one);
+    E += f * (p[k].E + d * (p[k].R + one));
   }
-  S = wave_sum_f32(S);
+  R = wave_sum_f32(R);
   E = wave_sum_f32(E);
   int n_list = 0;
   if constexpr (TOP) {
@@ -641,7 +699,7 @@ __global__ void __launch_bounds__(TOP ? 256 : 64)
       __syncthreads();
     }
   }
-  finish_row<DT>(a, r, tid, kThreadsHere, m, S, E, any_all, T, given, s_list, n_list);
+  finish_row<DT>(a, r, tid, kThreadsHere, m, R, has_all, E, any_all, T, given, s_list, n_list);
 }
 
 template <int DT, int THREADS, int NL, bool ROW>
