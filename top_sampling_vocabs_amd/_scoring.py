@@ -5,14 +5,13 @@ qs_head_logits. Like the rest of the binding it only marshals arguments; it is
 loaded on first use, because it needs torch at import.
 """
 
-import contextlib
-
 import torch
 
-from ._lib import QS_BF16, QS_F32, _check_logits, _check_rowvec, _status, load, sample
+from ._lib import QS_BF16, QS_F32, _check_logits, _status, load, sample
 
 _CODES = {torch.float32: QS_F32, torch.bfloat16: QS_BF16}
-_SAME_DEVICE = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream  # a handle; no Stream object made
 
 
 def _code(t, name):
@@ -27,41 +26,44 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(device):
-    """Context in which `device` is the current one (kernels launch there)."""
-    return _SAME_DEVICE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+def _enqueue(call, index, *args):
+    """call(*args, stream) on the current torch stream of device `index`, with that
+    device the current one (kernels launch there)."""
+    if _current_device() == index:
+        return call(*args, _current_stream(index))
+    with torch.cuda.device(index):
+        return call(*args, _current_stream(index))
 
 
-def _stream(device):
-    """The handle of the device's current torch stream (no Stream object made)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _check_device(t, device, name):
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _check_vec(t, B, dtype, index, name):
+    # one test a property, the cheap ones first: most calls here are small
+    if t is None or t.dtype is not dtype or t.dim() != 1 or t.size(0) != B \
+            or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape [{B}] and {dtype} on "
+                         f"cuda:{index}")
 
 
 def _check_row_inputs(logits, tokens, temperature, bitmask):
-    """The forward and the backward call's common inputs: (B, V, G)."""
+    """The forward and the backward call's common inputs: (B, V, G, device index)."""
     B, V = _check_logits(logits, bitmask)
-    dev = logits.device
-    if bitmask is not None:
-        _check_device(bitmask, dev, "bitmask")
+    index = logits.get_device()
+    if bitmask is not None and bitmask.get_device() != index:
+        raise ValueError(f"bitmask must be on cuda:{index}, got {bitmask.device}")
     if temperature is not None:
-        _check_rowvec(temperature, B, torch.float32, "temperature")
-        _check_device(temperature, dev, "temperature")
-    if tokens.dtype != torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != B \
-            or tokens.device != dev or not tokens.is_contiguous():
-        raise ValueError(f"tokens must be a contiguous int32 tensor [B] or [B, G] on {dev}")
-    return B, V, tokens.shape[1] if tokens.dim() == 2 else 1
+        _check_vec(temperature, B, torch.float32, index, "temperature")
+    n = tokens.dim()
+    if tokens.dtype is not torch.int32 or n not in (1, 2) or tokens.size(0) != B \
+            or tokens.get_device() != index or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 tensor [B] or [B, G] on "
+                         f"cuda:{index}")
+    return B, V, tokens.size(1) if n == 2 else 1, index
 
 
 def _padded_rows(B, V, dtype, device):
     """[B, V] uninitialised, rows starting 16 bytes aligned."""
-    over = -V % (4 if dtype == torch.float32 else 8)
-    t = torch.empty((B, V + over), dtype=dtype, device=device)
-    return t[:, :V] if over else t
+    width = V + -V % (4 if dtype is torch.float32 else 8)
+    t = torch.empty((B, width), dtype=dtype, device=device)
+    return t if width == V else t.as_strided((B, V), (width, 1))
 
 
 def token_logprobs_workspace_for(logits, top_n=0):
@@ -88,19 +90,20 @@ def token_logprobs(logits, tokens, *, temperature=None, bitmask=None, entropy=Fa
     graph, drop every eager autograd graph of the same leaves first, as torch
     asks for all backward passes, or capture token_logprobs_backward itself.
     """
-    B, V, G = _check_row_inputs(logits, tokens, temperature, bitmask)
+    shape = _check_row_inputs(logits, tokens, temperature, bitmask)
     if workspace is not None:
         _check_device(workspace, logits.device, "workspace")
     if logits.requires_grad and torch.is_grad_enabled():
-        keys, *out = _TokenLogprobs.apply(logits, tokens, temperature, bitmask, B, V, G, entropy,
+        keys, *out = _TokenLogprobs.apply(logits, tokens, temperature, bitmask, shape, entropy,
                                           int(top_n), workspace)
         return dict(zip(keys, out))
-    return _forward(logits, tokens, temperature, bitmask, B, V, G, entropy, top_n, workspace)
+    return _forward(logits, tokens, temperature, bitmask, shape, entropy, top_n, workspace)
 
 
-def _forward(logits, tokens, temperature, bitmask, B, V, G, entropy, top_n, workspace):
+def _forward(logits, tokens, temperature, bitmask, shape, entropy, top_n, workspace):
     lib = load()
     dev = logits.device
+    B, V, G, index = shape
     code = _code(logits, "logits")
     lps = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
     # the values per row in one allocation
@@ -118,14 +121,13 @@ def _forward(logits, tokens, temperature, bitmask, B, V, G, entropy, top_n, work
         n = lib.qs_token_logprobs_workspace_bytes(B, V, code, top_n)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        rc = lib.qs_token_logprobs(
-            logits.data_ptr(), code, B, V, logits.stride(0), _addr(temperature), _addr(bitmask),
-            0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G, lps.data_ptr(),
-            row_max.data_ptr(), log_sum.data_ptr(), ent[0].data_ptr() if entropy else None,
-            top_n, _addr(ids), _addr(tops), status.data_ptr(), _addr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(dev))
+    rc = _enqueue(
+        lib.qs_token_logprobs, index,
+        logits.data_ptr(), code, B, V, logits.stride(0), _addr(temperature), _addr(bitmask),
+        0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G, lps.data_ptr(),
+        row_max.data_ptr(), log_sum.data_ptr(), ent[0].data_ptr() if entropy else None,
+        top_n, _addr(ids), _addr(tops), status.data_ptr(), _addr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size())
     if rc:
         _status(rc, "qs_token_logprobs")
     return out
@@ -142,32 +144,31 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
     Returns grad_logits [B, V] in the logits' dtype (0 on rows whose status is
     not ROW_OK); out: where to write it (it may be logits itself).
     """
-    B, V, G = _check_row_inputs(logits, tokens, temperature, bitmask)
-    dev = logits.device
+    B, V, G, index = _check_row_inputs(logits, tokens, temperature, bitmask)
     if (entropy is None) != (grad_entropy is None):
         raise ValueError("entropy and grad_entropy go together")
-    for t, dtype, name in ((row_max, torch.float32, "row_max"), (log_sum, torch.float32, "log_sum"),
-                           (status, torch.int32, "status"), (entropy, torch.float32, "entropy"),
-                           (grad_entropy, torch.float32, "grad_entropy")):
-        if t is not None or name not in ("entropy", "grad_entropy"):
-            _check_rowvec(t, B, dtype, name)
-            _check_device(t, dev, name)
-    if grad_logprobs.shape != tokens.shape or grad_logprobs.dtype != torch.float32 \
-            or grad_logprobs.device != dev or not grad_logprobs.is_contiguous():
+    _check_vec(row_max, B, torch.float32, index, "row_max")
+    _check_vec(log_sum, B, torch.float32, index, "log_sum")
+    _check_vec(status, B, torch.int32, index, "status")
+    if entropy is not None:
+        _check_vec(entropy, B, torch.float32, index, "entropy")
+        _check_vec(grad_entropy, B, torch.float32, index, "grad_entropy")
+    if grad_logprobs.dtype is not torch.float32 or grad_logprobs.shape != tokens.shape \
+            or grad_logprobs.get_device() != index or not grad_logprobs.is_contiguous():
         raise ValueError("grad_logprobs must be a contiguous float32 tensor in the shape of "
-                         f"tokens on {dev}")
+                         f"tokens on cuda:{index}")
     if out is None:
-        out = _padded_rows(B, V, logits.dtype, dev)
-    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev \
-            or out.stride(1) != 1:
+        out = _padded_rows(B, V, logits.dtype, logits.device)
+    elif out.shape != logits.shape or out.dtype is not logits.dtype \
+            or out.get_device() != index or out.stride(1) != 1:
         raise ValueError("out must have the logits' shape, dtype and device "
                          "and unit column stride")
-    with _on(dev):
-        rc = load().qs_token_logprobs_backward(
-            logits.data_ptr(), _code(logits, "logits"), B, V, logits.stride(0), _addr(temperature),
-            _addr(bitmask), 0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G,
-            row_max.data_ptr(), log_sum.data_ptr(), status.data_ptr(), grad_logprobs.data_ptr(),
-            _addr(entropy), _addr(grad_entropy), out.data_ptr(), out.stride(0), _stream(dev))
+    rc = _enqueue(
+        load().qs_token_logprobs_backward, index,
+        logits.data_ptr(), _code(logits, "logits"), B, V, logits.stride(0), _addr(temperature),
+        _addr(bitmask), 0 if bitmask is None else bitmask.stride(0), tokens.data_ptr(), G,
+        row_max.data_ptr(), log_sum.data_ptr(), status.data_ptr(), grad_logprobs.data_ptr(),
+        _addr(entropy), _addr(grad_entropy), out.data_ptr(), out.stride(0))
     if rc:
         _status(rc, "qs_token_logprobs_backward")
     return out
@@ -178,8 +179,8 @@ class _TokenLogprobs(torch.autograd.Function):
     gradient to the logits."""
 
     @staticmethod
-    def forward(ctx, logits, tokens, temperature, bitmask, B, V, G, entropy, top_n, workspace):
-        out = _forward(logits, tokens, temperature, bitmask, B, V, G, entropy, top_n, workspace)
+    def forward(ctx, logits, tokens, temperature, bitmask, shape, entropy, top_n, workspace):
+        out = _forward(logits, tokens, temperature, bitmask, shape, entropy, top_n, workspace)
         ctx.keys = tuple(out)
         ctx.save_for_backward(logits, tokens, temperature, bitmask, out["row_max"],
                               out["log_sum"], out["status"], out.get("entropy"))
@@ -195,7 +196,7 @@ class _TokenLogprobs(torch.autograd.Function):
         g = dict(zip(ctx.keys, grads))
         g_lp, g_ent = g["logprobs"], g.get("entropy")
         if g_lp is None and g_ent is None:
-            return (None,) * 10
+            return (None,) * 8
         if g_lp is None:
             g_lp = torch.zeros(tokens.shape, dtype=torch.float32, device=tokens.device)
         grad = token_logprobs_backward(
@@ -203,7 +204,7 @@ class _TokenLogprobs(torch.autograd.Function):
             temperature=temperature, bitmask=bitmask,
             entropy=None if g_ent is None else ent,
             grad_entropy=None if g_ent is None else g_ent.contiguous())
-        return (grad,) + (None,) * 9
+        return (grad,) + (None,) * 7
 
 
 def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
@@ -217,38 +218,39 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
     them. Enqueued on the current stream. Inference only: tensors that require
     a gradient are refused.
     """
-    if hidden.dim() != 2 or not hidden.is_cuda or hidden.dtype != torch.bfloat16 \
+    if hidden.dtype is not torch.bfloat16 or hidden.dim() != 2 or not hidden.is_cuda \
             or hidden.stride(1) != 1:
         raise ValueError("hidden must be a bfloat16 CUDA tensor [B, K] with unit column stride")
-    dev = hidden.device
+    index = hidden.get_device()
     B, K = hidden.shape
-    if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.shape[1] * 2 != K \
-            or codes.stride(1) != 1 or codes.device != dev:
-        raise ValueError(f"codes must be a uint8 tensor [V, K/2] with unit column stride on {dev}")
-    V = codes.shape[0]
-    groups = scales.shape[1] if scales.dim() == 2 else 0
-    if groups < 1 or scales.shape[0] != V or K % groups or K // groups not in (32, 64, 128) \
-            or scales.stride(1) != 1 or scales.device != dev:
+    if codes.dtype is not torch.uint8 or codes.dim() != 2 or codes.size(1) * 2 != K \
+            or codes.stride(1) != 1 or codes.get_device() != index:
+        raise ValueError("codes must be a uint8 tensor [V, K/2] with unit column stride on "
+                         f"cuda:{index}")
+    V = codes.size(0)
+    groups = scales.size(1) if scales.dim() == 2 else 0
+    if groups < 1 or scales.size(0) != V or K % groups or K // groups not in (32, 64, 128) \
+            or scales.stride(1) != 1 or scales.get_device() != index:
         raise ValueError("scales must be [V, K/group] with group 32, 64 or 128 "
-                         f"and unit column stride on {dev}")
-    if zeros is not None and (zeros.shape != scales.shape or zeros.dtype != torch.uint8
-                              or zeros.stride(1) != 1 or zeros.device != dev):
-        raise ValueError(f"zeros must be a uint8 tensor in the shape of scales on {dev}")
+                         f"and unit column stride on cuda:{index}")
+    if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != scales.shape
+                              or zeros.stride(1) != 1 or zeros.get_device() != index):
+        raise ValueError(f"zeros must be a uint8 tensor in the shape of scales on cuda:{index}")
     if (hidden.requires_grad or scales.requires_grad) and torch.is_grad_enabled():
         raise ValueError("head_logits has no gradient: call it under torch.no_grad() "
                          "or on detached tensors")
     if out is None:
-        out = _padded_rows(B, V, dtype or torch.bfloat16, dev)
-    elif out.shape != (B, V) or out.stride(1) != 1 or out.device != dev \
-            or (dtype is not None and out.dtype != dtype):
+        out = _padded_rows(B, V, dtype or torch.bfloat16, hidden.device)
+    elif out.shape != (B, V) or out.stride(1) != 1 or out.get_device() != index \
+            or (dtype is not None and out.dtype is not dtype):
         raise ValueError("out must be [B, V] in the asked dtype with unit column stride "
-                         f"on {dev}")
-    with _on(dev):
-        rc = load().qs_head_logits(
-            hidden.data_ptr(), B, K, hidden.stride(0) if B > 1 else K, codes.data_ptr(), V, codes.stride(0),
-            scales.data_ptr(), _code(scales, "scales"), scales.stride(0), _addr(zeros),
-            0 if zeros is None else zeros.stride(0), K // groups, out.data_ptr(),
-            _code(out, "out"), out.stride(0), _stream(dev))
+                         f"on cuda:{index}")
+    rc = _enqueue(
+        load().qs_head_logits, index,
+        hidden.data_ptr(), B, K, hidden.stride(0) if B > 1 else K, codes.data_ptr(), V,
+        codes.stride(0), scales.data_ptr(), _code(scales, "scales"), scales.stride(0),
+        _addr(zeros), 0 if zeros is None else zeros.stride(0), K // groups, out.data_ptr(),
+        _code(out, "out"), out.stride(0))
     if rc:
         _status(rc, "qs_head_logits")
     return out

@@ -38,9 +38,9 @@
 //
 // Measured: 2048 rows of 151936 bf16, 115 us (5.4 TB/s, where a large copy
 // reaches 4.8: bound by the reads); 256 such rows with a mask and 20 top tokens,
-// 28 us and 6 us for the join (2.6 TB/s: bound by the vector instructions, two
-// passes of about a dozen a token, and by the top tokens' LDS lists); one row of
-// 32000, 6 us, its latency and its launch. A workgroup per row that walks the row
+// 33 us, 6 of them the join (2.6 TB/s: bound by the vector instructions, about a
+// dozen a token, and by the top tokens' LDS lists); one row of 32000, 8 us, its
+// latency. A workgroup per row that walks the row
 // in a loop, with one launch, was slower in every form tried (28 us against
 // 24 + 5.6 for the 256 rows; 21 against 11 + 4.6 for 64 rows of 128256 fp32).
 //
