@@ -122,6 +122,27 @@ def test_against_oracle(qs, case):
     check(x, codes, s, z, group, got, out)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("B", [1, 12, 30, 64])
+def test_nothing_left_from_before(qs, B, group):
+    """Groups past the row's end, in rows of one short chunk and of several, do not
+    see what an earlier call left on chip: here NaN and infinite scales."""
+    import torch
+    print(f"head leftovers B={B} group={group}", flush=True)
+    V = 24001
+    x, codes, s, z = (t.cuda() for t in make(3, B, V, 512, group, True, "f32"))
+    for K in (group, 256 + group, 384):
+        if K % group:
+            continue
+        for fill in (float("nan"), float("inf")):
+            qs.head_logits(x, codes, torch.full_like(s, fill), z, dtype=torch.float32)
+            got = qs.head_logits(x[:, :K], codes[:, :K // 2], s[:, :K // group], z[:, :K // group],
+                                 dtype=torch.float32)
+            torch.cuda.synchronize()
+            check(x[:, :K].cpu(), codes[:, :K // 2].cpu(), s[:, :K // group].cpu(),
+                  z[:, :K // group].cpu(), group, got, "f32")
+
+
 @pytest.mark.parametrize("B", [1, 6, 20, 64])
 def test_strides_and_padding(qs, B):
     """Row strides of every operand; rows and columns around the result stay."""

@@ -551,6 +551,17 @@ __global__ void __launch_bounds__(kThreads8, 2) head_stream_kernel(Args a, int c
           if constexpr (ZEROS) lds.zero[w][i][zto] = (uint8_t)(zero[i][e / 4] >> (8 * (e & 3)));
         }
       }
+      const int left = a.K / G - chunk * GC;  // groups of the row's last chunk
+      if (left < GC) {
+        // a scale of 0 behind them: what LDS held could be an infinity, which would
+        // make a NaN of the hidden values' 0
+        int at = n * kScaleStride + left + kg;
+        asm volatile("" : "+v"(at));  // worked out here, not kept over the loop
+        for (int g = left + kg; g < GC; g += 4, at += 4) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) lds.scale[w][i][at] = 0.0f;
+        }
+      }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       load_codes(chunk + 1);
