@@ -91,6 +91,13 @@ CASES = [
     (29, 4003, 3968, 128, False, "bf16", "f32"),
     (24, 20001, 1024, 64, True, "bf16", "f32"),
     (16, 2100, 8192, 32, True, "bf16", "f32"),
+    # 16 slices of k: full, nearly full, a last one empty
+    (16, 3001, 8192, 64, True, "f32", "f32"),
+    (3, 2100, 5152, 32, True, "bf16", "f32"),
+    (9, 24001, 6272, 128, True, "bf16", "bf16"),
+    (2, 30001, 5248, 128, False, "f32", "f32"),
+    (5, 101, 4224, 32, False, "bf16", "f32"),
+    (1, 21001, 7168, 32, True, "f32", "bf16"),
     # 6 to 16 rows through LDS; one to five tiles a wave; fewer groups than a lane
     # of scales holds, and groups that end inside a block of them
     (6, 20489, 384, 64, True, "bf16", "f32"),

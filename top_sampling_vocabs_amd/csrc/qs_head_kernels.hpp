@@ -91,8 +91,8 @@ constexpr int kThreads8 = 512;          // 8 waves
 // waves per SIMD that the registers are held to
 constexpr int occupancy(int P, int MT) { return P * MT <= 4 ? 4 : 2; }
 
-// The hidden values of one slice of k stay in each wave's registers: the 8
-// waves of a workgroup are KS slices of k by 8 / KS tiles of 16 vocabulary
+// The hidden values of one slice of k stay in each wave's registers: the NW (8 or
+// 16) waves of a workgroup are KS slices of k by NW / KS tiles of 16 vocabulary
 // rows, a wave holds P steps of x (16 MT hidden rows), and the workgroup walks
 // the tiles. A wave's codes of a tile are P * 64 consecutive bytes a row: they
 // are read with consecutive lanes on consecutive bytes (lanes in the product's
@@ -102,12 +102,11 @@ constexpr int occupancy(int P, int MT) { return P * MT <= 4 ? 4 : 2; }
 // result does not depend on which wave is first.
 //
 // Measured: 1 row, 151936 x 4096 in groups of 128, 59 us (5.5 TB/s of codes and
-// scales, where a large copy reaches 4.8 and a large sum 4.0); 1 row, 32000 x
-// 2048, 11.3 us; 16 rows, 128256 x 4096 in groups of 64 with zero points and
-// float32 logits, 74 us (3.9 TB/s: the factors and the offsets, five vector
-// instructions for every product, take over from the bytes).
-template <int P, int MT, int G, int SD, bool ZEROS>
-__global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
+// scales, where a large copy reaches 4.8 and a large sum 4.0); the same with 8192
+// columns, 115 us (5.5 TB/s); 1 row, 32000 x 2048, 11.3 us; 16 rows, 128256 x 4096
+// in groups of 64 with zero points and float32 logits, 74 us (4.0 TB/s).
+template <int NW, int P, int MT, int G, int SD, bool ZEROS>
+__global__ void __launch_bounds__(NW * 64, occupancy(P, MT))
     head_split_kernel(Args a, int steps, int tiles, int ks_log2) {
   constexpr int kGroups = kStepK / G;      // groups per step
   constexpr int NG = P * kGroups;          // groups per slice
@@ -117,16 +116,16 @@ __global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
   constexpr int kScaleStride = NG + 4;     // floats per row in LDS
   constexpr int SL = NG < 4 ? NG : 4;      // lanes per row of a scale load
   constexpr int EL = NG / SL;              // scales per lane
-  __shared__ f32x4 s_part[2][8][MT][64];
-  __shared__ f32x4 s_sum[8][NG][MT][4];    // sums of x over a slice's groups
-  __shared__ __align__(16) uint8_t s_code[8][16 * kCodeStride];
-  __shared__ __align__(16) float s_scale[8][16 * kScaleStride];
-  __shared__ __align__(16) float s_off[ZEROS ? 8 : 1][ZEROS ? 16 * kScaleStride : 1];
+  __shared__ f32x4 s_part[2][NW][MT][64];
+  __shared__ f32x4 s_sum[NW][NG][MT][4];    // sums of x over a slice's groups
+  __shared__ __align__(16) uint8_t s_code[NW][16 * kCodeStride];
+  __shared__ __align__(16) float s_scale[NW][16 * kScaleStride];
+  __shared__ __align__(16) float s_off[ZEROS ? NW : 1][ZEROS ? 16 * kScaleStride : 1];
   const int tid = threadIdx.x;
   const int w = uni(tid >> 6);
   const int lane = lane_id();
   const int n = lane & 15, kg = lane >> 4;
-  const int KS = 1 << ks_log2, TG = 8 >> ks_log2;
+  const int KS = 1 << ks_log2, TG = NW >> ks_log2;
   const int ks = w & (KS - 1), tg = w >> ks_log2;
   const int per = (steps + KS - 1) >> ks_log2;  // at most P
   const int s0 = ks * per;
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
 #pragma unroll
     for (int t = 0; t < MT; ++t) s_part[buf][w][t][lane] = y[t];
     __syncthreads();
-    for (int i = tid; i < TG * MT * 256; i += kThreads8) {
+    for (int i = tid; i < TG * MT * 256; i += NW * 64) {
       const int q = i / (MT * 256), t = (i >> 8) % MT;
       const int m = (i >> 4) & 15, col = i & 15;
       const int v = (batch * TG + q) * 16 + col, b = t * 16 + m;
@@ -300,19 +299,24 @@ __global__ void __launch_bounds__(kThreads8, occupancy(P, MT))
   }
 }
 
-template <int P, int MT, int G, int SD, bool ZEROS>
+template <int NW, int P, int MT, int G, int SD, bool ZEROS>
 hipError_t launch_split(const Args& a, int steps, int ks_log2, hipStream_t st) {
   const int tiles = (a.V + 15) / 16;
-  const int tg = 8 >> ks_log2;
-  const int grid = min(occupancy(P, MT) == 4 ? 512 : 256, (tiles + tg - 1) / tg);
-  hipLaunchKernelGGL((head_split_kernel<P, MT, G, SD, ZEROS>), dim3((unsigned)grid),
-                     dim3(kThreads8), 0, st, a, steps, tiles, ks_log2);
+  const int tg = NW >> ks_log2;
+  const int full = 256 * occupancy(P, MT) * 4 / NW;  // workgroups that the chip holds
+  const int grid = min(full, (tiles + tg - 1) / tg);
+  hipLaunchKernelGGL((head_split_kernel<NW, P, MT, G, SD, ZEROS>), dim3((unsigned)grid),
+                     dim3(NW * 64), 0, st, a, steps, tiles, ks_log2);
   return hipGetLastError();
 }
 
 template <int MT, int G, int SD, bool ZEROS>
 hipError_t pick_steps(const Args& a, hipStream_t st) {
   const int steps = (a.K + kStepK - 1) / kStepK;
+  // 16 waves where 8 slices would hold more than 4 steps each
+  if constexpr (MT == 1) {
+    if (steps > 32) return launch_split<16, 4, MT, G, SD, ZEROS>(a, steps, 4, st);
+  }
   // the fewest slices that leave a wave at most 4 steps
   int ks_log2 = 0;
   while (ks_log2 < 3 && (steps + (1 << ks_log2) - 1) >> ks_log2 > 4) ++ks_log2;
@@ -322,12 +326,9 @@ hipError_t pick_steps(const Args& a, hipStream_t st) {
   const int tiles = (a.V + 15) / 16;
   while (ks_log2 < 3 && (steps >> ks_log2) > 1 && tiles < (512 << (3 - ks_log2))) ++ks_log2;
   const int per = (steps + (1 << ks_log2) - 1) >> ks_log2;
-  if (per <= 1) return launch_split<1, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
-  if (per == 2) return launch_split<2, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
-  if constexpr (MT == 1) {
-    if (per > 4) return launch_split<8, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
-  }
-  return launch_split<4, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  if (per <= 1) return launch_split<8, 1, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  if (per == 2) return launch_split<8, 2, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
+  return launch_split<8, 4, MT, G, SD, ZEROS>(a, steps, ks_log2, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -688,9 +689,15 @@ hipError_t pick(const Args& a, hipStream_t st) {
   // rows, 65000 x 4096: 42 us against 33.5; 8 rows, 32000 x 2048: 15.8 against 12.1;
   // beside it 4 rows, 56000 x 4096: 28.3 against 29.0, 16 rows, 128256 x 4096 in
   // groups of 64: 79 against 83, 8 rows, 17000 x 4096: 16.2 against 19.1).
-  const int tiles = (a.V + 15) / 16;
+  // Past 4096 columns 16 slices of 4 steps have to be full (4 rows, 128256 x 8192:
+  // 101 us against 134; x 6144, 48 steps: 91 against 95; x 5120: 90 against 84), and
+  // in groups of 32 with zero points their scales and offsets outgrow the
+  // registers (196 against 182).
+  const int tiles = (a.V + 15) / 16, steps = (a.K + kStepK - 1) / kStepK;
   const bool few = a.B < 6 || tiles < 1280 || tiles > 3 * 2048;
-  if (a.B <= 16 && a.K <= 8192 && few) return pick_steps<1, G, SD, ZEROS>(a, st);
+  const bool full = steps > 48 || (few && steps > 40);
+  const bool slices = steps <= 32 ? few : tiles < 1280 || (full && !(G == 32 && ZEROS));
+  if (a.B <= 16 && a.K <= 8192 && slices) return pick_steps<1, G, SD, ZEROS>(a, st);
   if (a.B <= 16) return launch_stream<1, G, SD, ZEROS>(a, st);
   // 17 to 32 rows: in registers up to 4096 columns where tiles are few and the
   // slices of k fill the chip (32 rows, 5000 x 4096: 17 us against 21; 20 rows,
