@@ -98,6 +98,16 @@ CASES = [
     (2, 30001, 5248, 128, False, "f32", "f32"),
     (5, 101, 4224, 32, False, "bf16", "f32"),
     (1, 21001, 7168, 32, True, "f32", "bf16"),
+    # blocks of 16 rows in registers, the last one short, and beside them through LDS
+    (64, 1003, 8192, 128, False, "bf16", "f32"),
+    (49, 2001, 4096, 64, True, "bf16", "f32"),
+    (33, 4099, 1024, 32, True, "f32", "bf16"),
+    (18, 1999, 2048, 128, True, "bf16", "f32"),
+    (23, 9001, 6144, 64, False, "bf16", "f32"),
+    (64, 9001, 2048, 64, True, "bf16", "f32"),
+    (40, 15001, 8192, 128, False, "f32", "f32"),
+    (30, 15001, 8192, 32, True, "bf16", "f32"),
+    (66, 1001, 4096, 64, True, "bf16", "f32"),
     # 6 to 16 rows through LDS; one to five tiles a wave; fewer groups than a lane
     # of scales holds, and groups that end inside a block of them
     (6, 20489, 384, 64, True, "bf16", "f32"),

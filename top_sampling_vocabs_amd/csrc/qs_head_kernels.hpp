@@ -93,10 +93,11 @@ constexpr int occupancy(int P, int MT) { return P * MT <= 4 ? 4 : 2; }
 
 // The hidden values of one slice of k stay in each wave's registers: the NW (8 or
 // 16) waves of a workgroup are KS slices of k by NW / KS tiles of 16 vocabulary
-// rows, a wave holds P steps of x (16 MT hidden rows), and the workgroup walks
-// the tiles. A wave's codes of a tile are P * 64 consecutive bytes a row: they
-// are read with consecutive lanes on consecutive bytes (lanes in the product's
-// own order, 16 rows apart, cost four times the cache accesses), one tile ahead,
+// rows, a wave holds P steps of x (16 MT hidden rows; the grid's y counts blocks
+// of as many), and the workgroup walks the tiles. A wave's codes of a tile are
+// P * 64 consecutive bytes a row: they are read with consecutive lanes on
+// consecutive bytes (lanes in the product's own order, 16 rows apart, cost four
+// times the cache accesses), one tile ahead,
 // and change lanes through the wave's own LDS. The slices' float32 sums meet in
 // LDS (two buffers, one barrier a tile) and are added in slice order, so the
 // result does not depend on which wave is first.
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(NW * 64, occupancy(P, MT))
   const int k0 = s0 * kStepK;                    // the slice's first column
   const int cols = max(0, min(mine * kStepK, a.K - k0));
   const int batches = (tiles + TG - 1) / TG;
+  const int row0 = (int)blockIdx.y * MT * 16;
 
   // a tile's codes, scales and zero points, lanes along the rows: a scalar base
   // per tile and a lane's offset from it, which only the last tile changes
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(NW * 64, occupancy(P, MT))
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const int k = k0 + p * kStepK + chunk_of<G>(j, kg) * 8;
-        const int m = min(t * 16 + n, a.B - 1);
+        const int m = min(row0 + t * 16 + n, a.B - 1);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (p < mine && k < a.K)
           v = ordered(*reinterpret_cast<const uint4*>(a.hidden + (size_t)m * a.hidden_stride + k));
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(NW * 64, occupancy(P, MT))
     for (int i = tid; i < TG * MT * 256; i += NW * 64) {
       const int q = i / (MT * 256), t = (i >> 8) % MT;
       const int m = (i >> 4) & 15, col = i & 15;
-      const int v = (batch * TG + q) * 16 + col, b = t * 16 + m;
+      const int v = (batch * TG + q) * 16 + col, b = row0 + t * 16 + m;
       if (v < a.V && b < a.B) {
         float sum = 0.0f;
         for (int k = 0; k < KS; ++k) sum += s_part[buf][q * KS + k][t][(m >> 2) * 16 + col][m & 3];
@@ -305,8 +307,10 @@ hipError_t launch_split(const Args& a, int steps, int ks_log2, hipStream_t st) {
   const int tg = NW >> ks_log2;
   const int full = 256 * occupancy(P, MT) * 4 / NW;  // workgroups that the chip holds
   const int grid = min(full, (tiles + tg - 1) / tg);
-  hipLaunchKernelGGL((head_split_kernel<NW, P, MT, G, SD, ZEROS>), dim3((unsigned)grid),
-                     dim3(NW * 64), 0, st, a, steps, tiles, ks_log2);
+  const int blocks = (a.B + MT * 16 - 1) / (MT * 16);
+  hipLaunchKernelGGL((head_split_kernel<NW, P, MT, G, SD, ZEROS>),
+                     dim3((unsigned)grid, (unsigned)blocks), dim3(NW * 64), 0, st, a, steps,
+                     tiles, ks_log2);
   return hipGetLastError();
 }
 
@@ -353,13 +357,13 @@ constexpr int kMaxTiles = 5;             // tiles a wave holds at once
 // chunks). A chunk's codes are requested while the one before is multiplied, and
 // pass through the wave's own LDS from lanes along a row to the product's.
 //
-// Measured: 64 rows, 151936 x 8192 in groups of 128, 240 us (660 TFLOP/s, 2.8
+// Measured: 64 rows, 151936 x 8192 in groups of 128, 235 us (680 TFLOP/s, 2.8
 // TB/s; 288 with 3 tiles a wave and scales read per chunk); in groups of 32 with
-// float32 scales, 297 us (317); 48 rows, 100003 x 4096 in groups of 32 with zero
+// float32 scales, 289 us (317); 48 rows, 100003 x 4096 in groups of 32 with zero
 // points, 140 us (187). With all loads but the first taken out the products of
-// the first two take 167 and 220 us (the factors and, at small groups, the
-// scaling cost as many vector instructions as products); the loads alone 225 to
-// 250. 8 waves a compute unit are all that the registers of 5 tiles by 64 rows
+// the first two take 181 and 210 us (the factors and, at small groups, the
+// scaling cost as many vector instructions as products); the loads alone 168 and
+// 196. 8 waves a compute unit are all that the registers of 5 tiles by 64 rows
 // allow, so the two overlap imperfectly. Fewer waves with more columns, or a
 // chunk's columns split over the waves, were slower (355 and 328 us).
 template <int MT, int NT, int G, bool ZEROS>
@@ -699,6 +703,14 @@ hipError_t pick(const Args& a, hipStream_t st) {
   const bool slices = steps <= 32 ? few : tiles < 1280 || (full && !(G == 32 && ZEROS));
   if (a.B <= 16 && a.K <= 8192 && slices) return pick_steps<1, G, SD, ZEROS>(a, st);
   if (a.B <= 16) return launch_stream<1, G, SD, ZEROS>(a, st);
+  // More rows of small vocabularies: 16 at a time in registers, so that the blocks
+  // of rows and the slices of k fill the chip (64 rows, 1000 x 8192: 16 us against
+  // 63; 40 rows, 8000 x 8192: 53 against 78; 64 rows, 4000 x 8192: 57 against 63, of
+  // 8000: 68 against 64; 24 rows, 2000 x 4096: 9 against 12, of 4000: 13 either way).
+  const int blocks = (a.B + 15) / 16;
+  const int most = a.B <= 32 && a.K <= 4096 ? 256 : 1536;
+  if (a.B <= 64 && a.K <= 8192 && tiles * blocks <= most)
+    return pick_steps<1, G, SD, ZEROS>(a, st);
   // 17 to 32 rows: in registers up to 4096 columns where tiles are few and the
   // slices of k fill the chip (32 rows, 5000 x 4096: 17 us against 21; 20 rows,
   // 12000 x 2048: 14 against 16). Large vocabularies are a draw or worse (151936 x
