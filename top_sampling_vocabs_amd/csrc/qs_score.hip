@@ -23,11 +23,11 @@
 // One maximum's own weight, exactly 1, is left out of every sum: R = S - 1 is what
 // a wave, a part and a row hold, and log S = log1p(R). The log-probability of a
 // token that is almost certain then keeps float32's relative precision (added to
-// 1, the other weights would keep 2^-24 absolutely). A wave whose S is 4 or more
-// loses nothing by the subtraction; the others take the lane of their maximum,
-// whose tokens go through LDS to as many lanes and are weighed again there
-// without the one. (2048 rows of 151936 bf16: 115 us; 119 if every wave did it,
-// 110 with the plain sum.)
+// 1, the other weights would keep 2^-24 absolutely). A wave whose S is 2.25 or
+// more loses nothing by the subtraction; the others take the lane of their maximum,
+// whose tokens are read again, a load to a lane, and weighed again without the
+// one. (2048 rows of 151936 bf16: 112 us; 110 with the plain sum, 115 with the
+// lane's registers kept for it, 119 if every wave did that.)
 //
 // Rows of up to kRowBlock * kRowLoads loads go to one workgroup and one launch:
 // a second launch costs more than one compute unit needs for such a row. Longer
@@ -36,9 +36,9 @@
 // exponentials; a second launch joins the parts of each row. Where that gives
 // at most kFewParts parts they are halved, so that the chip fills evenly.
 //
-// Measured: 2048 rows of 151936 bf16, 115 us (5.4 TB/s, where a large copy
+// Measured: 2048 rows of 151936 bf16, 112 us (5.6 TB/s, where a large copy
 // reaches 4.8: bound by the reads); 256 such rows with a mask and 20 top tokens,
-// 33 us, 6 of them the join (2.6 TB/s: bound by the vector instructions, about a
+// 34 us, 6 of them the join (2.4 TB/s: bound by the vector instructions, about a
 // dozen a token, and by the top tokens' LDS lists); one row of 32000, 8 us, its
 // latency. A workgroup per row that walks the row
 // in a loop, with one launch, was slower in every form tried (28 us against
@@ -73,6 +73,9 @@ constexpr int kSmallBlock = 256;  // threads of a short row's workgroup
 constexpr int kSmallLoads = 4;
 constexpr int kListCap = 256;     // collected keys per workgroup
 constexpr int kJoinCap = 1024;    // keys of all parts that reach the row's t
+// S from which 1 may be subtracted: R's relative error is then at most 1.8 times
+// S's, whose terms pass at most 73 additions in a wave
+constexpr float kPlain = 2.25f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -334,7 +337,6 @@ __global__ void __launch_bounds__(THREADS)
   constexpr bool kTable = MASK && DT == QS_BF16;
   __shared__ Shared s;
   __shared__ uint4 s_masks[kTable ? 256 : 1];  // masks_of every byte of legal bits
-  __shared__ uint4 s_peak[kWavesHere][NL];     // tokens of the lane of a wave's maximum
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int w = tid >> 6;
@@ -439,20 +441,19 @@ __global__ void __launch_bounds__(THREADS)
   }
   float Rw = wave_sum_f32(S[0] + S[1]), Ew = wave_sum_f32(E[0] + E[1]);
   bool has = true;
-  if (Rw >= 4.0f || Rw != Rw) {
+  if (Rw >= kPlain || Rw != Rw) {
     Rw -= 1.0f;
   } else {
     // the maximum's lane again, a load to each of the first lanes, without the one
     const int peak = __builtin_ctzll(ballot(lane_max == wave_max));
-    if (lane == peak) {
-#pragma unroll
-      for (int u = 0; u < NL; ++u) s_peak[w][u] = v[u];
+    const int i = begin + (lane * THREADS + (tid & ~63) + peak) * P;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t bits = 0u;
+    if (lane < part_loads && i < a.V) {
+      q = *reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P));
+      bits = bits_at(i, MASK ? mask_row[i >> 3] : 0xFFu);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    uint4 q = masks_of<DT>(0u);
-    q = blank<DT>(q, q);  // -inf
-    if (lane < NL) q = s_peak[w][lane];
+    q = blank<DT>(q, masks_of<DT>(bits));
     bool is_max = false;
 #pragma unroll
     for (int e = 0; e < P; ++e) is_max |= token<DT>(q, e) == wave_max;
