@@ -586,3 +586,55 @@ def test_peaked_rows(qs, V, dtype):
         H = logS + X
         t_H = tol + U * ((2 * depth(V) + 16) * X + 4 * X2 + 2 * H) + 1e-37
         assert abs(o["entropy"][r] - H) <= t_H, (r, o["entropy"][r], H)
+
+
+def gap_rows(seed, B, V):
+    """Rows with a stretch of V / 3 tokens (whole waves and parts of long rows) that
+    is illegal in the rows 1, 4, .. and legal but -inf in the rows 2, 5, .."""
+    z = make(seed, B, V, "normal")
+    legal = np.random.default_rng(seed).random((B, V)) < 0.6
+    legal[:, V - 1] = True
+    gap = slice(V // 3, 2 * V // 3)
+    legal[1::3, gap] = False
+    z[2::3, gap] = -np.inf
+    return z, legal
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 40, 700, 3001, 100003])
+def test_temperatures(qs, V, dtype):
+    """Every power of ten that a temperature can be, beside waves and parts
+    without a legal or a finite token."""
+    print(f"score temperatures V={V} {dtype}", flush=True)
+    T = np.repeat(10.0 ** np.arange(-37, 39), 3).astype(np.float32)
+    B = T.size
+    z, legal = gap_rows(V, B, V)
+    tokens = tokens_for(np.random.default_rng(V), B, V, 2)
+    for n in (0, 5):
+        _, _, _, out = run(qs, z, dtype, tokens, T, legal, n)
+        check_forward(z, tokens, T, legal, n, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3001, 100003])
+def test_large_logits(qs, V, dtype):
+    """Logits up to 1e37 as they are and at temperatures of their own size, and
+    (float32) whole numbers beside a large offset, where neighbours differ by 1."""
+    print(f"score large logits V={V} {dtype}", flush=True)
+    e = np.repeat(np.arange(0, 37), 2)
+    B = e.size
+    z, legal = gap_rows(V, B, V)
+    z = bf16(z * (10.0 ** e)[:, None])
+    T = np.where(np.arange(B) % 2 == 0, 1.0, 10.0 ** e).astype(np.float32)
+    tokens = tokens_for(np.random.default_rng(V), B, V, 2)
+    _, _, _, out = run(qs, z, dtype, tokens, T, legal, 3)
+    check_forward(z, tokens, T, legal, 3, out)
+    if dtype == "f32":
+        rng = np.random.default_rng(V + 1)
+        base = np.repeat(2.0 ** np.array([8, 16, 20, 22, 23, -8, -16, -20, -22, -23]), 4)
+        base = np.where(np.arange(base.size) // 4 < 5, base, -(base ** -1.0))
+        z = (base[:, None] + rng.integers(0, 40, (base.size, V))).astype(np.float32)
+        T = np.tile([4.0, 1.0, 0.25, 0.01], base.size // 4).astype(np.float32)
+        tokens = tokens_for(rng, base.size, V, 2)
+        _, _, _, out = run(qs, z, "f32", tokens, T, None, 3)
+        check_forward(z, tokens, T, None, 3, out)

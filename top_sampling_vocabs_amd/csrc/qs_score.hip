@@ -13,9 +13,9 @@
 // rescaling. Each wave uses its own maximum m_w and, for one operation per
 // token, the rounded product k_w = fl(m_w c), c = log2(e) / T, as its reference:
 // with 2^(z c - k_w) from one fused multiply-add the sums are off by the common
-// factor 2^(m_w c - k_w) alone, which one more gives exactly. (Where m_w c leaves
-// float32's comfortable range the difference comes first.) The waves' (m, S, E)
-// are joined as
+// factor 2^(m_w c - k_w) alone, which one more gives exactly. (Past |k_w| = 2^24,
+// where that factor is no longer within 1/2 and 2 and soon leaves float32's range,
+// the difference comes first.) The waves' (m, S, E) are joined as
 //   S = sum_w S_w f_w,  E = sum_w f_w (E_w + S_w (m_w - m) c),
 //   f_w = 2^((m_w - m) c).
 // Weights and E are kept in units of log 2 (one hardware exponential each).
@@ -76,6 +76,9 @@ constexpr int kJoinCap = 1024;    // keys of all parts that reach the row's t
 // S from which 1 may be subtracted: R's relative error is then at most 1.8 times
 // S's, whose terms pass at most 73 additions in a wave
 constexpr float kPlain = 2.25f;
+// |k_w| up to which exponents may be taken against k_w: its rounding, the exponent
+// of the sums' common factor, is at most 1/2 there
+constexpr float kFused = 16777216.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(THREADS)
   // the wave's sums against its own maximum
   float S[2] = {0.0f, 0.0f}, E[2] = {0.0f, 0.0f};
   const float k = wave_max * c;
-  if (fabsf(k) < 1e30f && c < 1e30f) {
+  if (fabsf(k) < kFused && c < 1e30f) {
 #pragma unroll
     for (int u = 0; u < NL; ++u) {
       opaque(v[u]);
