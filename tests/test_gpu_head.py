@@ -383,3 +383,70 @@ def test_captured_and_replayed(qs):
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(bits(got[n]), bits(want[n])), (k, n)
+
+
+def long_chain(qs, seed, B, V):
+    """chain_inputs for rows of several parts, with scratch memory of their own."""
+    import torch
+    x, codes, s, z, par, tok2 = chain_inputs(qs, seed=seed, B=B, V=V, K=512)
+    par["ws"] = qs.token_logprobs_workspace_for(
+        torch.empty((B, -(-V // 8) * 8), dtype=torch.bfloat16, device="cuda")[:, :V], 5)
+    assert par["ws"] is not None
+    return x, codes, s, z, par, tok2
+
+
+def test_two_streams_long_rows(qs):
+    """test_two_streams with rows whose parts pass through scratch memory, the
+    caller's and the call's own."""
+    import torch
+    ins = [long_chain(qs, k, 3 + 10 * k, 131072 + k) for k in (1, 2)]
+    want = [chain(qs, *i[:4], dict(i[4], ws=None), i[5]) for i in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    for own in (False, True, False):
+        got = []
+        for st, i in zip(streams, ins):
+            with torch.cuda.stream(st):
+                got.append(chain(qs, *i[:4], dict(i[4], ws=None) if own else i[4], i[5]))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for k in b:
+                assert torch.equal(bits(a[k]), bits(b[k])), k
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_captured_and_replayed_long_rows(qs, own):
+    """test_captured_and_replayed with rows of several parts; two graphs with the
+    caller's scratch memory each, or with the graph's own."""
+    import torch
+    ins = [long_chain(qs, 5 + k, 5 + k, 131077 + k) for k in (0, 1)]
+    if own:
+        for i in ins:
+            i[4]["ws"] = None
+    cs = torch.cuda.Stream()
+    cs.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(cs):
+        for i in ins:
+            chain(qs, *i)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=cs):
+            out = chain(qs, *i)
+        graphs.append((g, out))
+    torch.cuda.synchronize()
+    for k in range(4):
+        for i in ins:
+            i[0].copy_(torch.randn(i[0].shape, device="cuda"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(cs):
+            for g, _ in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        for i, (_, out) in zip(ins, graphs):
+            got = {n: v.clone() for n, v in out.items()}
+            want = chain(qs, *i[:4], dict(i[4], ws=None), i[5])
+            torch.cuda.synchronize()
+            for n in want:
+                assert torch.equal(bits(got[n]), bits(want[n])), (k, n)

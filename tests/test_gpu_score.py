@@ -638,3 +638,42 @@ def test_large_logits(qs, V, dtype):
         tokens = tokens_for(rng, base.size, V, 2)
         _, _, _, out = run(qs, z, "f32", tokens, T, None, 3)
         check_forward(z, tokens, T, None, 3, out)
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 32769), ("f32", 40003), ("bf16", 131077)])
+def test_caller_workspace(qs, V, dtype):
+    """Rows of several parts with the caller's scratch memory, used again for
+    smaller and other calls: the bits of a call that makes its own. What cannot
+    hold the call is refused."""
+    import torch
+    print(f"score workspace V={V} {dtype}", flush=True)
+    B = 6
+    z = make(V, B, V, "normal")
+    tokens = tokens_for(np.random.default_rng(V), B, V, 2)
+    _, _, _, want = run(qs, z, dtype, tokens, None, None, 20)
+    check_forward(z, tokens, None, None, 20, want)
+    lg = on_gpu(z, dtype)
+    tok = torch.from_numpy(tokens).cuda()
+    ws = qs.token_logprobs_workspace_for(lg, 20)
+    assert ws is not None and ws.device == lg.device
+    for fill in (0, 255):
+        ws.fill_(fill)
+        got = qs.token_logprobs(lg, tok, entropy=True, top_n=20, workspace=ws)
+        torch.cuda.synchronize()
+        for k in want:
+            assert torch.equal(got[k].view(torch.int32), want[k].view(torch.int32)), k
+    small = qs.token_logprobs(lg[:2], tok[:2], entropy=True, workspace=ws)
+    leaf = lg.detach().requires_grad_()
+    out = qs.token_logprobs(leaf, tok, workspace=ws)
+    (grad,) = torch.autograd.grad(out["logprobs"].sum(), leaf)
+    torch.cuda.synchronize()
+    assert torch.equal(small["logprobs"], want["logprobs"][:2])
+    assert torch.equal(out["logprobs"], want["logprobs"]) and bool(torch.isfinite(grad).all())
+    n = ws.numel()
+    for bad in (ws.cpu(), ws[:1].expand(n), torch.empty(2 * n, dtype=torch.uint8,
+                                                        device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            qs.token_logprobs(lg, tok, top_n=20, workspace=bad)
+    for bad in (ws[:n - 1], ws[256:], torch.empty(n + 64, dtype=torch.uint8, device="cuda")[64:]):
+        with pytest.raises(RuntimeError):
+            qs.token_logprobs(lg, tok, top_n=20, workspace=bad)

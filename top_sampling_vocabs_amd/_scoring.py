@@ -91,8 +91,9 @@ def token_logprobs(logits, tokens, *, temperature=None, bitmask=None, entropy=Fa
     asks for all backward passes, or capture token_logprobs_backward itself.
     """
     shape = _check_row_inputs(logits, tokens, temperature, bitmask)
-    if workspace is not None:
-        _check_device(workspace, logits.device, "workspace")
+    if workspace is not None and (workspace.get_device() != shape[3]
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{shape[3]}")
     if logits.requires_grad and torch.is_grad_enabled():
         keys, *out = _TokenLogprobs.apply(logits, tokens, temperature, bitmask, shape, entropy,
                                           int(top_n), workspace)
