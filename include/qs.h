@@ -497,7 +497,9 @@ QS_API int qs_token_logprobs(const void* logits, int dtype, int64_t B, int64_t V
  *              It may be the logits' own buffer (same address and stride); any
  *              other overlap is not allowed.
  * Computed in float32, rounded once to the dtype (nearest even). Tokens outside
- * [0, V) are ignored. One kernel launch on `stream`; nothing is allocated. */
+ * [0, V) are ignored. An infinity or a NaN among a row's incoming gradients (empty
+ * slots apart) leaves no legal token of that row a finite gradient. One kernel
+ * launch on `stream`; nothing is allocated. */
 QS_API int qs_token_logprobs_backward(const void* logits, int dtype, int64_t B, int64_t V,
                       int64_t row_stride, const float* temperature, const uint32_t* bitmask,
                       int64_t bitmask_stride, const int32_t* tokens, int64_t G,

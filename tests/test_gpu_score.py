@@ -677,3 +677,65 @@ def test_caller_workspace(qs, V, dtype):
     for bad in (ws[:n - 1], ws[256:], torch.empty(n + 64, dtype=torch.uint8, device="cuda")[64:]):
         with pytest.raises(RuntimeError):
             qs.token_logprobs(lg, tok, top_n=20, workspace=bad)
+
+
+@pytest.mark.parametrize("G", [1, 3])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_grad_of_non_finite_gradients(qs, dtype, G):
+    """A NaN or an infinity in an incoming gradient reaches every legal token of its
+    row, whatever token it belongs to, and no other row. Illegal tokens and rows
+    with an error stay 0."""
+    import torch
+    print(f"grad non-finite {dtype} G={G}", flush=True)
+    rng = np.random.default_rng(21)
+    V, bad = 5003, [np.nan, np.inf, -np.inf]
+    B = 16
+    z = make(21, B, V, "normal")
+    legal = rng.random((B, V)) < 0.5
+    legal[:, 0], legal[:, 1] = True, False
+    legal[12] = False                      # a row without a legal token
+    tokens = rng.integers(2, V, (B, G)).astype(np.int32)
+    gl = rng.normal(0, 1, (B, G)).astype(np.float32)
+    gH = rng.normal(0, 1, B).astype(np.float32)
+    for r in range(3):
+        tokens[r, -1], gl[r, -1] = 0, bad[r]          # a legal token's gradient
+        tokens[3 + r, -1], gl[3 + r, -1] = 1, bad[r]  # an illegal one's
+        gH[6 + r] = bad[r]
+    gl[9, 0], gH[9] = np.inf, -np.inf
+    gl[12], gH[12] = np.nan, np.nan
+    tokens[13, 0], gl[13, 0] = -1, np.nan             # an empty slot's is not read
+    for use_entropy in (True, False):
+        g = gH if use_entropy else None
+        _, out, grad = run_grad(qs, z, dtype, tokens, None, legal, gl, g)
+        got = grad.float().cpu().numpy()
+        lost = [r for r in range(10) if use_entropy or not 6 <= r < 9]
+        for r in range(B):
+            if r in lost:
+                assert not np.isfinite(got[r][legal[r]]).any(), r
+                if r in (0, 3, 6):
+                    assert np.isnan(got[r][legal[r]]).all(), r
+                assert (got[r][~legal[r]] == 0).all(), r
+        keep = [r for r in range(B) if r not in lost]
+        pick = {k: v[keep] for k, v in out.items()}
+        check_grad(z[keep], dtype, tokens[keep], None, legal[keep], gl[keep],
+                   None if g is None else g[keep], pick, grad[keep])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_grad_past_the_largest_value(qs, dtype):
+    """Finite gradients whose quotient by T overflows: a token without weight still
+    gets 0 (not 0 times an infinity), and the row holds no NaN."""
+    import torch
+    z = np.full((2, 600), -1e4, np.float32)
+    z[:, 7] = 0.0
+    z[0, 8] = 0.0
+    tokens = np.array([[7], [9]], np.int32)
+    T = np.array([1e-9, 1e-9], np.float32)
+    gl = np.full((2, 1), 1e35, np.float32)
+    gH = np.full(2, 1e35, np.float32)
+    _, out, grad = run_grad(qs, z, dtype, tokens, T, None, gl, gH)
+    got = grad.float().cpu().numpy()
+    assert not np.isnan(got).any()
+    still = np.ones(600, bool)
+    still[[7, 8, 9]] = False
+    assert (got[:, still] == 0).all() and got[0, 7] > 1e38 and got[0, 8] < -1e38

@@ -36,8 +36,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 template <int DT> constexpr int kPer = DT == QS_F32 ? 4 : 8;  // tokens per 16-byte load
 
-__device__ __forceinline__ float clamp_to(float x, float most) {
-  return fminf(fmaxf(x, -most), most);
+// x within +-most; as it is where `keep` is set (fmaxf would turn a NaN into -most)
+__device__ __forceinline__ float clamp_to(float x, float most, bool keep) {
+  return keep ? x : fminf(fmaxf(x, -most), most);
 }
 
 template <int DT, bool MASK, bool ONE>
@@ -96,9 +97,11 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
     __syncthreads();
   }
   const float gH = a.g_ent ? a.g_ent[r] : 0.0f, H = a.g_ent ? a.entropy[r] : 0.0f;
-  // finite, so that a p of 0 gives 0
-  const float A = clamp_to(-(gs + gH * H) * inv_T, 3e38f);
-  const float Bc = clamp_to(-gH * 0.6931471805599453f * inv_T, 1e36f);
+  // finite where the row's incoming sums are, so that a p of 0 gives 0; infinities
+  // and NaN go through to every legal token
+  const bool lost = !(fabsf(gs) < INFINITY && fabsf(gH) < INFINITY && fabsf(H) < INFINITY);
+  const float A = clamp_to(-(gs + gH * H) * inv_T, 3e38f, lost);
+  const float Bc = clamp_to(-gH * 0.6931471805599453f * inv_T, 1e36f, lost);
 
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
