@@ -739,3 +739,52 @@ def test_grad_past_the_largest_value(qs, dtype):
     still = np.ones(600, bool)
     still[[7, 8, 9]] = False
     assert (got[:, still] == 0).all() and got[0, 7] > 1e38 and got[0, 8] < -1e38
+
+
+def test_writes_are_seen_by_autograd(qs):
+    """A buffer that a call writes into counts as changed: a graph that saved it
+    reports so, as for torch's own writes. Leaves that require a gradient are
+    refused as outputs; tensors of inference mode are taken."""
+    import torch
+    torch.manual_seed(1)
+    B, V, K = 4, 512, 256
+    hidden = torch.randn(B, K, device="cuda").bfloat16()
+    codes = torch.randint(0, 256, (V, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.rand(V, K // 64, device="cuda") * 0.02
+    tok = torch.randint(0, V, (B,), dtype=torch.int32, device="cuda")
+    T, k, p = (torch.full((B,), v, device="cuda") for v in (1.0, 0, 1.0))
+    sample = (codes, scales, None, T, k.int(), p)
+    buf = torch.empty(B, V, device="cuda")
+    base = qs.token_logprobs(qs.head_logits(hidden, codes, scales, out=buf), tok)
+    grad_args = (tok, base["row_max"], base["log_sum"], base["status"],
+                 torch.ones(B, device="cuda"))
+    history = torch.zeros(B, 3, dtype=torch.int32, device="cuda")
+    count, one = torch.full((B,), 3, dtype=torch.int32, device="cuda"), torch.ones(B, device="cuda")
+    writes = {
+        "head_logits": lambda t: qs.head_logits(hidden, codes, scales, out=t),
+        "sample_hidden": lambda t: qs.sample_hidden(hidden, *sample, logits=t,
+                                                    uniforms=torch.zeros(B, dtype=torch.float64,
+                                                                         device="cuda")),
+        "backward": lambda t: qs.token_logprobs_backward(buf, *grad_args, out=t),
+        "penalties": lambda t: qs.apply_penalties(t, history, count, 2 * one, one),
+        "bias": lambda t: qs.apply_logit_bias(t, history, torch.ones(B, 3, device="cuda"), count),
+    }
+    for name, write in writes.items():
+        z = torch.randn(B, V, device="cuda").requires_grad_()
+        kept = z.detach()                  # shares its memory and its version
+        before = kept._version
+        out = qs.token_logprobs(z, tok)
+        write(kept)
+        assert kept._version > before, name
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out["logprobs"].sum().backward()
+        with torch.inference_mode():
+            write(torch.zeros(B, V, device="cuda"))
+    for name in ("head_logits", "sample_hidden", "backward"):
+        leaf = torch.zeros(B, V, device="cuda").requires_grad_()
+        for t in (leaf, leaf * 2):
+            with pytest.raises(ValueError, match="gradient"):
+                writes[name](t)
+        with torch.no_grad():
+            writes[name](leaf)
+    torch.cuda.synchronize()

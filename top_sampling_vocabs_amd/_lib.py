@@ -485,6 +485,7 @@ def apply_penalties(logits, history, history_count, repetition, presence, freque
                                 _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(status),
                                 _stream(logits.device))
     _status(rc, "qs_apply_penalties")
+    torch.autograd.graph.increment_version(logits)  # written in place
     return status
 
 
@@ -510,6 +511,7 @@ def apply_logit_bias(logits, bias_ids, bias_values, bias_count):
                                  _ptr(bias_ids), _ptr(bias_values), bias_ids.shape[1],
                                  _ptr(bias_count), _ptr(status), _stream(logits.device))
     _status(rc, "qs_apply_logit_bias")
+    torch.autograd.graph.increment_version(logits)  # written in place
     return status
 
 

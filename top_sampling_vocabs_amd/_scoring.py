@@ -35,6 +35,20 @@ def _enqueue(call, index, *args):
         return call(*args, _current_stream(index))
 
 
+def _check_out(out):
+    """An output buffer of the caller's: written without a node of torch's graph, so
+    it cannot be one that a gradient flows through."""
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("an output buffer must not require a gradient: call under "
+                         "torch.no_grad() or with a detached tensor")
+
+
+def _wrote(out):
+    """Counts a launched kernel's writes into the caller's tensor as a change in
+    place: a graph that saved the tensor reports it instead of reading it."""
+    torch.autograd.graph.increment_version(out)
+
+
 def _check_vec(t, B, dtype, index, name):
     # one test a property, the cheap ones first: most calls here are small
     if t is None or t.dtype is not dtype or t.dim() != 1 or t.size(0) != B \
@@ -143,7 +157,8 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
     log_sum, status (and entropy): its outputs; grad_logprobs float32 in the
     shape of tokens; grad_entropy float32 [B], together with entropy, or None.
     Returns grad_logits [B, V] in the logits' dtype (0 on rows whose status is
-    not ROW_OK); out: where to write it (it may be logits itself).
+    not ROW_OK); out: where to write it (it may be logits itself; counted as a
+    change in place, so it must not require a gradient).
     """
     B, V, G, index = _check_row_inputs(logits, tokens, temperature, bitmask)
     if (entropy is None) != (grad_entropy is None):
@@ -158,12 +173,15 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
             or grad_logprobs.get_device() != index or not grad_logprobs.is_contiguous():
         raise ValueError("grad_logprobs must be a contiguous float32 tensor in the shape of "
                          f"tokens on cuda:{index}")
-    if out is None:
+    given = out is not None
+    if not given:
         out = _padded_rows(B, V, logits.dtype, logits.device)
     elif out.shape != logits.shape or out.dtype is not logits.dtype \
             or out.get_device() != index or out.stride(1) != 1:
         raise ValueError("out must have the logits' shape, dtype and device "
                          "and unit column stride")
+    if given:
+        _check_out(out)
     rc = _enqueue(
         load().qs_token_logprobs_backward, index,
         logits.data_ptr(), _code(logits, "logits"), B, V, logits.stride(0), _addr(temperature),
@@ -172,6 +190,8 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
         _addr(entropy), _addr(grad_entropy), out.data_ptr(), out.stride(0))
     if rc:
         _status(rc, "qs_token_logprobs_backward")
+    if given:
+        _wrote(out)
     return out
 
 
@@ -216,8 +236,8 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
     or 128; zeros uint8 [V, K/group] or None (8). Weight [v, k] is
     (code - zero) * scale. Returns logits [B, V] in `dtype` (bfloat16 unless
     given) with rows laid out as the selection reads them; out: where to write
-    them. Enqueued on the current stream. Inference only: tensors that require
-    a gradient are refused.
+    them (counted as a change in place). Enqueued on the current stream. Inference
+    only: tensors that require a gradient are refused.
     """
     if hidden.dtype is not torch.bfloat16 or hidden.dim() != 2 or not hidden.is_cuda \
             or hidden.stride(1) != 1:
@@ -240,12 +260,15 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
     if (hidden.requires_grad or scales.requires_grad) and torch.is_grad_enabled():
         raise ValueError("head_logits has no gradient: call it under torch.no_grad() "
                          "or on detached tensors")
-    if out is None:
+    given = out is not None
+    if not given:
         out = _padded_rows(B, V, dtype or torch.bfloat16, hidden.device)
     elif out.shape != (B, V) or out.stride(1) != 1 or out.get_device() != index \
             or (dtype is not None and out.dtype is not dtype):
         raise ValueError("out must be [B, V] in the asked dtype with unit column stride "
                          f"on cuda:{index}")
+    if given:
+        _check_out(out)
     rc = _enqueue(
         load().qs_head_logits, index,
         hidden.data_ptr(), B, K, hidden.stride(0) if B > 1 else K, codes.data_ptr(), V,
@@ -254,6 +277,8 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
         _code(out, "out"), out.stride(0))
     if rc:
         _status(rc, "qs_head_logits")
+    if given:
+        _wrote(out)
     return out
 
 
