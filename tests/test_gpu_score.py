@@ -788,3 +788,39 @@ def test_writes_are_seen_by_autograd(qs):
         with torch.no_grad():
             writes[name](leaf)
     torch.cuda.synchronize()
+
+
+def test_forward_mode_is_refused(qs):
+    """Tangents are not carried: a dual tensor is refused, not taken without its
+    tangent. Under a dual level plain tensors work as ever."""
+    import torch
+    from torch.autograd import forward_ad
+    torch.manual_seed(2)
+    B, V, K = 3, 512, 128
+    z = torch.randn(B, V, device="cuda")
+    tok = torch.randint(0, V, (B,), dtype=torch.int32, device="cuda")
+    T = torch.ones(B, device="cuda")
+    hidden = torch.randn(B, K, device="cuda").bfloat16()
+    codes = torch.randint(0, 256, (V, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.rand(V, K // 64, device="cuda")
+    out = qs.token_logprobs(z, tok, entropy=True)
+    stats = (out["row_max"], out["log_sum"], out["status"])
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+        again = qs.token_logprobs(z, tok, entropy=True)
+        qs.head_logits(hidden, codes, scales)
+        qs.token_logprobs_backward(z, tok, *stats, T)
+        for call in (lambda: qs.token_logprobs(dual(z), tok),
+                     lambda: qs.token_logprobs(dual(z.clone().requires_grad_()), tok),
+                     lambda: qs.token_logprobs(z, tok, temperature=dual(T)),
+                     lambda: qs.token_logprobs_backward(dual(z), tok, *stats, T),
+                     lambda: qs.token_logprobs_backward(z, tok, *stats, dual(T)),
+                     lambda: qs.token_logprobs_backward(z, tok, *stats, T, entropy=out["entropy"],
+                                                        grad_entropy=dual(T)),
+                     lambda: qs.head_logits(dual(hidden), codes, scales),
+                     lambda: qs.head_logits(hidden, codes, dual(scales))):
+            with pytest.raises(ValueError, match="forward"):
+                call()
+    torch.cuda.synchronize()
+    assert torch.equal(again["logprobs"], out["logprobs"])

@@ -6,6 +6,7 @@ loaded on first use, because it needs torch at import.
 """
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import QS_BF16, QS_F32, _check_logits, _status, load, sample
 
@@ -33,6 +34,16 @@ def _enqueue(call, index, *args):
         return call(*args, _current_stream(index))
     with torch.cuda.device(index):
         return call(*args, _current_stream(index))
+
+
+def _refuse_tangents(*tensors):
+    """Forward-mode tangents would be dropped without a word: refused. (Outside a
+    dual level no tensor has one; a torch that does not say is asked for each.)"""
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("tangents of forward-mode differentiation are not carried")
 
 
 def _check_out(out):
@@ -100,14 +111,16 @@ def token_logprobs(logits, tokens, *, temperature=None, bitmask=None, entropy=Fa
     top_logprobs [B, top_n] (top_n <= 64). Enqueued on the current stream.
 
     If logits require a gradient, logprobs and entropy carry it (to the logits
-    only; a second derivative is not available). To capture a training step in a
-    graph, drop every eager autograd graph of the same leaves first, as torch
-    asks for all backward passes, or capture token_logprobs_backward itself.
+    only; a second derivative and forward mode are not available). To capture a
+    training step in a graph, drop every eager autograd graph of the same leaves
+    first, as torch asks for all backward passes, or capture
+    token_logprobs_backward itself.
     """
     shape = _check_row_inputs(logits, tokens, temperature, bitmask)
     if workspace is not None and (workspace.get_device() != shape[3]
                                   or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{shape[3]}")
+    _refuse_tangents(logits, temperature)
     if logits.requires_grad and torch.is_grad_enabled():
         keys, *out = _TokenLogprobs.apply(logits, tokens, temperature, bitmask, shape, entropy,
                                           int(top_n), workspace)
@@ -182,6 +195,8 @@ def token_logprobs_backward(logits, tokens, row_max, log_sum, status, grad_logpr
                          "and unit column stride")
     if given:
         _check_out(out)
+    _refuse_tangents(logits, temperature, row_max, log_sum, grad_logprobs, entropy, grad_entropy,
+                     out)
     rc = _enqueue(
         load().qs_token_logprobs_backward, index,
         logits.data_ptr(), _code(logits, "logits"), B, V, logits.stride(0), _addr(temperature),
@@ -237,7 +252,7 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
     (code - zero) * scale. Returns logits [B, V] in `dtype` (bfloat16 unless
     given) with rows laid out as the selection reads them; out: where to write
     them (counted as a change in place). Enqueued on the current stream. Inference
-    only: tensors that require a gradient are refused.
+    only: tensors that require a gradient or carry a tangent are refused.
     """
     if hidden.dtype is not torch.bfloat16 or hidden.dim() != 2 or not hidden.is_cuda \
             or hidden.stride(1) != 1:
@@ -260,6 +275,7 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
     if (hidden.requires_grad or scales.requires_grad) and torch.is_grad_enabled():
         raise ValueError("head_logits has no gradient: call it under torch.no_grad() "
                          "or on detached tensors")
+    _refuse_tangents(hidden, scales, out)
     given = out is not None
     if not given:
         out = _padded_rows(B, V, dtype or torch.bfloat16, hidden.device)
