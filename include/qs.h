@@ -466,7 +466,8 @@ QS_API int qs_top_logprobs(int64_t B, const int32_t* cand_ids, const float* cand
  * workspace    qs_token_logprobs_workspace_bytes(B, V, dtype, top_n) bytes of
  *              device scratch, 256-byte aligned (NULL / 0 when that is 0), as
  *              for qs_filter_mask: its contents on entry do not matter, calls
- *              that may overlap in time need different ones.
+ *              that may overlap in time need different ones. The size for B rows
+ *              does for any smaller batch of the same V, dtype and top_n.
  * Sums are held in float32 per lane and joined in a fixed order: the same call
  * gives the same bits. Logits are read once, and the few pieces of 16 bytes that
  * hold top tokens again. One kernel launch on `stream` for rows of at most 32768

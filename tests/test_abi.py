@@ -385,3 +385,14 @@ def test_head_logits_rejects_bad_arguments(lib, kw):
 def test_head_logits_empty_batch(lib):
     assert lib.qs_head_logits(None, 0, 256, 256, None, 64, 128, None, 0, 4, None, 0, 64, None, 0,
                               64, None) == _lib.QS_OK
+
+
+@pytest.mark.parametrize("V,dtype", [(151936, 1), (65537, 1), (131073, 1), (32769, 0), (128256, 0),
+                                     (1 << 20, 0), (1 << 24, 1)])
+@pytest.mark.parametrize("top_n", [0, 1, 64])
+def test_token_logprobs_workspace_serves_smaller_batches(lib, V, dtype, top_n):
+    """Scratch memory sized for a batch also does for every smaller one."""
+    f = lib.qs_token_logprobs_workspace_bytes
+    sizes = [f(B, V, dtype, top_n) for B in list(range(1, 2600)) + [4096, 1 << 16, (1 << 22) - 1]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert sizes[0] > 0

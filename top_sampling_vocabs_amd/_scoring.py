@@ -93,7 +93,8 @@ def _padded_rows(B, V, dtype, device):
 
 def token_logprobs_workspace_for(logits, top_n=0):
     """A workspace tensor for token_logprobs on these logits, or None when the
-    call needs none. Reuse it across calls on one stream."""
+    call needs none. Reuse it across calls on one stream, for batches of as many
+    rows or fewer."""
     n = load().qs_token_logprobs_workspace_bytes(int(logits.shape[0]), int(logits.shape[1]),
                                                  _code(logits, "logits"), int(top_n))
     return torch.empty(n, dtype=torch.uint8, device=logits.device) if n else None

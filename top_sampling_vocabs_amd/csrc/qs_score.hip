@@ -56,6 +56,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/qs.h"
 #include "qs_device.hpp"
 #include "qs_score.hpp"
@@ -759,10 +761,14 @@ hipError_t launch_dt(const Args& a, int B, int parts, uint8_t* ws, hipStream_t s
 
 }  // namespace
 
+// Enough for every batch of at most B rows: the largest of them whose parts are
+// short has up to twice the parts of a somewhat larger one whose parts are long.
 size_t workspace_bytes(int64_t B, int64_t V, int dtype, int64_t top_n) {
   const int64_t parts = parts_for(B, V, dtype);
   if (parts == 1) return 0;
-  const size_t n = (size_t)B * parts;
+  const int64_t few = kFewParts / parts_of(V, dtype, kPartLoads);  // rows of the last such batch
+  size_t n = (size_t)B * parts;
+  if (B > few) n = std::max(n, (size_t)few * parts_of(V, dtype, kShortLoads));
   return align256(n * sizeof(Part)) + (top_n > 0 ? n * kListCap * sizeof(uint64_t) : 0);
 }
 
