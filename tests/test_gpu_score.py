@@ -824,3 +824,45 @@ def test_forward_mode_is_refused(qs):
                 call()
     torch.cuda.synchronize()
     assert torch.equal(again["logprobs"], out["logprobs"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [9, 1000, 32003])
+def test_grad_of_peaked_rows(qs, V, dtype):
+    """The gradient at a token that is almost certain keeps relative precision.
+    With lp = -log S there (a = 0, so log S alone rounds nothing) its own slots give
+    -g expm1(lp): a rounding each of the sum of the slots, of expm1 (two units),
+    of the product and of the quotient; the other slots' sum times p, with p's few
+    units; and p (lp + H) gH, both terms of one size."""
+    import torch
+    print(f"grad peaked V={V} {dtype}", flush=True)
+    rng = np.random.default_rng(V)
+    B = 8
+    z = rng.normal(0, 2, (B, V))
+    at = rng.integers(0, V, B)
+    z[np.arange(B), at] = [12, 16, 20, 26, 34, 20, 26, 50]
+    z = bf16(z)
+    T = np.array([1, 1, 0.7, 1.3, 1, 1, 1, 1], np.float32)
+    half = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+    for G in (1, 3):
+        tokens = np.repeat(at[:, None], G, 1).astype(np.int32)
+        gl = rng.normal(0, 1, (B, G)).astype(np.float32)
+        if G == 3:
+            tokens[4:, 1] = (at[4:] + 1) % V
+            gl[4:, 1] *= 1e-9              # of the size of what the peak leaves
+        for gH in (None, rng.normal(0, 1, B).astype(np.float32)):
+            _, out, grad = run_grad(qs, z, dtype, tokens, T, None, gl, gH)
+            got = grad.float().cpu().numpy().astype(np.float64)
+            for r in range(B):
+                ls, H = (float(out[k][r]) for k in ("log_sum", "entropy"))
+                own = tokens[r] == at[r]
+                hit, rest = (gl[r][m].astype(np.float64) for m in (own, ~own))
+                p = math.exp(-ls)
+                g = 0.0 if gH is None else float(gH[r])
+                want = (-hit.sum() * math.expm1(-ls) - rest.sum() * p
+                        - g * p * (H - ls)) / T[r]
+                tol = U * ((G + 8) * np.abs(hit).sum() * -math.expm1(-ls)
+                           + (G + 8) * np.abs(rest).sum() * p
+                           + 8 * abs(g) * p * (H + ls)) / T[r]
+                tol = tol * 1.01 + half * abs(want) * 1.01 + 2.0 ** -126
+                assert abs(got[r, at[r]] - want) <= tol, (r, G, got[r, at[r]], want, tol)

@@ -11,11 +11,17 @@
 // A workgroup takes kLoads 16-byte loads per lane of one row. Which 16-byte
 // chunks hold a given token is a bitmap in LDS (built from the row's token
 // list; a single token is compared directly), so that only those chunks look
-// at the list. Measured: 2048 rows of 151936 bf16, one token each, 222 us
-// (5.6 TB/s read and written, where a large copy reaches 4.8); 333 masked rows
-// of 128259, four tokens each, 39 us (4.4 TB/s, the launch and the token lists
+// at the list. Measured: 2048 rows of 151936 bf16, one token each, 225 us
+// (5.5 TB/s read and written, where a large copy reaches 4.8); 333 masked rows
+// of 128259, four tokens each, 39.5 us (4.5 TB/s, the launch and the token lists
 // included). A token named by several slots gets their sum, in slot order,
 // and each element is rounded once.
+//
+// At a given token the sum of its own slots enters as gl (1 - p) = -gl expm1(log p):
+// where the token is almost certain, gl / T and p A would cancel to the rounding
+// of either, and what the rest of the row gets would have no counterpart. The
+// other slots' sum is added up without its own for the same reason. (1 us of the
+// 225, 0.6 of the 39.5.)
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -75,7 +81,7 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   const float inv_T = fminf(1.0f / T, 1e38f);
   const float c = fminf(fmaxf(1.4426950408889634f / T, 1.17549435e-38f), 3.4e38f);
   const float m = a.row_max[r];
-  const float ls2 = a.log_sum[r] * 1.4426950408889634f;
+  const float ls = a.log_sum[r], ls2 = ls * 1.4426950408889634f;
   float gs = 0.0f;
   int only = -1;
   if constexpr (ONE) {
@@ -103,6 +109,17 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   const float A = clamp_to(-(gs + gH * H) * inv_T, 3e38f, lost);
   const float Bc = clamp_to(-gH * 0.6931471805599453f * inv_T, 1e36f, lost);
 
+  auto logit = [](const uint32_t* w, int e) {
+    if constexpr (DT == QS_F32) return __uint_as_float(w[e]);
+    return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+  };
+  // a given token's element, its slots' sum and that of the others apart
+  auto given = [&](float z, float own, float others) {
+    const float lp = fmaxf((z - m) / T - ls, -140.0f);
+    const float p = __builtin_amdgcn_exp2f((z - m) * c - ls2);
+    return -(own * expm1f(lp) + others * p + gH * (p * (lp + H))) / T;
+  };
+
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
     const int k = u * kBlock + tid;
@@ -112,30 +129,36 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
     float x[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      float z;
-      if constexpr (DT == QS_F32) z = __uint_as_float(w[e]);
-      else z = __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
-      const float l = fmaxf((z - m) * c - ls2, -200.0f);
+      const float l = fmaxf((logit(w, e) - m) * c - ls2, -200.0f);
       x[e] = __builtin_amdgcn_exp2f(l) * (A + Bc * l);
     }
+    uint32_t hits = 0u;  // the load's given tokens
     if constexpr (ONE) {
-      if (only >= i && only < i + P) {
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-          if (only == i + e) x[e] += gs * inv_T;
-      }
+      if (only >= i && only < i + P) hits = 1u << (only - i);
     } else if ((s_hit[k >> 5] >> (k & 31)) & 1u) {
-      float hit[P];
-#pragma unroll
-      for (int e = 0; e < P; ++e) hit[e] = 0.0f;
       for (int g = 0; g < a.G; ++g) {
-        const int t = tokens[g] - i;
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-          if (t == e) hit[e] += gl[g];
+        const int t = tokens[g];
+        if (t >= i && t < i + P && t < a.V) hits |= 1u << (t - i);
+      }
+    }
+    // one at a time: they are rare, and sums kept for all eight cost three waves a SIMD
+    for (; hits != 0u; hits &= hits - 1u) {
+      const int at = __builtin_ctz(hits);
+      float own = gs, others = 0.0f, z = 0.0f;
+      if constexpr (!ONE) {
+        own = 0.0f;
+        for (int g = 0; g < a.G; ++g) {
+          const int t = tokens[g];
+          if (t < 0 || t >= a.V) continue;
+          if (t == i + at) own += gl[g];
+          else others += gl[g];
+        }
       }
 #pragma unroll
-      for (int e = 0; e < P; ++e) x[e] += hit[e] * inv_T;
+      for (int e = 0; e < P; ++e) z = at == e ? logit(w, e) : z;
+      const float y = given(z, own, others);
+#pragma unroll
+      for (int e = 0; e < P; ++e) x[e] = at == e ? y : x[e];
     }
     uint32_t o[4];
 #pragma unroll
