@@ -396,3 +396,22 @@ def test_token_logprobs_workspace_serves_smaller_batches(lib, V, dtype, top_n):
     sizes = [f(B, V, dtype, top_n) for B in list(range(1, 2600)) + [4096, 1 << 16, (1 << 22) - 1]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
     assert sizes[0] > 0
+
+
+def test_scoring_module_needs_no_private_torch_names(monkeypatch):
+    """Without torch's private device and stream calls the module takes the public
+    ones."""
+    import importlib.util
+    torch = pytest.importorskip("torch")
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda device: type("S", (), {"cuda_stream": 77 + device}))
+    path = os.path.join(_lib.PKG, "_scoring.py")
+    spec = importlib.util.spec_from_file_location(_lib.__package__ + "._scoring_public", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module._enqueue(lambda *a: seen.append(a) or 0, 3, "x") == 0
+    assert seen == [("x", 80)]

@@ -11,8 +11,11 @@ from torch.autograd import forward_ad
 from ._lib import QS_BF16, QS_F32, _check_logits, _status, load, sample
 
 _CODES = {torch.float32: QS_F32, torch.bfloat16: QS_BF16}
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream  # a handle; no Stream object made
+# what torch.cuda's own calls are made of, without their checks and without a Stream
+# object; those themselves where a torch does not have these
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _code(t, name):
