@@ -866,3 +866,34 @@ def test_grad_of_peaked_rows(qs, V, dtype):
                            + 8 * abs(g) * p * (H + ls)) / T[r]
                 tol = tol * 1.01 + half * abs(want) * 1.01 + 2.0 ** -126
                 assert abs(got[r, at[r]] - want) <= tol, (r, G, got[r, at[r]], want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_temperatures(qs, dtype):
+    """Temperatures up to float32's largest value over logits of that size: log2(e) / T
+    is below the least normal float32 there, still good to 2^-22 of itself, which
+    |a| below 3 turns into 12 units at most (the sums' own tolerance has 128)."""
+    print(f"score largest temperatures {dtype}", flush=True)
+    T = np.array([1e37, 1e38, 1.2e38, 1.3e38, 2e38, 3e38, 3.4e38], np.float32)
+    rng = np.random.default_rng(8)
+    B = T.size
+    for V in (40, 3001, 70003):
+        z = bf16(rng.uniform(-1.6e38, 1.6e38, (B, V)))
+        tokens = tokens_for(rng, B, V, 3)
+        _, _, _, out = run(qs, z, dtype, tokens, T, None, 4)
+        check_forward(z, tokens, T, None, 4, out)
+
+
+def test_grad_at_largest_temperatures(qs):
+    """Gradients large enough that their quotients by such temperatures are normal
+    numbers."""
+    print("grad largest temperatures", flush=True)
+    T = np.array([1e37, 1.2e38, 2e38, 3.4e38], np.float32)
+    rng = np.random.default_rng(9)
+    B, V = T.size, 3001
+    z = bf16(rng.uniform(-1.6e38, 1.6e38, (B, V)))
+    tokens = tokens_for(rng, B, V, 2)
+    gl = (1e20 * rng.normal(0, 1, (B, 2))).astype(np.float32)
+    gH = (1e20 * rng.normal(0, 1, B)).astype(np.float32)
+    _, out, grad = run_grad(qs, z, "f32", tokens, T, None, gl, gH)
+    check_grad(z, "f32", tokens, T, None, gl, gH, out, grad)

@@ -117,9 +117,10 @@ int64_t parts_for(int64_t B, int64_t V, int dtype) {
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // log2(e) / T held to finite, non-zero values: 0 times it is 0, and -inf
-// times it is -inf.
+// times it is -inf. (Past T = 1.2e38 it is below the least normal float32, still
+// good to 2^-22 of itself.)
 __device__ __forceinline__ float scale_of(float T) {
-  return fminf(fmaxf(kLog2e / T, 1.17549435e-38f), 3.4e38f);
+  return fminf(fmaxf(kLog2e / T, 1.4e-45f), 3.4e38f);
 }
 
 template <int CTRL>

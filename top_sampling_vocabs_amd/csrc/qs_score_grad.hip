@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
 
   const float T = a.T ? a.T[r] : 1.0f;
   const float inv_T = fminf(1.0f / T, 1e38f);
-  const float c = fminf(fmaxf(1.4426950408889634f / T, 1.17549435e-38f), 3.4e38f);
+  const float c = fminf(fmaxf(1.4426950408889634f / T, 1.4e-45f), 3.4e38f);
   const float m = a.row_max[r];
   const float ls = a.log_sum[r], ls2 = ls * 1.4426950408889634f;
   float gs = 0.0f;
