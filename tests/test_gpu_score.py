@@ -897,3 +897,22 @@ def test_grad_at_largest_temperatures(qs):
     gH = (1e20 * rng.normal(0, 1, B)).astype(np.float32)
     _, out, grad = run_grad(qs, z, "f32", tokens, T, None, gl, gH)
     check_grad(z, "f32", tokens, T, None, gl, gH, out, grad)
+
+
+@pytest.mark.parametrize("T", [2e-38, 1e-38, 3e-39, 1e-39, 1e-41])
+def test_grad_at_smallest_temperatures(qs, T):
+    """Two equal maxima share the row, everything else has no weight: the gradient at
+    a given one is g / (2 T), at the other -g / (2 T), by a float32 product and
+    quotient, also where 1 / T has no float32."""
+    print(f"grad smallest temperature {T}", flush=True)
+    z = np.full((1, 300), -2.0, np.float32)
+    z[0, [11, 200]] = 1.5
+    T = np.array([T], np.float32)
+    g = np.float32(float(T[0]) * 1e30)
+    _, out, grad = run_grad(qs, z, "f32", np.array([[200]], np.int32), T, None,
+                            np.array([[g]], np.float32), None)
+    got = grad[0].cpu().numpy().astype(np.float64)
+    want = float(g) / (2 * float(T[0]))
+    assert abs(got[200] - want) <= 16 * U * want and abs(got[11] + want) <= 16 * U * want
+    got[[11, 200]] = 0
+    assert (got == 0).all()

@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   }
 
   const float T = a.T ? a.T[r] : 1.0f;
-  const float inv_T = fminf(1.0f / T, 1e38f);
   const float c = fminf(fmaxf(1.4426950408889634f / T, 1.4e-45f), 3.4e38f);
   const float m = a.row_max[r];
   const float ls = a.log_sum[r], ls2 = ls * 1.4426950408889634f;
@@ -106,8 +105,8 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   // finite where the row's incoming sums are, so that a p of 0 gives 0; infinities
   // and NaN go through to every legal token
   const bool lost = !(fabsf(gs) < INFINITY && fabsf(gH) < INFINITY && fabsf(H) < INFINITY);
-  const float A = clamp_to(-(gs + gH * H) * inv_T, 3e38f, lost);
-  const float Bc = clamp_to(-gH * 0.6931471805599453f * inv_T, 1e36f, lost);
+  const float A = clamp_to(-(gs + gH * H) / T, 3e38f, lost);
+  const float Bc = clamp_to(-gH * 0.6931471805599453f / T, 1e36f, lost);
 
   auto logit = [](const uint32_t* w, int e) {
     if constexpr (DT == QS_F32) return __uint_as_float(w[e]);
