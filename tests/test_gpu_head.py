@@ -450,3 +450,46 @@ def test_captured_and_replayed_long_rows(qs, own):
             torch.cuda.synchronize()
             for n in want:
                 assert torch.equal(bits(got[n]), bits(want[n])), (k, n)
+
+
+@pytest.mark.parametrize("B", [1, 8, 20, 40])
+def test_most_vocabulary_rows(qs, B):
+    """2^24 vocabulary rows, the most a call takes: every logit of some rows' tiles,
+    the first and the last among them."""
+    import torch
+    print(f"head most vocabulary rows B={B}", flush=True)
+    V, K = 1 << 24, 32
+    x, codes, s, z = make(B, B, 4096, K, 32, True, "bf16")
+    many = V // 4096
+    # every block of 4096 rows of weights is the same but for its scale, a power of two
+    power = torch.exp2((torch.arange(many, device="cuda") % 7).float()).repeat_interleave(4096)
+    scales = (s.cuda().repeat(many, 1).float() * power[:, None]).bfloat16()
+    got = qs.head_logits(x.cuda(), codes.cuda().repeat(many, 1), scales, z.cuda().repeat(many, 1))
+    torch.cuda.synchronize()
+    blocks = got.view(B, many, 4096)
+    check(x, codes, s, z, 32, blocks[:, 0], "bf16")
+    assert torch.equal(blocks.float(), blocks[:, :1].float()
+                       * power.view(many, 4096)[None])
+
+
+def test_most_rows(qs):
+    """2^20 hidden rows, the most a call takes, and the first count past them."""
+    import torch
+    print("head most rows", flush=True)
+    B, V, K = 1 << 20, 19, 64
+    x, codes, s, z = make(7, B, V, K, 64, True, "f32")
+    got = qs.head_logits(x.cuda(), codes.cuda(), s.cuda(), z.cuda(), dtype=torch.float32)
+    torch.cuda.synchronize()
+    check(x, codes, s, z, 64, got, "f32")
+    with pytest.raises(RuntimeError):
+        qs.head_logits(torch.zeros(B + 1, K, dtype=torch.bfloat16, device="cuda"), codes.cuda(),
+                       s.cuda(), z.cuda())
+
+
+def test_empty_batch_of_hidden_states(qs):
+    import torch
+    x, codes, s, z = (t.cuda() for t in make(1, 2, 64, 256, 64, True, "f32"))
+    none = torch.zeros(0, device="cuda")
+    out = qs.sample_hidden(x[:0], codes, s, z, none, none.int(), none,
+                           uniforms=none.double())
+    assert out["logits"].shape == (0, 64) and out["tokens"].shape == (0,)

@@ -916,3 +916,116 @@ def test_grad_at_smallest_temperatures(qs, T):
     assert abs(got[200] - want) <= 16 * U * want and abs(got[11] + want) <= 16 * U * want
     got[[11, 200]] = 0
     assert (got == 0).all()
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 70001), ("f32", 20001), ("f32", 40001)])
+def test_many_tokens_of_long_rows(qs, dtype, V):
+    """More given tokens than the workgroup that writes them has threads."""
+    print(f"score many tokens V={V} {dtype}", flush=True)
+    rng = np.random.default_rng(V)
+    z = make(V, 3, V, "normal")
+    tokens = tokens_for(rng, 3, V, 1024)
+    tokens[2, 1023] = V                    # an error in the last slot
+    for n in (0, 20):
+        _, _, _, out = run(qs, z, dtype, tokens, None, None, n)
+        check_forward(z, tokens, None, None, n, out)
+
+
+@pytest.mark.parametrize("V", [45, 3001, 70001])
+def test_bits_past_the_row_are_ignored(qs, V):
+    """Legal bits from V on, in the last word and in a wider stride's words."""
+    import torch
+    print(f"score bits past the row V={V}", flush=True)
+    rng = np.random.default_rng(V)
+    B = 3
+    z = make(V, B, V, "normal")
+    legal = rng.random((B, V)) < 0.5
+    legal[2] = False                       # no legal token, whatever lies behind
+    tokens = tokens_for(rng, B, V, 2)
+    gl = rng.normal(0, 1, (B, 2)).astype(np.float32)
+    W = -(-V // 32)
+    words = np.full((B, W + 3), 0xFFFFFFFF, np.uint32)
+    words[:, :W] = pack(legal).view(np.uint32)
+    words[:, W - 1] |= np.uint32((0xFFFFFFFF << (V % 32)) & 0xFFFFFFFF)
+    bm = torch.from_numpy(words.view(np.int32)).cuda()[:, :W]
+    tok = torch.from_numpy(tokens).cuda()
+    for dtype in ("f32", "bf16"):
+        lg = on_gpu(z, dtype, extra=1)
+        out = qs.token_logprobs(lg, tok, bitmask=bm, entropy=True, top_n=5)
+        grad = qs.token_logprobs_backward(lg, tok, out["row_max"], out["log_sum"], out["status"],
+                                          torch.from_numpy(gl).cuda(), bitmask=bm)
+        torch.cuda.synchronize()
+        check_forward(z, tokens, None, legal, 5, out)
+        check_grad(z, dtype, tokens, None, legal, gl, None, out, grad)
+
+
+def test_most_rows(qs):
+    """The largest batch, 2^22 - 1 rows. Seven terms of S, so log S is off by 16 + 4 sum
+    p |a| units at most (|a| < 64, p |a| below 1/e each) and a log-probability by
+    4 |a| units more; a gradient element of size at most 1 by 4 + 4 p |a| units
+    and a bf16 half step."""
+    import torch
+    print("score most rows", flush=True)
+    B, V = (1 << 22) - 1, 7
+    torch.manual_seed(3)
+    z = torch.randn(B, 8, device="cuda").mul_(3).bfloat16()[:, :V]
+    tok = torch.randint(0, V, (B,), dtype=torch.int32, device="cuda")
+    out = qs.token_logprobs(z, tok, top_n=2)
+    lp = torch.log_softmax(z.double(), 1)
+    at = tok.long()[:, None]
+    want = lp.gather(1, at)[:, 0]
+    assert bool((out["status"] == 0).all())
+    assert bool(((out["logprobs"] - want).abs() <= U * (64 + 5 * want.abs())).all())
+    best = torch.sort(z.float(), dim=1, descending=True, stable=True).indices[:, :2]
+    assert torch.equal(out["top_ids"], best.int())
+    grad = qs.token_logprobs_backward(z, tok, out["row_max"], out["log_sum"], out["status"],
+                                      torch.ones(B, device="cuda"))
+    want = (-lp.exp()).scatter_add_(1, at, torch.ones_like(at, dtype=torch.float64))
+    tol = 2.0 ** -8 * 1.01 * want.abs() + 64 * U
+    assert bool(((grad - want).abs() <= tol).all())
+
+
+def test_empty_batches(qs):
+    """No rows: outputs of the right shape, no error, in every call."""
+    import torch
+    e = dict(device="cuda")
+    z, tok = torch.zeros(0, 64, **e), torch.zeros((0, 2), dtype=torch.int32, **e)
+    row, st = torch.zeros(0, **e), torch.zeros(0, dtype=torch.int32, **e)
+    grad = qs.token_logprobs_backward(z, tok, row, row, st, torch.zeros((0, 2), **e), entropy=row,
+                                      grad_entropy=row)
+    assert grad.shape == (0, 64)
+    leaf = z.clone().requires_grad_()
+    out = qs.token_logprobs(leaf, tok, entropy=True)
+    (out["logprobs"].sum() + out["entropy"].sum()).backward()
+    assert leaf.grad.shape == (0, 64)
+    long = torch.zeros(0, 70016, **e)
+    assert qs.token_logprobs_workspace_for(long, 5) is None
+    assert qs.token_logprobs(long, tok, top_n=5)["top_ids"].shape == (0, 5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3001, 70001])
+def test_lowest_values(qs, V, dtype):
+    """The type's lowest value as a mask: in half a row, in all of it, in all but one
+    token, with and without other tokens in the same wave."""
+    print(f"lowest values V={V} {dtype}", flush=True)
+    rng = np.random.default_rng(V)
+    low = np.float32(np.finfo(np.float32).min) if dtype == "f32" else \
+        np.uint32(0xFF7F0000).view(np.float32)
+    B = 5
+    z = make(V, B, V, "normal")
+    z[0, rng.random(V) < 0.5] = low
+    z[1] = low
+    z[2, : V // 2] = low
+    z[3] = low
+    z[3, V - 1] = -3.0
+    z[4] = low
+    z[4, 0] = -np.inf
+    T = np.array([0.3, 0.7, 2.0, 1.0, 1e-3], np.float32)
+    tokens = tokens_for(rng, B, V, 2, pad=False)
+    gl = rng.normal(0, 1, (B, 2)).astype(np.float32)
+    gH = rng.normal(0, 1, B).astype(np.float32)
+    _, _, _, out = run(qs, z, dtype, tokens, T, None, 20)
+    check_forward(z, tokens, T, None, 20, out)
+    _, out, grad = run_grad(qs, z, dtype, tokens, T, None, gl, gH)
+    check_grad(z, dtype, tokens, T, None, gl, gH, out, grad)
