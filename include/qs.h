@@ -441,6 +441,8 @@ QS_API int qs_top_logprobs(int64_t B, const int32_t* cand_ids, const float* cand
  * tokens. With L the legal tokens of the row, m = max over L of z and
  * S = sum over L of exp((z - m) / T):
  *   log p_t = (z_t - m) / T - ln S,   H = -sum over L of p ln p.
+ * Differences z - m and quotients are float32: a token more than its largest value
+ * below m has no weight.
  *
  * logits, bitmask   as for qs_filter_mask (dtype float32 or bfloat16)
  * temperature  [B] float32, optional (NULL: 1); finite and > 0 (0, the greedy

@@ -359,8 +359,9 @@ constexpr int kMaxTiles = 5;             // tiles a wave holds at once
 //
 // Measured: 64 rows, 151936 x 8192 in groups of 128, 235 us (680 TFLOP/s, 2.8
 // TB/s; 288 with 3 tiles a wave and scales read per chunk); in groups of 32 with
-// float32 scales, 289 us (317); 48 rows, 100003 x 4096 in groups of 32 with zero
-// points, 140 us (187). With all loads but the first taken out the products of
+// float32 scales, 287 us (317; the first calls after a pause up to 350); 48 rows,
+// 100003 x 4096 in groups of 32 with zero points, 140 us (187). With all loads but
+// the first taken out the products of
 // the first two take 181 and 210 us (the factors and, at small groups, the
 // scaling cost as many vector instructions as products); the loads alone 168 and
 // 196. 8 waves a compute unit are all that the registers of 5 tiles by 64 rows

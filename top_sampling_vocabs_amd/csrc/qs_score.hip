@@ -36,11 +36,10 @@
 // exponentials; a second launch joins the parts of each row. Where that gives
 // at most kFewParts parts they are halved, so that the chip fills evenly.
 //
-// Measured: 2048 rows of 151936 bf16, 112 us (5.6 TB/s, where a large copy
-// reaches 4.8: bound by the reads); 256 such rows with a mask and 20 top tokens,
-// 34 us, 6 of them the join (2.4 TB/s: bound by the vector instructions, about a
-// dozen a token, and by the top tokens' LDS lists); one row of 32000, 8 us, its
-// latency. A workgroup per row that walks the row
+// Measured: 2048 rows of 151936 bf16, 110 us (5.6 TB/s, where a large copy
+// reaches 4.8: bound by the reads); 256 such rows, 18.9 us and 3.9 for the join,
+// with a mask 2 more, with 20 top tokens 5 and 2 more, with both 29.7 and 6.2 (each
+// part searches for its own top tokens); one row of 32000 fp32, 8 us, its latency. A workgroup per row that walks the row
 // in a loop, with one launch, was slower in every form tried (28 us against
 // 24 + 5.6 for the 256 rows; 21 against 11 + 4.6 for 64 rows of 128256 fp32).
 //
