@@ -1029,3 +1029,34 @@ def test_lowest_values(qs, V, dtype):
     check_forward(z, tokens, T, None, 20, out)
     _, out, grad = run_grad(qs, z, dtype, tokens, T, None, gl, gH)
     check_grad(z, dtype, tokens, T, None, gl, gH, out, grad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["spread", "close", "one"])
+def test_grad_token_lists(qs, kind, dtype):
+    """1024 slots spread over a row, next to each other across the border of two
+    workgroups, and all of one token; illegal tokens and empty slots among them.
+    In place and twice: the same bits."""
+    import torch
+    print(f"grad token lists {kind} {dtype}", flush=True)
+    rng = np.random.default_rng(31)
+    B, V, G = 3, 40003, 1024
+    z = make(31, B, V, "normal")
+    legal = rng.random((B, V)) < 0.7
+    tokens = {"spread": rng.integers(0, V, (B, G)),
+              "close": 8192 - G // 4 + rng.integers(0, G // 2, (B, G)),
+              "one": np.full((B, G), 8191)}[kind].astype(np.int32)
+    tokens[rng.random((B, G)) < 0.1] = -1
+    legal[:2, 8191] = True
+    legal[2, 8191] = False
+    gl = rng.normal(0, 1, (B, G)).astype(np.float32)
+    gH = rng.normal(0, 1, B).astype(np.float32)
+    _, out, grad = run_grad(qs, z, dtype, tokens, None, legal, gl, gH)
+    check_grad(z, dtype, tokens, None, legal, gl, gH, out, grad)
+    lg, tok, d, _ = run(qs, z, dtype, tokens, None, legal)
+    args = (tok, out["row_max"], out["log_sum"], out["status"], torch.from_numpy(gl).cuda())
+    ent = dict(entropy=out["entropy"], grad_entropy=torch.from_numpy(gH).cuda())
+    for o in (None, lg):
+        again = qs.token_logprobs_backward(lg, *args, out=o, **d, **ent)
+        torch.cuda.synchronize()
+        assert torch.equal(again, grad)

@@ -39,9 +39,10 @@
 // Measured: 2048 rows of 151936 bf16, 110 us (5.6 TB/s, where a large copy
 // reaches 4.8: bound by the reads); 256 such rows, 18.9 us and 3.9 for the join,
 // with a mask 2 more, with 20 top tokens 5 and 2 more, with both 29.7 and 6.2 (each
-// part searches for its own top tokens); one row of 32000 fp32, 8 us, its latency. A workgroup per row that walks the row
-// in a loop, with one launch, was slower in every form tried (28 us against
-// 24 + 5.6 for the 256 rows; 21 against 11 + 4.6 for 64 rows of 128256 fp32).
+// part searches for its own top tokens); one row of 32000 fp32, 8 us, its latency.
+// A workgroup per row that walks the row in a loop, with one launch, was slower in
+// every form tried (28 us against 24 + 5.6 for the 256 rows; 21 against 11 + 4.6 for
+// 64 rows of 128256 fp32).
 //
 // Top tokens: with t the n-th largest of the maxima of 256 groups of lanes, n
 // tokens (one of each of n groups) reach t, so the n largest tokens lie among

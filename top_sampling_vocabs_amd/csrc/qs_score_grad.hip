@@ -8,20 +8,24 @@
 // so a token costs one exponential and a few operations, and the kernel is
 // bound by reading the logits and writing their gradient once.
 //
-// A workgroup takes kLoads 16-byte loads per lane of one row. Which 16-byte
-// chunks hold a given token is a bitmap in LDS (built from the row's token
-// list; a single token is compared directly), so that only those chunks look
-// at the list. Measured: 2048 rows of 151936 bf16, one token each, 225 us
-// (5.5 TB/s read and written, where a large copy reaches 4.8); 333 masked rows
-// of 128259, four tokens each, 39.5 us (4.5 TB/s, the launch and the token lists
-// included). A token named by several slots gets their sum, in slot order,
-// and each element is rounded once.
+// A workgroup takes kLoads 16-byte loads per lane of one row. The row's single
+// token is compared directly. Of a list of tokens one wave keeps the slots that lie
+// in this workgroup, in LDS; a thread to each works out its token's element from
+// them, and the elements are written over the 16-byte stores at the end, so that
+// the other 8191 know nothing of the list. (Every 16-byte chunk with a given token
+// going through the list itself: 333 masked rows of 128259 with four tokens each
+// 38.6 us against 35.2; 512 rows of 151936 with 64 tokens 189 against 53, with 1024
+// tokens 7.4 ms against 90 us.) A token named by several slots gets their sum, in
+// slot order, and each element is rounded once.
 //
 // At a given token the sum of its own slots enters as gl (1 - p) = -gl expm1(log p):
 // where the token is almost certain, gl / T and p A would cancel to the rounding
 // of either, and what the rest of the row gets would have no counterpart. The
-// other slots' sum is added up without its own for the same reason. (1 us of the
-// 225, 0.6 of the 39.5.)
+// other slots' sum is added up without its own for the same reason.
+//
+// Measured: 2048 rows of 151936 bf16, one token each, 225 us (5.5 TB/s read and
+// written, where a large copy reaches 4.8); the 333 rows 35.2 us (5.0 TB/s, the
+// launch included).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -50,7 +54,10 @@ __device__ __forceinline__ float clamp_to(float x, float most, bool keep) {
 template <int DT, bool MASK, bool ONE>
 __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   constexpr int P = kPer<DT>;
-  __shared__ uint32_t s_hit[kBlock * kLoads / 32];
+  __shared__ int2 s_slot[ONE ? 1 : kTokensMax];  // this block's slots: place, gradient's bits
+  __shared__ float s_given[ONE ? 1 : kTokensMax];
+  __shared__ int s_slots;
+  __shared__ float s_sum[2];
   const int tid = threadIdx.x;
   const int r = (int)(blockIdx.x / (unsigned)chunks);
   const int begin = (int)(blockIdx.x - (unsigned)r * (unsigned)chunks) * (kBlock * kLoads * P);
@@ -87,19 +94,44 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
     only = tokens[0];
     if (only >= 0 && only < a.V) gs = gl[0];
   } else {
-    for (int k = tid; k < kBlock * kLoads / 32; k += kBlock) s_hit[k] = 0u;
-    __syncthreads();
-    // every wave sums the list (the same order, the same bits)
-    for (int g = lane_id(); g < a.G; g += 64) {
-      const int t = tokens[g];
-      if (t < 0 || t >= a.V) continue;
-      gs += gl[g];
-      const int k = (t - begin) / P;
-      if (t >= begin && k < kBlock * kLoads) atomicOr(&s_hit[k >> 5], 1u << (k & 31));
-    }
+    // one wave reads the list: sums over the whole row, and the slots whose tokens
+    // lie in this block, in slot order
+    if (tid < 64) {
+      float away = 0.0f;
+      int n = 0;
+      for (int g0 = 0; g0 < a.G; g0 += 64) {
+        const int g = g0 + tid;
+        int t = -1;
+        float v = 0.0f;
+        if (g < a.G) {
+          t = tokens[g];
+          v = gl[g];
+        }
+        if (t < 0 || t >= a.V) t = -1, v = 0.0f;
+        const int d = t - begin;
+        const bool here = t >= begin && d < kBlock * kLoads * P;
+        const uint64_t lanes = ballot(here);
+        if (here)
+          s_slot[n + __popcll(lanes & ((1ull << tid) - 1ull))] =
+              make_int2(d, (int)__float_as_uint(v));
+        else
+          away += v;
+        gs += v;
+        n += __popcll(lanes);
+      }
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) gs += __shfl_xor(gs, off, 64);
+      for (int off = 32; off > 0; off >>= 1) {
+        gs += __shfl_xor(gs, off, 64);
+        away += __shfl_xor(away, off, 64);
+      }
+      if (tid == 0) {
+        s_slots = ok ? n : 0;
+        s_sum[0] = gs;
+        s_sum[1] = away;
+      }
+    }
     __syncthreads();
+    gs = s_sum[0];
   }
   const float gH = a.g_ent ? a.g_ent[r] : 0.0f, H = a.g_ent ? a.entropy[r] : 0.0f;
   // finite where the row's incoming sums are, so that a p of 0 gives 0; infinities
@@ -119,10 +151,34 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
     return -(own * expm1f(lp) + others * p + gH * (p * (lp + H))) / T;
   };
 
+  // a thread to each of the block's slots: its token's element, written over the
+  // others' 16 bytes at the end (slots of one token write the same bits)
+  int slots = 0;
+  if constexpr (!ONE) {
+    slots = s_slots;
+    for (int j = tid; j < slots; j += kBlock) {
+      const int d = s_slot[j].x, i = begin + d;
+      float z;
+      if constexpr (DT == QS_F32) z = reinterpret_cast<const float*>(row)[i];
+      else z = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
+      bool is_legal = true;
+      if constexpr (MASK)
+        is_legal = (a.bitmask[(size_t)r * a.bm_stride + (i >> 5)] >> (i & 31)) & 1u;
+      float own = 0.0f, others = s_sum[1];
+      for (int q = 0; q < slots; ++q) {
+        const int2 slot = s_slot[q];
+        const float v = __uint_as_float((uint32_t)slot.y);
+        own += slot.x == d ? v : 0.0f;
+        others += slot.x == d ? 0.0f : v;
+      }
+      s_given[j] = is_legal ? given(z, own, others) : 0.0f;
+    }
+    if (slots > 0) __syncthreads();  // in place: no element changes before it is read here
+  }
+
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
-    const int k = u * kBlock + tid;
-    const int i = begin + k * P;
+    const int i = begin + (u * kBlock + tid) * P;
     if (i >= a.V) break;
     const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     float x[P];
@@ -131,33 +187,16 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
       const float l = fmaxf((logit(w, e) - m) * c - ls2, -200.0f);
       x[e] = __builtin_amdgcn_exp2f(l) * (A + Bc * l);
     }
-    uint32_t hits = 0u;  // the load's given tokens
     if constexpr (ONE) {
-      if (only >= i && only < i + P) hits = 1u << (only - i);
-    } else if ((s_hit[k >> 5] >> (k & 31)) & 1u) {
-      for (int g = 0; g < a.G; ++g) {
-        const int t = tokens[g];
-        if (t >= i && t < i + P && t < a.V) hits |= 1u << (t - i);
-      }
-    }
-    // one at a time: they are rare, and sums kept for all eight cost three waves a SIMD
-    for (; hits != 0u; hits &= hits - 1u) {
-      const int at = __builtin_ctz(hits);
-      float own = gs, others = 0.0f, z = 0.0f;
-      if constexpr (!ONE) {
-        own = 0.0f;
-        for (int g = 0; g < a.G; ++g) {
-          const int t = tokens[g];
-          if (t < 0 || t >= a.V) continue;
-          if (t == i + at) own += gl[g];
-          else others += gl[g];
-        }
-      }
+      const int at = only - i;
+      if (at >= 0 && at < P) {
+        float z = 0.0f;
 #pragma unroll
-      for (int e = 0; e < P; ++e) z = at == e ? logit(w, e) : z;
-      const float y = given(z, own, others);
+        for (int e = 0; e < P; ++e) z = at == e ? logit(w, e) : z;
+        const float y = given(z, gs, 0.0f);
 #pragma unroll
-      for (int e = 0; e < P; ++e) x[e] = at == e ? y : x[e];
+        for (int e = 0; e < P; ++e) x[e] = at == e ? y : x[e];
+      }
     }
     uint32_t o[4];
 #pragma unroll
@@ -184,6 +223,14 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
           else reinterpret_cast<uint16_t*>(at)[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
         }
       }
+    }
+  }
+  if (slots > 0) {
+    __syncthreads();
+    for (int j = tid; j < slots; j += kBlock) {
+      const int i = begin + s_slot[j].x;
+      if constexpr (DT == QS_F32) reinterpret_cast<float*>(out)[i] = s_given[j];
+      else reinterpret_cast<__bf16*>(out)[i] = (__bf16)s_given[j];
     }
   }
 }
