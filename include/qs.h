@@ -544,6 +544,117 @@ QS_API int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidd
                       int64_t zero_stride, int64_t group, void* logits, int logits_dtype,
                       int64_t row_stride, void* stream);
 
+/* Distillation from a teacher of which only the top tokens are known: per row the
+ * divergence of the student's tempered, masked softmax p from the teacher's
+ * probabilities q. With L the legal tokens, m = max over L of z and
+ * S = sum over L of exp((z - m) / T), log p_i = (z_i - m) / T - ln S; with j the
+ * teacher's tokens and R the legal tokens that it does not name (the rest):
+ *   loss = sum over j of q_j (ln q_j - ln p_j) + q_R (ln q_R - ln p_R)
+ * with 0 ln 0 = 0. rest = 0: the values are the teacher's logits (or anything that
+ * differs from them by a constant), q their softmax at the row's T over the named
+ * tokens alone, and q_R = 0. rest = 1: the values are the teacher's
+ * log-probabilities at its own temperature, q_j their exponentials and
+ * q_R = max(0, 1 - sum q_j), what the teacher leaves for the rest (0 if no token
+ * of the rest has a finite logit).
+ *
+ * logits, bitmask, temperature   as for qs_token_logprobs
+ * teacher_ids    [B][K] int32, 1 <= K <= 1024: the named tokens, any order; -1 (what
+ *                qs_token_logprobs writes past a row's last token) is an empty slot
+ * teacher_values [B][K] float32; not read in empty slots. -inf is a probability of 0
+ *                (of a token that is named all the same)
+ * rest           0 or 1
+ * loss           [B] float32 out; +inf where the teacher gives a token (or the rest) a
+ *                probability that the student's logit of -inf does not. 0 on a row
+ *                whose teacher names no legal token of positive probability and
+ *                leaves nothing to the rest
+ * row_state      [B][8] float32 out, what the gradient needs: m; ln S; the rest's
+ *                largest logit m_R and ln of the sum over R of exp((z - m_R) / T);
+ *                Q p_R - q_R, with Q = sum q_j + q_R; the teacher's largest value and
+ *                the ln of its sum relative to it (rest = 1: 0, 0); Q - 1. The third
+ *                to fifth are 0 if no token of the rest has a finite logit
+ * row_status     [B] int32 out: QS_ROW_BAD_PARAM (T; an id outside [-1, V) or named
+ *                twice; a legal token's value that is NaN or +inf, or with rest = 1
+ *                above 1), then as for qs_filter_mask. An error row gets NaN in loss and
+ *                row_state.
+ * A slot that names an illegal token counts as empty. workspace:
+ * qs_distill_loss_workspace_bytes(B, V, dtype) bytes, 256-byte aligned (NULL / 0 when
+ * that is 0), as for qs_token_logprobs; the size for B rows does for any smaller
+ * batch. Logits are read once, in float32 sums joined in a fixed order (the same call
+ * gives the same bits); what a row does with its slots is done in float64. Nothing is
+ * allocated. */
+QS_API size_t qs_distill_loss_workspace_bytes(int64_t B, int64_t V, int dtype);
+QS_API int qs_distill_loss(const void* logits, int dtype, int64_t B, int64_t V,
+                      int64_t row_stride, const float* temperature, const uint32_t* bitmask,
+                      int64_t bitmask_stride, const int32_t* teacher_ids,
+                      const float* teacher_values, int64_t K, int rest, float* loss,
+                      float* row_state, int32_t* row_status, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Gradient of qs_distill_loss with respect to the logits, for incoming gradients g of
+ * the losses:
+ *   dz_j = (g / T) (Q p_j - q_j)            for a named legal token,
+ *   dz_i = (g / T) (Q p_R - q_R) p_i / p_R  for every other legal one, 0 for illegal.
+ *
+ * logits, temperature, bitmask, teacher_ids, teacher_values, rest
+ *               the forward call's inputs
+ * row_state, row_status   its outputs (inputs here)
+ * grad_loss     [B] float32
+ * grad_logits   [B][grad_stride] out, as for qs_token_logprobs_backward: the logits'
+ *               dtype, 0 on rows whose row_status is not QS_ROW_OK, it may be the
+ *               logits' own buffer
+ * Computed in float32 (named tokens in float64), rounded to float32 and once to the
+ * dtype. An infinite or NaN incoming gradient leaves no legal token of its row a
+ * finite gradient. One kernel launch on `stream`; nothing is allocated. */
+QS_API int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, int64_t V,
+                      int64_t row_stride, const float* temperature, const uint32_t* bitmask,
+                      int64_t bitmask_stride, const int32_t* teacher_ids,
+                      const float* teacher_values, int64_t K, int rest,
+                      const float* row_state, const int32_t* row_status,
+                      const float* grad_loss, void* grad_logits, int64_t grad_stride,
+                      void* stream);
+
+/* Low-rank adapters of many requests beside a shared output projection: each row's
+ * logits z (qs_head_logits', or any projection's) moved by its own adapter a =
+ * index[b]:
+ *   y[b][v] = z[b][v] + scale[a] * sum over r of up[a][v][r] *
+ *             sum over k of down[a][r][k] * hidden[b][k]
+ *
+ * logits       [B][row_stride] float32 or bfloat16 (dtype), B at most 2^20, V at most
+ *              2^24, 16-byte aligned, row_stride * element size a multiple of 16
+ * hidden       [B][hidden_stride] bfloat16, the hidden states that z came from; 16-byte
+ *              aligned, hidden_stride a multiple of 8 and >= K; K a multiple of 8, at
+ *              most 65536
+ * down         [count] adapters of [rank] rows of K bfloat16, down_stride elements from
+ *              adapter to adapter and down_row_stride (>= K) from row to row
+ * up           [count] adapters of [V] rows of `rank` bfloat16, up_stride and
+ *              up_row_stride (>= rank) likewise. down and up are 16-byte aligned, their
+ *              strides multiples of 8, and may be NULL if count is 0
+ * count        adapters held, 0 <= count < 2^31
+ * rank         a multiple of 8, 8 to 128 (factors of a lower rank: rows and columns of 0)
+ * index        [B] int32: 0 <= index < count, or -1: no adapter, y = z. Rows may share
+ *              adapters in any order
+ * scale        [count] float32, optional (NULL: 1)
+ * out          [B][out_stride] out, in the logits' dtype, laid out like them, columns
+ *              from V on left as they are. It may be the logits' own buffer (same
+ *              address and stride), where rows without an adapter are not touched; any
+ *              other overlap is not allowed
+ * row_status   [B] int32 out: QS_ROW_OK, or QS_ROW_BAD_PARAM for another index (y = z)
+ * workspace    qs_adapters_workspace_bytes(B, rank) bytes of device scratch, 256-byte
+ *              aligned, as for qs_filter_mask
+ * Sums are held in float32; each logit is rounded once. A row's result depends on its
+ * own hidden state, logits and adapter alone. The same call gives the same bits. Made
+ * for the 1 to 64 rows of a decode step. Two kernel launches on `stream`; nothing is
+ * allocated. */
+QS_API size_t qs_adapters_workspace_bytes(int64_t B, int64_t rank);
+QS_API int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V,
+                      int64_t row_stride, const void* hidden, int64_t K,
+                      int64_t hidden_stride, const void* down, int64_t down_stride,
+                      int64_t down_row_stride, const void* up, int64_t up_stride,
+                      int64_t up_row_stride, int64_t count, int64_t rank,
+                      const int32_t* index, const float* scale, void* out,
+                      int64_t out_stride, int32_t* row_status, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* Library version string (static storage). */
 QS_API const char* qs_version(void);
 

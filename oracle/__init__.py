@@ -21,6 +21,8 @@ Modules:
   and an additive logit bias list per row.
 * ``scoring``  — log-probabilities of given tokens with entropy and top tokens,
   their gradient, and the output head with 4-bit weights.
+* ``distill``  — distillation from a teacher's top tokens, its gradient, and
+  low-rank adapters beside the output projection.
 * ``batch``    — row loops over a whole [B, V] batch with the exact input layout
   the C-ABI uses (fp32 or bf16 bit patterns, packed uint32 bitmask).
 """
@@ -38,3 +40,4 @@ from .spec import spec_verify_row, spec_verify_batch  # noqa: F401
 from .penalties import (apply_penalties_row, apply_penalties_batch,  # noqa: F401
                         apply_logit_bias_row, apply_logit_bias_batch)
 from .scoring import score_row, grad_row, head_weights  # noqa: F401
+from .distill import distill_row, distill_grad_row, adapted_row  # noqa: F401

@@ -17,14 +17,21 @@ from ._lib import (  # noqa: F401
 
 __version__ = "0.1.0"
 
-_SCORING = ("token_logprobs", "token_logprobs_backward", "token_logprobs_workspace_for",
-            "head_logits", "sample_hidden")
+# calls of modules that import torch
+_LATER = {name: module for module, names in {
+    "_scoring": ("token_logprobs", "token_logprobs_backward", "token_logprobs_workspace_for",
+                 "head_logits", "sample_hidden"),
+    "_distill": ("distill_loss", "distill_loss_backward", "distill_loss_workspace_for"),
+    "_adapters": ("apply_adapters", "adapters_workspace_for"),
+}.items() for name in names}
 
 
 def __getattr__(name):
-    """The scoring calls, from a module that imports torch: loaded on first use."""
-    if name not in _SCORING:
+    """The calls of modules that import torch: loaded on first use."""
+    module = _LATER.get(name)
+    if module is None:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import _scoring
-    globals().update({n: getattr(_scoring, n) for n in _SCORING})
+    import importlib
+    loaded = importlib.import_module("." + module, __name__)
+    globals().update({n: getattr(loaded, n) for n, m in _LATER.items() if m == module})
     return globals()[name]

@@ -44,7 +44,9 @@ EXPORTS = ("qs_workspace_bytes", "qs_filter_mask", "qs_sample", "qs_sample_noall
            "qs_spec_verify",
            "qs_apply_penalties", "qs_apply_logit_bias", "qs_top_logprobs",
            "qs_token_logprobs_workspace_bytes", "qs_token_logprobs", "qs_token_logprobs_backward",
-           "qs_head_logits", "qs_version")
+           "qs_head_logits", "qs_distill_loss_workspace_bytes", "qs_distill_loss",
+           "qs_distill_loss_backward", "qs_adapters_workspace_bytes", "qs_apply_adapters",
+           "qs_version")
 
 _lib = None
 
@@ -146,6 +148,32 @@ def load(path=LIB_PATH):
         _p, _i64, _i64,                      # codes, V, codes_stride
         _p, _i32, _i64, _p, _i64, _i64,      # scales, dtype, stride, zeros, stride, group
         _p, _i32, _i64, _p]                  # logits, logits_dtype, row_stride, stream
+    lib.qs_distill_loss_workspace_bytes.restype = _sz
+    lib.qs_distill_loss_workspace_bytes.argtypes = [_i64, _i64, _i32]  # B, V, dtype
+    lib.qs_distill_loss.restype = _i32
+    lib.qs_distill_loss.argtypes = [
+        _p, _i32, _i64, _i64, _i64,          # logits, dtype, B, V, row_stride
+        _p, _p, _i64,                        # temperature, bitmask, bitmask_stride
+        _p, _p, _i64, _i32,                  # teacher ids, values, K, rest
+        _p, _p, _p,                          # loss, row_state, row_status
+        _p, _sz, _p]                         # workspace, workspace_bytes, stream
+    lib.qs_distill_loss_backward.restype = _i32
+    lib.qs_distill_loss_backward.argtypes = [
+        _p, _i32, _i64, _i64, _i64,          # logits, dtype, B, V, row_stride
+        _p, _p, _i64,                        # temperature, bitmask, bitmask_stride
+        _p, _p, _i64, _i32,                  # teacher ids, values, K, rest
+        _p, _p, _p,                          # row_state, row_status, grad_loss
+        _p, _i64, _p]                        # grad_logits, grad_stride, stream
+    lib.qs_adapters_workspace_bytes.restype = _sz
+    lib.qs_adapters_workspace_bytes.argtypes = [_i64, _i64]  # B, rank
+    lib.qs_apply_adapters.restype = _i32
+    lib.qs_apply_adapters.argtypes = [
+        _p, _i32, _i64, _i64, _i64,          # logits, dtype, B, V, row_stride
+        _p, _i64, _i64,                      # hidden, K, hidden_stride
+        _p, _i64, _i64, _p, _i64, _i64,      # down, up: address, adapter and row stride
+        _i64, _i64, _p, _p,                  # count, rank, index, scale
+        _p, _i64, _p,                        # out, out_stride, row_status
+        _p, _sz, _p]                         # workspace, workspace_bytes, stream
     lib.qs_version.restype = ctypes.c_char_p
     lib.qs_version.argtypes = []
     if path == LIB_PATH:

@@ -303,11 +303,21 @@ def head_logits(hidden, codes, scales, zeros=None, *, dtype=None, out=None):
 
 
 def sample_hidden(hidden, codes, scales, zeros, temperature, top_k, top_p, bitmask=None, *,
-                  dtype=None, logits=None, **options):
+                  dtype=None, logits=None, adapters=None, **options):
     """sample() from hidden states: head_logits into `logits` (a buffer [B, V];
     made per call when omitted), then the selection, on the current stream.
-    options: sample()'s keyword arguments. The result holds the logits too."""
+    adapters: low-rank adapters of the rows between the two, a dict of
+    apply_adapters' down, up, index and (optional) scale and workspace; bfloat16
+    logits are then rounded once by the head and once with the adapters, float32
+    ones (dtype) hardly at all. options: sample()'s keyword arguments. The result
+    holds the logits too, and with adapters adapter_status."""
     z = head_logits(hidden, codes, scales, zeros, dtype=dtype, out=logits)
+    moved = None
+    if adapters is not None:
+        from ._adapters import apply_adapters
+        moved = apply_adapters(z, hidden, **adapters)
     out = sample(z, temperature, top_k, top_p, bitmask, **options)
     out["logits"] = z
+    if moved is not None:
+        out["adapter_status"] = moved
     return out

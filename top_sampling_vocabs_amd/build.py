@@ -22,7 +22,8 @@ SOURCES = ["qs_filter_bf16.hip", "qs_filter_f32.hip", "qs_filter_bf16_proc.hip",
            "qs_filter_f32_topn.hip", "qs_chunk.hip", "qs_api.hip",
            "qs_spec.hip", "qs_penalty.hip", "qs_toplp.hip",
            "qs_score.hip", "qs_score_grad.hip", "qs_head_g32.hip",
-           "qs_head_g64.hip", "qs_head_g128.hip"]
+           "qs_head_g64.hip", "qs_head_g128.hip", "qs_distill.hip", "qs_distill_grad.hip",
+           "qs_adapters.hip"]
 ARCH = os.environ.get("QS_OFFLOAD_ARCH", "gfx950")
 
 COMPILE_FLAGS = [

@@ -11,8 +11,10 @@
 
 #include "../../include/qs.h"
 
+#include "qs_adapters.hpp"
 #include "qs_aux.hpp"
 #include "qs_chunk.hpp"
+#include "qs_distill.hpp"
 #include "qs_head.hpp"
 #include "qs_launch.hpp"
 #include "qs_proc.hpp"
@@ -613,6 +615,155 @@ int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidden_stri
   a.logits_dtype = logits_dtype;
   a.row_stride = row_stride;
   hipError_t e = qs::head::launch_head(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QS_OK : QS_ERR_HIP;
+}
+
+size_t qs_distill_loss_workspace_bytes(int64_t B, int64_t V, int dtype) {
+  if (B < 1 || B > kMaxB || V < 1 || V > kMaxV || (dtype != QS_F32 && dtype != QS_BF16)) return 0;
+  return qs::distill::workspace_bytes(B, V, dtype);
+}
+
+int qs_distill_loss(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                    const float* temperature, const uint32_t* bitmask, int64_t bitmask_stride,
+                    const int32_t* teacher_ids, const float* teacher_values, int64_t K, int rest,
+                    float* loss, float* row_state, int32_t* row_status, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int rc = check_input(logits, dtype, B, V, row_stride, bitmask, bitmask_stride);
+  if (rc != QS_OK) return rc;
+  if (B == 0) return QS_OK;
+  if (K < 1 || K > qs::distill::kSlotsMax || (rest != 0 && rest != 1)) return QS_ERR_INVALID_ARG;
+  const void* req4[] = {teacher_ids, teacher_values, loss, row_state, row_status};
+  for (const void* p : req4)
+    if (!p || !aligned(p, 4)) return QS_ERR_INVALID_ARG;
+  if (!aligned(temperature, 4)) return QS_ERR_INVALID_ARG;
+  if (!qs::distill::grid_fits(B, V, dtype)) return QS_ERR_INVALID_ARG;
+  const size_t need = qs::distill::workspace_bytes(B, V, dtype);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+    return QS_ERR_WORKSPACE;
+  qs::distill::Args a;
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.row_bytes = row_stride * (dtype == QS_F32 ? 4 : 2);
+  a.V = (int)V;
+  a.T = temperature;
+  a.bitmask = bitmask;
+  a.bm_stride = bitmask_stride;
+  a.ids = teacher_ids;
+  a.values = teacher_values;
+  a.K = (int)K;
+  a.rest = rest;
+  a.loss = loss;
+  a.state = row_state;
+  a.status = row_status;
+  hipError_t e =
+      qs::distill::launch_loss(a, dtype, (int)B, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QS_OK : QS_ERR_HIP;
+}
+
+int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, int64_t V,
+                             int64_t row_stride, const float* temperature,
+                             const uint32_t* bitmask, int64_t bitmask_stride,
+                             const int32_t* teacher_ids, const float* teacher_values, int64_t K,
+                             int rest, const float* row_state, const int32_t* row_status,
+                             const float* grad_loss, void* grad_logits, int64_t grad_stride,
+                             void* stream) {
+  int rc = check_input(logits, dtype, B, V, row_stride, bitmask, bitmask_stride);
+  if (rc != QS_OK) return rc;
+  if (B == 0) return QS_OK;
+  if (K < 1 || K > qs::distill::kSlotsMax || (rest != 0 && rest != 1)) return QS_ERR_INVALID_ARG;
+  const void* req4[] = {teacher_ids, teacher_values, row_state, row_status, grad_loss};
+  for (const void* p : req4)
+    if (!p || !aligned(p, 4)) return QS_ERR_INVALID_ARG;
+  if (!aligned(temperature, 4)) return QS_ERR_INVALID_ARG;
+  const int64_t es = dtype == QS_F32 ? 4 : 2;
+  if (!grad_logits || !aligned(grad_logits, 16) || grad_stride < V || (grad_stride * es) % 16 != 0)
+    return QS_ERR_INVALID_ARG;
+  if (!qs::distill::grad_grid_fits(B, V, dtype)) return QS_ERR_INVALID_ARG;
+  // in place only row for row: otherwise one row's writes meet another's reads
+  if (grad_logits == logits && grad_stride != row_stride) return QS_ERR_INVALID_ARG;
+  qs::distill::GradArgs a;
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.row_bytes = row_stride * es;
+  a.V = (int)V;
+  a.T = temperature;
+  a.bitmask = bitmask;
+  a.bm_stride = bitmask_stride;
+  a.ids = teacher_ids;
+  a.values = teacher_values;
+  a.K = (int)K;
+  a.rest = rest;
+  a.state = row_state;
+  a.status = row_status;
+  a.g_loss = grad_loss;
+  a.grad = static_cast<uint8_t*>(grad_logits);
+  a.grad_bytes = grad_stride * es;
+  hipError_t e = qs::distill::launch_grad(a, dtype, (int)B, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QS_OK : QS_ERR_HIP;
+}
+
+size_t qs_adapters_workspace_bytes(int64_t B, int64_t rank) {
+  if (B < 1 || B > qs::adapters::kMaxB || rank < 8 || rank > qs::adapters::kMaxRank || rank % 8 != 0)
+    return 0;
+  return qs::adapters::workspace_bytes(B, rank);
+}
+
+int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                      const void* hidden, int64_t K, int64_t hidden_stride, const void* down,
+                      int64_t down_stride, int64_t down_row_stride, const void* up,
+                      int64_t up_stride, int64_t up_row_stride, int64_t count, int64_t rank,
+                      const int32_t* index, const float* scale, void* out, int64_t out_stride,
+                      int32_t* row_status, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  namespace ad = qs::adapters;
+  int rc = check_input(logits, dtype, B, V, row_stride, nullptr, 0);
+  if (rc != QS_OK) return rc;
+  if (B > ad::kMaxB || V > ad::kMaxV || K < 8 || K > ad::kMaxK || K % 8 != 0)
+    return QS_ERR_INVALID_ARG;
+  if (rank < 8 || rank > ad::kMaxRank || rank % 8 != 0 || count < 0 || count >= (int64_t)1 << 31)
+    return QS_ERR_INVALID_ARG;
+  if (B == 0) return QS_OK;
+  if (!hidden || !aligned(hidden, 16) || hidden_stride < K || hidden_stride % 8 != 0)
+    return QS_ERR_INVALID_ARG;
+  if (count > 0) {
+    if (!down || !aligned(down, 16) || down_row_stride < K || down_row_stride % 8 != 0 ||
+        down_stride < 0 || down_stride % 8 != 0)
+      return QS_ERR_INVALID_ARG;
+    if (!up || !aligned(up, 16) || up_row_stride < rank || up_row_stride % 8 != 0 ||
+        up_stride < 0 || up_stride % 8 != 0)
+      return QS_ERR_INVALID_ARG;
+  }
+  if (!index || !aligned(index, 4) || !aligned(scale, 4) || !row_status || !aligned(row_status, 4))
+    return QS_ERR_INVALID_ARG;
+  const int64_t es = dtype == QS_F32 ? 4 : 2;
+  if (!out || !aligned(out, 16) || out_stride < V || (out_stride * es) % 16 != 0)
+    return QS_ERR_INVALID_ARG;
+  // in place only row for row: otherwise one row's writes meet another's reads
+  if (out == logits && out_stride != row_stride) return QS_ERR_INVALID_ARG;
+  if (!ad::grid_fits(B, V, rank)) return QS_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < ad::workspace_bytes(B, rank))
+    return QS_ERR_WORKSPACE;
+  ad::Args a;
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.row_bytes = row_stride * es;
+  a.out = static_cast<uint8_t*>(out);
+  a.out_bytes = out_stride * es;
+  a.B = (int)B;
+  a.V = (int)V;
+  a.K = (int)K;
+  a.rank = (int)rank;
+  a.count = count;
+  a.hidden = static_cast<const uint16_t*>(hidden);
+  a.hidden_stride = hidden_stride;
+  a.down = static_cast<const uint16_t*>(down);
+  a.down_stride = down_stride;
+  a.down_row_stride = down_row_stride;
+  a.up = static_cast<const uint16_t*>(up);
+  a.up_stride = up_stride;
+  a.up_row_stride = up_row_stride;
+  a.index = index;
+  a.scale = scale;
+  a.status = row_status;
+  a.low = static_cast<float*>(workspace);
+  hipError_t e = ad::launch_adapters(a, dtype, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QS_OK : QS_ERR_HIP;
 }
 
