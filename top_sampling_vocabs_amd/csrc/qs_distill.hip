@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/qs.h"
 #include "qs_device.hpp"
 #include "qs_distill.hpp"
@@ -28,11 +30,17 @@ namespace {
 
 using namespace score;
 
-constexpr int kRowBlock = 1024;  // threads of a row's workgroup
-constexpr int kRowLoads = 8;     // 16-byte loads per lane at a time
+constexpr int kPartBlock = 256;   // threads of a part's workgroup
+constexpr int kPartLoads = 16;    // 16-byte loads per lane
+constexpr int kShortLoads = 8;    // the same where parts are few
+constexpr int kRowBlock = 1024;   // threads of a whole row's workgroup
+constexpr int kRowLoads = 8;
+constexpr int kSmallBlock = 256;  // threads of a short row's workgroup
+constexpr int kSmallLoads = 4;
+constexpr int kJoinSlots = 4;     // slots per thread of the join
 constexpr float kLowest = -3.402823466e38f;
 
-// What a pass over (a part of) a row leaves.
+// What a part's workgroup leaves for the join.
 struct Part {
   float m;        // largest legal token outside the list (kLowest: none is finite)
   float S;        // sum of 2^((z - m) c) over them; NaN if one is NaN or +inf
@@ -41,68 +49,104 @@ struct Part {
 };
 static_assert(sizeof(Part) == 16, "one 16-byte store");
 
+// Loads per lane of a part: the long parts' workgroups are more than kFewParts
+// (eight per compute unit), or else the row is cut into twice as many.
+constexpr int64_t kFewParts = 2048;
+int64_t parts_of(int64_t V, int dtype, int loads) {
+  const int64_t n = (int64_t)(dtype == QS_F32 ? 4 : 8) * kPartBlock * loads;
+  return (V + n - 1) / n;
+}
+int loads_for(int64_t B, int64_t V, int dtype) {
+  return B * parts_of(V, dtype, kPartLoads) > kFewParts ? kPartLoads : kShortLoads;
+}
+int64_t parts_for(int64_t B, int64_t V, int dtype) {
+  if (V <= (int64_t)(dtype == QS_F32 ? 4 : 8) * kRowBlock * kRowLoads) return 1;
+  return parts_of(V, dtype, loads_for(B, V, dtype));
+}
+
+constexpr uint32_t kBadSlot = 1u, kNonfinite = 2u;
+
+// A thread's slots j = i * THREADS + tid: the teacher's value and the student's logit
+// of those that name a legal token.
+template <int DT, int THREADS, int N>
+struct Slots {
+  int id[N];
+  float z[N], t[N];
+  uint32_t live, flags;
+
+  __device__ __forceinline__ void load_ids(const Args& a, int r, int tid) {
+    flags = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int j = i * THREADS + tid;
+      id[i] = -1;
+      if (j < a.K) id[i] = a.ids[(size_t)r * a.K + j];
+      if (id[i] < -1 || id[i] >= a.V) {
+        flags = kBadSlot;
+        id[i] = -1;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const Args& a, int r, int tid) {
+    const uint8_t* const row = a.logits + (size_t)r * a.row_bytes;
+    const uint32_t* const mask = a.bitmask ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
+    live = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      z[i] = t[i] = -INFINITY;
+      if (id[i] < 0) continue;
+      t[i] = a.values[(size_t)r * a.K + i * THREADS + tid];
+      z[i] = logit_at<DT>(row, id[i]);
+      if (!mask || ((mask[id[i] >> 5] >> (id[i] & 31)) & 1u)) live |= 1u << i;
+    }
+  }
+};
+
 struct FinishShared {
   float zmax[kRowBlock / 64], tmax[kRowBlock / 64];
   uint32_t flags[kRowBlock / 64];
   double sum[5][kRowBlock / 64];
 };
 
-constexpr uint32_t kBadSlot = 1u, kNonfinite = 2u;
-
 // Writes one row's outputs from the rest's statistics; called by every thread of a
-// workgroup of THREADS, at most kSlotsMax slots.
-template <int DT, int THREADS>
-__device__ __forceinline__ void finish_row(const Args& a, int r, int tid, const Part& rest,
-                                           FinishShared& s) {
+// workgroup of THREADS with its slots.
+template <int DT, int THREADS, int N>
+__device__ __forceinline__ void finish_row(const Args& a, int r, int tid,
+                                           Slots<DT, THREADS, N> s, const Part& rest,
+                                           FinishShared& sh) {
   constexpr int kWavesHere = THREADS / 64;
-  constexpr int kSlots = (kSlotsMax + THREADS - 1) / THREADS;
   const int lane = lane_id(), w = tid >> 6;
   const float Tf = a.T ? a.T[r] : 1.0f;
   const bool bad_T = !(Tf > 0.0f) || Tf == INFINITY;
   const double T = Tf;
-  const uint8_t* const row = a.logits + (size_t)r * a.row_bytes;
-  const uint32_t* const mask = a.bitmask ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
   const float most = a.rest ? 1.0f : 3.402823466e38f;
 
-  float z[kSlots], t[kSlots];
-  bool live[kSlots];
   float zmax = -INFINITY, tmax = -INFINITY;
-  uint32_t flags = 0u;
+  uint32_t flags = s.flags;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const int j = i * THREADS + tid;
-    live[i] = false;
-    z[i] = t[i] = -INFINITY;
-    if (j < a.K) {
-      const int id = a.ids[(size_t)r * a.K + j];
-      if (id < -1 || id >= a.V) flags |= kBadSlot;
-      else if (id >= 0 && (!mask || ((mask[id >> 5] >> (id & 31)) & 1u))) {
-        live[i] = true;
-        t[i] = a.values[(size_t)r * a.K + j];
-        z[i] = logit_at<DT>(row, id);
-        if (!(t[i] <= most)) flags |= kBadSlot;
-        if (!(z[i] < INFINITY)) flags |= kNonfinite;
-        zmax = fmaxf(zmax, z[i]);
-        tmax = fmaxf(tmax, t[i]);
-      }
-    }
+  for (int i = 0; i < N; ++i) {
+    if (!((s.live >> i) & 1u)) continue;
+    if (!(s.t[i] <= most)) flags |= kBadSlot;
+    if (!(s.z[i] < INFINITY)) flags |= kNonfinite;
+    zmax = fmaxf(zmax, s.z[i]);
+    tmax = fmaxf(tmax, s.t[i]);
   }
   zmax = wave_max_f32(zmax);
   tmax = wave_max_f32(tmax);
   flags = (ballot(flags & kBadSlot) ? kBadSlot : 0u) | (ballot(flags & kNonfinite) ? kNonfinite : 0u);
   if constexpr (kWavesHere > 1) {
     if (lane == 0) {
-      s.zmax[w] = zmax;
-      s.tmax[w] = tmax;
-      s.flags[w] = flags;
+      sh.zmax[w] = zmax;
+      sh.tmax[w] = tmax;
+      sh.flags[w] = flags;
     }
     __syncthreads();
-    zmax = s.zmax[0], tmax = s.tmax[0], flags = s.flags[0];
+    zmax = sh.zmax[0], tmax = sh.tmax[0], flags = sh.flags[0];
 #pragma unroll
     for (int k = 1; k < kWavesHere; ++k) {
-      zmax = fmaxf(zmax, s.zmax[k]);
-      tmax = fmaxf(tmax, s.tmax[k]);
-      flags |= s.flags[k];
+      zmax = fmaxf(zmax, sh.zmax[k]);
+      tmax = fmaxf(tmax, sh.tmax[k]);
+      flags |= sh.flags[k];
     }
   }
   const bool has = rest.S != 0.0f;  // the rest has a finite token (or is NaN)
@@ -128,28 +172,30 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, const 
   // for the two normalisers
   double sum[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    if (!live[i]) continue;
-    const double d = ((double)z[i] - (double)m) / T;
-    const double tau = a.rest ? (double)t[i] : ((double)t[i] - (double)tmax) / T;
+  for (int i = 0; i < N; ++i) {
+    if (!((s.live >> i) & 1u)) continue;
+    const double d = ((double)s.z[i] - (double)m) / T;
+    const double tau = a.rest ? (double)s.t[i] : ((double)s.t[i] - (double)tmax) / T;
     const double wt = exp(tau);
-    if (z[i] == m) sum[1] += 1.0;
+    if (s.z[i] == m) sum[1] += 1.0;
     else sum[0] += exp(d);
-    if (!a.rest && t[i] == tmax) sum[3] += 1.0;
+    if (!a.rest && s.t[i] == tmax) sum[3] += 1.0;
     else sum[2] += wt;
     if (wt > 0.0) sum[4] += wt * (tau - d);
   }
 #pragma unroll
   for (int k = 0; k < 5; ++k) sum[k] = wave_sum_f64(sum[k]);
   if constexpr (kWavesHere > 1) {
-    if (lane < 5) s.sum[lane][w] = lane == 0 ? sum[0] : lane == 1 ? sum[1] : lane == 2 ? sum[2]
-                                   : lane == 3 ? sum[3] : sum[4];
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < 5; ++k) sh.sum[k][w] = sum[k];
+    }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
-      sum[k] = s.sum[k][0];
+      sum[k] = sh.sum[k][0];
 #pragma unroll
-      for (int v = 1; v < kWavesHere; ++v) sum[k] += s.sum[k][v];
+      for (int v = 1; v < kWavesHere; ++v) sum[k] += sh.sum[k][v];
     }
   }
   if (tid != 0) return;
@@ -191,99 +237,218 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid, const 
   state[7] = (float)(mass - 1.0);
 }
 
-// One workgroup per row, which walks it.
-template <int DT, bool MASK>
-__global__ void __launch_bounds__(kRowBlock) distill_row_kernel(Args a) {
-  constexpr int P = kPer<DT>, kSpan = kRowBlock * kRowLoads * P;
+// One workgroup per row (ROW: parts == 1, outputs written here) or per part.
+template <int DT, int THREADS, int NL, bool MASK, bool ROW>
+__global__ void __launch_bounds__(THREADS)
+    distill_kernel(Args a, int parts, int part_loads, Part* ws_parts) {
+  constexpr int kWavesHere = THREADS / 64;
+  constexpr int P = kPer<DT>, kSpan = THREADS * NL * P;
+  constexpr bool kTable = MASK && DT == QS_BF16;
+  constexpr int N = (kSlotsMax + THREADS - 1) / THREADS;
   __shared__ uint32_t s_named[kSpan / 32];
+  __shared__ uint4 s_masks[kTable ? 256 : 1];  // masks_of every byte of legal bits
   __shared__ FinishShared s_fin;
-  __shared__ float s_m[kRowBlock / 64], s_S[kRowBlock / 64];
+  __shared__ float s_m[kWavesHere], s_S[kWavesHere];
   const int tid = threadIdx.x, lane = lane_id(), w = tid >> 6;
-  const int r = blockIdx.x;
+  const int r = ROW ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)parts);
+  const int part = ROW ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)parts);
+  const int span = part_loads * THREADS * P;
+  const int begin = part * span;  // first token of this workgroup
   const uint8_t* const row = a.logits + (size_t)r * a.row_bytes;
   const uint8_t* const mask_row =
       reinterpret_cast<const uint8_t*>(a.bitmask + (size_t)r * a.bm_stride);
   const float c = scale_of(a.T ? a.T[r] : 1.0f);
-  float m = kLowest, S = 0.0f;
-  uint32_t any = 0u, dup = 0u;
-  for (int64_t begin64 = 0; begin64 < a.V; begin64 += kSpan) {
-    const int begin = (int)begin64;
-    __syncthreads();  // the bitmap of the span before has been read
-    for (int i = tid; i < kSpan / 32; i += kRowBlock) s_named[i] = 0u;
-    __syncthreads();
-    for (int j = tid; j < a.K; j += kRowBlock) {
-      const int id = a.ids[(size_t)r * a.K + j], d = id - begin;
-      if (id >= begin && id < a.V && d < kSpan) {
-        const uint32_t bit = 1u << (d & 31);
-        dup |= atomicOr(&s_named[d >> 5], bit) & bit;
-      }
+
+  // requests: the slots, then 16 bytes per lane and load; loads that begin past the
+  // row's end are left out (a 16-byte chunk that begins inside the row ends inside
+  // its stride)
+  Slots<DT, THREADS, N> slots;
+  slots.load_ids(a, r, tid);
+  uint4 v[NL];
+  uint32_t legal[NL];
+#pragma unroll
+  for (int u = 0; u < NL; ++u) {
+    const int i = begin + (u * THREADS + tid) * P;
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    legal[u] = 0u;
+    if (u < part_loads && i < a.V) {
+      v[u] = *reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P));
+      legal[u] = 0xFFu;
+      if constexpr (MASK) legal[u] = mask_row[i >> 3];
     }
-    __syncthreads();
-    uint4 v[kRowLoads];
-    float top = m;
-#pragma unroll
-    for (int u = 0; u < kRowLoads; ++u) {
-      const int d = (u * kRowBlock + tid) * P;
-      uint32_t bits = 0u;
-      v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (d < a.V - begin) {
-        const int i = begin + d;
-        bits = 0xFFu;
-        if constexpr (MASK) bits = mask_row[i >> 3];
-        uint32_t named = reinterpret_cast<const uint8_t*>(s_named)[d >> 3];
-        if constexpr (P == 4) {
-          if (MASK) bits >>= i & 4;
-          named >>= d & 4;
-        }
-        const int left = a.V - i;
-        bits &= left >= P ? (1u << P) - 1u : (1u << left) - 1u;
-        any |= bits;
-        bits &= ~named;
-        v[u] = *reinterpret_cast<const uint4*>(row + (size_t)i * (16 / P));
-      }
-      v[u] = blank<DT>(v[u], masks_of<DT>(bits));
-#pragma unroll
-      for (int e = 0; e < P; ++e) top = fmaxf(top, token<DT>(v[u], e));
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kRowLoads; ++u) {
-#pragma unroll
-      for (int e = 0; e < P; ++e) sum += exp2_hw((token<DT>(v[u], e) - top) * c);
-    }
-    S = fmaf(S, exp2_hw((m - top) * c), sum);
-    m = top;
   }
-  const float wm = wave_max_f32(m);
-  S = wave_sum_f32(S * exp2_hw((m - wm) * c));
-  if (lane == 0) s_m[w] = wm, s_S[w] = S;
+  // which tokens of this workgroup are named
+  for (int i = tid; i < kSpan / 32; i += THREADS) s_named[i] = 0u;
+  if constexpr (kTable) {
+    for (int k = tid; k < 256; k += THREADS) s_masks[k] = masks_of<DT>((uint32_t)k);
+  }
+  __syncthreads();
+  uint32_t dup = 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int d = slots.id[i] - begin;
+    if (slots.id[i] >= begin && d < span) {
+      const uint32_t bit = 1u << (d & 31);
+      dup |= atomicOr(&s_named[d >> 5], bit) & bit;
+    }
+  }
+  if constexpr (ROW) slots.load(a, r, tid);
+  __syncthreads();
+
+  // largest legal token of the lane that is not named; the others become -inf
+  Largest<DT> largest;
+  uint32_t any = 0u;
+#pragma unroll
+  for (int u = 0; u < NL; ++u) {
+    const int d = (u * THREADS + tid) * P, left = a.V - begin - d;
+    uint32_t bits = legal[u], named = reinterpret_cast<const uint8_t*>(s_named)[d >> 3];
+    if constexpr (P == 4) {
+      if (MASK) bits >>= d & 4;
+      named >>= d & 4;
+    }
+    bits &= left >= P ? (1u << P) - 1u : left > 0 ? (1u << left) - 1u : 0u;
+    any |= bits;
+    bits &= ~named;
+    if constexpr (kTable) v[u] = blank<DT>(v[u], s_masks[bits]);
+    else if (MASK || bits != (1u << P) - 1u) v[u] = blank<DT>(v[u], masks_of<DT>(bits));
+    largest.add(v[u]);
+  }
+  const float wave_max = wave_max_f32(fmaxf(largest.value(), kLowest));
+
+  // the wave's sum against its own maximum: with 2^(z c - k), k = fl(m_w c), from one
+  // multiply-add it is off by the factor 2^(m_w c - k) alone; past |k| = 2^24 the
+  // difference comes first
+  float S[2] = {0.0f, 0.0f};
+  const float k = wave_max * c;
+  if (fabsf(k) < kFused && c < 1e30f) {
+#pragma unroll
+    for (int u = 0; u < NL; ++u) {
+      opaque(v[u]);
+#pragma unroll
+      for (int e = 0; e < P; ++e) S[e & 1] += exp2_hw(fmaf(token<DT>(v[u], e), c, -k));
+    }
+    const float f = exp2_hw(-fmaf(wave_max, c, -k));
+    S[0] *= f;
+    S[1] *= f;
+  } else {
+#pragma unroll
+    for (int u = 0; u < NL; ++u) {
+      opaque(v[u]);
+#pragma unroll
+      for (int e = 0; e < P; ++e) S[e & 1] += exp2_hw((token<DT>(v[u], e) - wave_max) * c);
+    }
+  }
+  const float Sw = wave_sum_f32(S[0] + S[1]);
+  if (lane == 0) {
+    s_m[w] = wave_max;
+    s_S[w] = Sw;
+  }
   any = __syncthreads_or(any != 0u);
   dup = __syncthreads_or(dup != 0u);
   Part p{s_m[0], 0.0f, any, dup};
 #pragma unroll
-  for (int k = 1; k < kRowBlock / 64; ++k) p.m = fmaxf(p.m, s_m[k]);
+  for (int q = 1; q < kWavesHere; ++q) p.m = fmaxf(p.m, s_m[q]);
 #pragma unroll
-  for (int k = 0; k < kRowBlock / 64; ++k) p.S += s_S[k] * exp2_hw((s_m[k] - p.m) * c);
-  finish_row<DT, kRowBlock>(a, r, tid, p, s_fin);
+  for (int q = 0; q < kWavesHere; ++q) p.S += s_S[q] * exp2_hw(rel(s_m[q], p.m, c));
+  if constexpr (ROW) {
+    finish_row<DT, THREADS, N>(a, r, tid, slots, p, s_fin);
+  } else {
+    if (tid == 0) ws_parts[(size_t)r * parts + part] = p;
+  }
+}
+
+// Joins the parts of each row: one workgroup per row.
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    distill_join_kernel(Args a, int parts, const Part* ws_parts) {
+  __shared__ FinishShared s_fin;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = lane_id();
+  const Part* const p = ws_parts + (size_t)r * parts;
+  Slots<DT, THREADS, kJoinSlots> slots;
+  slots.load_ids(a, r, tid);
+  Part mine{kLowest, 0.0f, 0u, 0u};
+  if (lane < parts) mine = p[lane];
+  slots.load(a, r, tid);
+  const float c = scale_of(a.T ? a.T[r] : 1.0f);
+  // every wave joins all parts (the same values in every thread)
+  float m = mine.m;
+  uint32_t any = mine.any, dup = mine.dup;
+  for (int k = lane + 64; k < parts; k += 64) {
+    m = fmaxf(m, p[k].m);
+    any |= p[k].any;
+    dup |= p[k].dup;
+  }
+  m = wave_max_f32(m);
+  float S = mine.S * exp2_hw(rel(mine.m, m, c));
+  for (int k = lane + 64; k < parts; k += 64) S += p[k].S * exp2_hw(rel(p[k].m, m, c));
+  const Part rest{m, wave_sum_f32(S), ballot(any != 0u) != 0, ballot(dup != 0u) != 0};
+  finish_row<DT, THREADS, kJoinSlots>(a, r, tid, slots, rest, s_fin);
+}
+
+template <int DT, int THREADS, int NL, bool ROW>
+void launch(const Args& a, int blocks, int parts, int part_loads, Part* wp, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(THREADS);
+  if (a.bitmask)
+    hipLaunchKernelGGL((distill_kernel<DT, THREADS, NL, true, ROW>), grid, block, 0, st, a, parts,
+                       part_loads, wp);
+  else
+    hipLaunchKernelGGL((distill_kernel<DT, THREADS, NL, false, ROW>), grid, block, 0, st, a, parts,
+                       part_loads, wp);
+}
+
+template <int DT>
+hipError_t launch_dt(const Args& a, int B, int parts, Part* wp, hipStream_t st) {
+  constexpr int P = kPer<DT>;
+  if (parts == 1) {
+    if (a.V <= kSmallBlock * kSmallLoads * P)
+      launch<DT, kSmallBlock, kSmallLoads, true>(
+          a, B, 1, (a.V + kSmallBlock * P - 1) / (kSmallBlock * P), nullptr, st);
+    else
+      launch<DT, kRowBlock, kRowLoads, true>(
+          a, B, 1, (a.V + kRowBlock * P - 1) / (kRowBlock * P), nullptr, st);
+    return hipGetLastError();
+  }
+  // parts of equal length, in whole loads
+  const int loads = (a.V + kPartBlock * P - 1) / (kPartBlock * P);
+  const int each = (loads + parts - 1) / parts;
+  if (loads_for(B, a.V, DT) == kPartLoads)
+    launch<DT, kPartBlock, kPartLoads, false>(a, B * parts, parts, each, wp, st);
+  else
+    launch<DT, kPartBlock, kShortLoads, false>(a, B * parts, parts, each, wp, st);
+  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  // one wave a row where its lanes hold the slots
+  if (a.K <= 64 * kJoinSlots)
+    hipLaunchKernelGGL((distill_join_kernel<DT, 64>), dim3((unsigned)B), dim3(64), 0, st, a, parts,
+                       wp);
+  else
+    hipLaunchKernelGGL((distill_join_kernel<DT, 256>), dim3((unsigned)B), dim3(256), 0, st, a,
+                       parts, wp);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t workspace_bytes(int64_t, int64_t, int) { return 0; }
-bool grid_fits(int64_t B, int64_t, int) { return B * kRowBlock < (int64_t)1 << 32; }
+// Enough for every batch of at most B rows: the largest of them whose parts are
+// short has up to twice the parts of a somewhat larger one whose parts are long.
+size_t workspace_bytes(int64_t B, int64_t V, int dtype) {
+  const int64_t parts = parts_for(B, V, dtype);
+  if (parts == 1) return 0;
+  const int64_t few = kFewParts / parts_of(V, dtype, kPartLoads);  // rows of the last such batch
+  size_t n = (size_t)B * parts;
+  if (B > few) n = std::max(n, (size_t)few * parts_of(V, dtype, kShortLoads));
+  return (n * sizeof(Part) + 255) & ~(size_t)255;
+}
 
-hipError_t launch_loss(const Args& a, int dtype, int B, void*, hipStream_t st) {
-  const dim3 grid((unsigned)B), block(kRowBlock);
-  const bool mask = a.bitmask != nullptr;
-  if (dtype == QS_F32 && mask)
-    hipLaunchKernelGGL((distill_row_kernel<QS_F32, true>), grid, block, 0, st, a);
-  else if (dtype == QS_F32)
-    hipLaunchKernelGGL((distill_row_kernel<QS_F32, false>), grid, block, 0, st, a);
-  else if (mask)
-    hipLaunchKernelGGL((distill_row_kernel<QS_BF16, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((distill_row_kernel<QS_BF16, false>), grid, block, 0, st, a);
-  return hipGetLastError();
+bool grid_fits(int64_t B, int64_t V, int dtype) {
+  const int64_t parts = parts_for(B, V, dtype);
+  return B * parts * (parts == 1 ? kRowBlock : kPartBlock) < (int64_t)1 << 32;
+}
+
+hipError_t launch_loss(const Args& a, int dtype, int B, void* workspace, hipStream_t st) {
+  const int parts = (int)parts_for(B, a.V, dtype);
+  Part* const wp = static_cast<Part*>(workspace);
+  return dtype == QS_F32 ? launch_dt<QS_F32>(a, B, parts, wp, st)
+                         : launch_dt<QS_BF16>(a, B, parts, wp, st);
 }
 
 }  // namespace distill
