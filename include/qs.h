@@ -567,7 +567,7 @@ QS_API int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidd
  *                probability that the student's logit of -inf does not. 0 on a row
  *                whose teacher names no legal token of positive probability and
  *                leaves nothing to the rest
- * row_state      [B][8] float32 out, what the gradient needs: m; ln S; the rest's
+ * row_state      [B][8] float32 out, 16-byte aligned, what the gradient needs: m; ln S; the rest's
  *                largest logit m_R and ln of the sum over R of exp((z - m_R) / T);
  *                Q p_R - q_R, with Q = sum q_j + q_R; the teacher's largest value and
  *                the ln of its sum relative to it (rest = 1: 0, 0); Q - 1. The third

@@ -24,7 +24,7 @@ def loss(lib, **kw):  # noqa: F811
     dict(T=ODD), dict(bm=A16, bms=1), dict(bm=ODD, bms=2), dict(ids=None), dict(ids=ODD),
     dict(values=None), dict(values=ODD), dict(K=0), dict(K=-1), dict(K=1025), dict(rest=2),
     dict(rest=-1), dict(loss=None), dict(loss=ODD), dict(state=None), dict(state=ODD),
-    dict(status=None), dict(status=ODD),
+    dict(state=ctypes.c_void_p(0x100008)), dict(status=None), dict(status=ODD),
 ])
 def test_distill_loss_rejects_bad_arguments(lib, kw):  # noqa: F811
     assert loss(lib, **kw) == _lib.QS_ERR_INVALID_ARG
@@ -58,7 +58,7 @@ def test_distill_loss_workspace_serves_smaller_batches(lib, V, dtype):  # noqa: 
 @pytest.mark.parametrize("kw", [
     dict(logits=None), dict(dtype=3), dict(B=-1), dict(V=0), dict(stride=65), dict(ids=None),
     dict(ids=ODD), dict(values=None), dict(K=0), dict(K=1025), dict(rest=2), dict(state=None),
-    dict(state=ODD), dict(status=None), dict(g=None), dict(g=ODD), dict(grad=None),
+    dict(state=ODD), dict(state=ctypes.c_void_p(0x100008)), dict(status=None), dict(g=None), dict(g=ODD), dict(grad=None),
     dict(grad=ODD), dict(gs=60), dict(gs=65), dict(T=ODD), dict(bm=A16, bms=1),
     dict(grad=A16, gs=128),
 ])

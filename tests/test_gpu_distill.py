@@ -552,6 +552,31 @@ def test_autograd(qs):
             loss.sum().backward()
 
 
+def test_autograd_outputs_in_place(qs):
+    """The losses may be changed in place (a masked or weighted sum does so); the state,
+    which the gradient reads, may not: torch reports it."""
+    import torch
+    z = torch.randn(4, 512, device="cuda")
+    ids = torch.tensor([[1, 500, -1, 3]] * 4, dtype=torch.int32, device="cuda")
+    val = torch.rand(4, 4, device="cuda").log()
+    w = torch.tensor([1.0, 0.0, 2.0, -1.0], device="cuda")
+    grads = []
+    for in_place in (False, True):
+        lg = z.clone().requires_grad_()
+        loss = qs.distill_loss(lg, ids, val)["loss"]
+        if in_place:
+            loss *= w
+        else:
+            loss = loss * w
+        loss.sum().backward()
+        grads.append(lg.grad)
+    assert torch.equal(*grads) and bool(grads[0].any())
+    with pytest.raises(RuntimeError):
+        out = qs.distill_loss(z.clone().requires_grad_(), ids, val)
+        out["state"].mul_(2.0)
+        out["loss"].sum().backward()
+
+
 def test_refusals(qs):
     import torch
     B, V, K = 3, 100, 4

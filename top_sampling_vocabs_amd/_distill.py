@@ -83,10 +83,11 @@ def _forward(logits, ids, values, temperature, bitmask, shape, rest, workspace):
     dev = logits.device
     B, V, K, index = shape
     code = _code(logits, "logits")
+    # allocations of their own: a loss changed in place (a masked or weighted sum does
+    # so) is no change of what the gradient reads
+    loss = torch.empty(B, dtype=torch.float32, device=dev)
     state = torch.empty((B, STATE), dtype=torch.float32, device=dev)
-    # the values per row in one allocation
-    loss, status = torch.empty((2, B), dtype=torch.float32, device=dev).unbind(0)
-    status = status.view(torch.int32)
+    status = torch.empty(B, dtype=torch.int32, device=dev)
     if workspace is None:
         n = lib.qs_distill_loss_workspace_bytes(B, V, code)
         if n:

@@ -635,7 +635,7 @@ int qs_distill_loss(const void* logits, int dtype, int64_t B, int64_t V, int64_t
   const void* req4[] = {teacher_ids, teacher_values, loss, row_state, row_status};
   for (const void* p : req4)
     if (!p || !aligned(p, 4)) return QS_ERR_INVALID_ARG;
-  if (!aligned(temperature, 4)) return QS_ERR_INVALID_ARG;
+  if (!aligned(temperature, 4) || !aligned(row_state, 16)) return QS_ERR_INVALID_ARG;
   if (!qs::distill::grid_fits(B, V, dtype)) return QS_ERR_INVALID_ARG;
   const size_t need = qs::distill::workspace_bytes(B, V, dtype);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
@@ -673,7 +673,7 @@ int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, int64_t V
   const void* req4[] = {teacher_ids, teacher_values, row_state, row_status, grad_loss};
   for (const void* p : req4)
     if (!p || !aligned(p, 4)) return QS_ERR_INVALID_ARG;
-  if (!aligned(temperature, 4)) return QS_ERR_INVALID_ARG;
+  if (!aligned(temperature, 4) || !aligned(row_state, 16)) return QS_ERR_INVALID_ARG;
   const int64_t es = dtype == QS_F32 ? 4 : 2;
   if (!grad_logits || !aligned(grad_logits, 16) || grad_stride < V || (grad_stride * es) % 16 != 0)
     return QS_ERR_INVALID_ARG;

@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/qs.h"
 #include "qs_device.hpp"
@@ -198,58 +199,63 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid,
       for (int v = 1; v < kWavesHere; ++v) sum[k] += sh.sum[k][v];
     }
   }
-  if (tid != 0) return;
+  if (tid >= 64) return;
+  // What is left is a handful of numbers. Four logarithms of the row stand side by
+  // side in four lanes, as log1p of an argument that keeps their relative precision:
+  // 0 the student's sum, one maximum's own 1 left out (so that log S keeps it where
+  // one token is almost certain), 1 the rest's sum, 2 the teacher's sum likewise,
+  // 3 q_R = 2^n (1 + x).
   const double below = sum[0], at = sum[1], cross = sum[4];
-  // the rest's weight against m; one maximum's own 1 is left out of the sum, so
-  // that log S keeps its relative precision where one token is almost certain
   const double dr = has ? ((double)rest.m - (double)m) / T : 0.0;
   const double f = has ? exp(dr) * (double)rest.S : 0.0;
   const double others = at > 0.0 ? below + (at - 1.0) + f : below + (f - 1.0);
-  const double ls = log1p(others);
-  const double lsr = has ? log((double)rest.S) : 0.0;
+  const double W = sum[2] + sum[3];
+  const double q_list = a.rest ? W : W > 0.0 ? 1.0 : 0.0;
+  const double q_rest = a.rest && has ? fmax(1.0 - q_list, 0.0) : 0.0;
+  int n = 0;
+  const double x3 = q_rest > 0.5 ? q_rest - 1.0 : q_rest > 0.0 ? frexp(q_rest, &n) - 1.0 : 0.0;
+  const double x = lane == 0 ? others : lane == 1 ? (has ? (double)rest.S - 1.0 : 0.0)
+                   : lane == 2 ? (!a.rest && W > 0.0 ? sum[2] + (sum[3] - 1.0) : 0.0) : x3;
+  const double y = log1p(x);
+  const double ls = readlane_f64(y, 0), lsr = readlane_f64(y, 1), tls = readlane_f64(y, 2);
+  const double lqr = readlane_f64(y, 3) + n * 0.69314718055994530942;
   const double lpr = dr + lsr - ls;
-  double loss, mass, q_list, q_rest = 0.0, tls = 0.0;
+  double loss;
   if (a.rest) {
-    q_list = sum[2];
-    if (has) q_rest = fmax(1.0 - q_list, 0.0);
     loss = cross + ls * q_list;
-    if (q_rest > 0.0) loss += q_rest * (log(q_rest) - lpr);
+    if (q_rest > 0.0) loss += q_rest * (lqr - lpr);
   } else {
-    const double W = sum[2] + sum[3];
-    q_list = W > 0.0 ? 1.0 : 0.0;
-    if (W > 0.0) tls = log1p(sum[2] + (sum[3] - 1.0));
     loss = W > 0.0 ? cross / W - tls + ls : 0.0;
   }
-  mass = q_list + q_rest;
+  const double mass = q_list + q_rest;
   const double pr = exp(lpr);
   // Q p_R - q_R, from the smaller of the two halves
   const double rest_grad =
       !has ? 0.0 : pr < 0.5 ? mass * pr - q_rest : q_list - mass * (below + at) / (1.0 + others);
+  if (tid != 0) return;
   a.status[r] = QS_ROW_OK;
   a.loss[r] = (float)loss;
-  state[0] = m;
-  state[1] = (float)ls;
-  state[2] = has ? rest.m : 0.0f;
-  state[3] = (float)lsr;
-  state[4] = (float)rest_grad;
-  state[5] = a.rest ? 0.0f : tmax;
-  state[6] = (float)tls;
-  state[7] = (float)(mass - 1.0);
+  float4* const out = reinterpret_cast<float4*>(state);
+  out[0] = make_float4(m, (float)ls, has ? rest.m : 0.0f, (float)lsr);
+  out[1] = make_float4((float)rest_grad, a.rest ? 0.0f : tmax, (float)tls, (float)(mass - 1.0));
 }
 
-// One workgroup per row (ROW: parts == 1, outputs written here) or per part.
-template <int DT, int THREADS, int NL, bool MASK, bool ROW>
+// One workgroup per row (ROW: parts == 1, outputs written here) or per part. Of a whole
+// row's workgroup one wave takes the slots and finishes the row, which needs no
+// barrier, where its lanes hold them (FT == 64), and all waves longer lists.
+template <int DT, int THREADS, int NL, bool MASK, bool ROW, int FT>
 __global__ void __launch_bounds__(THREADS)
     distill_kernel(Args a, int parts, int part_loads, Part* ws_parts) {
   constexpr int kWavesHere = THREADS / 64;
   constexpr int P = kPer<DT>, kSpan = THREADS * NL * P;
   constexpr bool kTable = MASK && DT == QS_BF16;
-  constexpr int N = (kSlotsMax + THREADS - 1) / THREADS;
+  constexpr int N = FT == 64 ? kJoinSlots : kSlotsMax / FT;
   __shared__ uint32_t s_named[kSpan / 32];
   __shared__ uint4 s_masks[kTable ? 256 : 1];  // masks_of every byte of legal bits
   __shared__ FinishShared s_fin;
   __shared__ float s_m[kWavesHere], s_S[kWavesHere];
-  const int tid = threadIdx.x, lane = lane_id(), w = tid >> 6;
+  __shared__ uint32_t s_any[kWavesHere], s_dup[kWavesHere];
+  const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
   const int r = ROW ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)parts);
   const int part = ROW ? 0 : (int)(blockIdx.x - (unsigned)r * (unsigned)parts);
   const int span = part_loads * THREADS * P;
@@ -262,8 +268,9 @@ __global__ void __launch_bounds__(THREADS)
   // requests: the slots, then 16 bytes per lane and load; loads that begin past the
   // row's end are left out (a 16-byte chunk that begins inside the row ends inside
   // its stride)
-  Slots<DT, THREADS, N> slots;
-  slots.load_ids(a, r, tid);
+  Slots<DT, FT, N> slots;
+  const bool finisher = FT == THREADS || w == 0;
+  if (finisher) slots.load_ids(a, r, tid);
   uint4 v[NL];
   uint32_t legal[NL];
 #pragma unroll
@@ -284,15 +291,17 @@ __global__ void __launch_bounds__(THREADS)
   }
   __syncthreads();
   uint32_t dup = 0u;
+  if (finisher) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int d = slots.id[i] - begin;
-    if (slots.id[i] >= begin && d < span) {
-      const uint32_t bit = 1u << (d & 31);
-      dup |= atomicOr(&s_named[d >> 5], bit) & bit;
+    for (int i = 0; i < N; ++i) {
+      const int d = slots.id[i] - begin;
+      if (slots.id[i] >= begin && d < span) {
+        const uint32_t bit = 1u << (d & 31);
+        dup |= atomicOr(&s_named[d >> 5], bit) & bit;
+      }
     }
+    if constexpr (ROW) slots.load(a, r, tid);
   }
-  if constexpr (ROW) slots.load(a, r, tid);
   __syncthreads();
 
   // largest legal token of the lane that is not named; the others become -inf
@@ -339,19 +348,26 @@ __global__ void __launch_bounds__(THREADS)
     }
   }
   const float Sw = wave_sum_f32(S[0] + S[1]);
+  const bool anyw = ballot(any != 0u) != 0, dupw = ballot(dup != 0u) != 0;
   if (lane == 0) {
     s_m[w] = wave_max;
     s_S[w] = Sw;
+    s_any[w] = anyw;
+    s_dup[w] = dupw;
   }
-  any = __syncthreads_or(any != 0u);
-  dup = __syncthreads_or(dup != 0u);
-  Part p{s_m[0], 0.0f, any, dup};
+  __syncthreads();
+  if (!finisher) return;
+  Part p{s_m[0], 0.0f, s_any[0], s_dup[0]};
 #pragma unroll
-  for (int q = 1; q < kWavesHere; ++q) p.m = fmaxf(p.m, s_m[q]);
+  for (int q = 1; q < kWavesHere; ++q) {
+    p.m = fmaxf(p.m, s_m[q]);
+    p.any |= s_any[q];
+    p.dup |= s_dup[q];
+  }
 #pragma unroll
   for (int q = 0; q < kWavesHere; ++q) p.S += s_S[q] * exp2_hw(rel(s_m[q], p.m, c));
   if constexpr (ROW) {
-    finish_row<DT, THREADS, N>(a, r, tid, slots, p, s_fin);
+    finish_row<DT, FT, N>(a, r, tid, slots, p, s_fin);
   } else {
     if (tid == 0) ws_parts[(size_t)r * parts + part] = p;
   }
@@ -385,39 +401,43 @@ __global__ void __launch_bounds__(THREADS)
   finish_row<DT, THREADS, kJoinSlots>(a, r, tid, slots, rest, s_fin);
 }
 
-template <int DT, int THREADS, int NL, bool ROW>
+template <int DT, int THREADS, int NL, bool ROW, int FT>
 void launch(const Args& a, int blocks, int parts, int part_loads, Part* wp, hipStream_t st) {
   const dim3 grid((unsigned)blocks), block(THREADS);
   if (a.bitmask)
-    hipLaunchKernelGGL((distill_kernel<DT, THREADS, NL, true, ROW>), grid, block, 0, st, a, parts,
-                       part_loads, wp);
+    hipLaunchKernelGGL((distill_kernel<DT, THREADS, NL, true, ROW, FT>), grid, block, 0, st, a,
+                       parts, part_loads, wp);
   else
-    hipLaunchKernelGGL((distill_kernel<DT, THREADS, NL, false, ROW>), grid, block, 0, st, a, parts,
-                       part_loads, wp);
+    hipLaunchKernelGGL((distill_kernel<DT, THREADS, NL, false, ROW, FT>), grid, block, 0, st, a,
+                       parts, part_loads, wp);
 }
 
 template <int DT>
 hipError_t launch_dt(const Args& a, int B, int parts, Part* wp, hipStream_t st) {
   constexpr int P = kPer<DT>;
+  const bool few = a.K <= 64 * kJoinSlots;  // slots that one wave holds
   if (parts == 1) {
+    auto run = [&](auto threads, auto loads) {
+      constexpr int TH = decltype(threads)::value, NL = decltype(loads)::value;
+      const int each = (a.V + TH * P - 1) / (TH * P);
+      if (few) launch<DT, TH, NL, true, 64>(a, B, 1, each, nullptr, st);
+      else launch<DT, TH, NL, true, TH>(a, B, 1, each, nullptr, st);
+    };
     if (a.V <= kSmallBlock * kSmallLoads * P)
-      launch<DT, kSmallBlock, kSmallLoads, true>(
-          a, B, 1, (a.V + kSmallBlock * P - 1) / (kSmallBlock * P), nullptr, st);
+      run(std::integral_constant<int, kSmallBlock>(), std::integral_constant<int, kSmallLoads>());
     else
-      launch<DT, kRowBlock, kRowLoads, true>(
-          a, B, 1, (a.V + kRowBlock * P - 1) / (kRowBlock * P), nullptr, st);
+      run(std::integral_constant<int, kRowBlock>(), std::integral_constant<int, kRowLoads>());
     return hipGetLastError();
   }
   // parts of equal length, in whole loads
   const int loads = (a.V + kPartBlock * P - 1) / (kPartBlock * P);
   const int each = (loads + parts - 1) / parts;
   if (loads_for(B, a.V, DT) == kPartLoads)
-    launch<DT, kPartBlock, kPartLoads, false>(a, B * parts, parts, each, wp, st);
+    launch<DT, kPartBlock, kPartLoads, false, kPartBlock>(a, B * parts, parts, each, wp, st);
   else
-    launch<DT, kPartBlock, kShortLoads, false>(a, B * parts, parts, each, wp, st);
+    launch<DT, kPartBlock, kShortLoads, false, kPartBlock>(a, B * parts, parts, each, wp, st);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  // one wave a row where its lanes hold the slots
-  if (a.K <= 64 * kJoinSlots)
+  if (few)
     hipLaunchKernelGGL((distill_join_kernel<DT, 64>), dim3((unsigned)B), dim3(64), 0, st, a, parts,
                        wp);
   else
