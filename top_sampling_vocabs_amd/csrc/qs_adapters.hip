@@ -2,9 +2,20 @@
 // adapter of row b,
 //   y[b][v] = z[b][v] + scale[a] sum_r up[a][v][r] u[b][r],
 //   u[b][r] = sum_k down[a][r][k] x[b][k].
-// Two launches: the rows' low-rank coordinates u, in float32, then their product with
-// the adapters' up factors on top of the logits. Products are exact in float32, sums
-// are held in float32, and each logit is rounded once.
+// Two launches: the rows' low-rank coordinates scale * u, then their product with the
+// up factors on top of the logits. Every used adapter is read once per 64 rows,
+// however they share it; what bounds the calls is reading the up factors, and the
+// logits read and written.
+//
+// Both products run on the matrix cores (16x16x32) with the factor's rows on one side
+// and 16 rows of the batch on the other. A product's column depends on its own batch
+// row alone, so an adapter is multiplied with all 16 and taken by the rows that are
+// its own: no gathering of rows by adapter, and what another row holds (an infinity,
+// uninitialised scratch) cannot reach a result. Products of the bf16 factors are exact.
+// The coordinates are float32; for the second product each is cut into three bf16
+// numbers of 8 bits, whose sum is it: the three products cost nothing beside the
+// factors' bytes (one rounded to bf16 would cost the result 2^-8 of the adapter's
+// share). Sums are held in float32, and each logit is rounded once.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -17,97 +28,273 @@ namespace qs {
 namespace adapters {
 namespace {
 
-constexpr int kBlock = 256;
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+constexpr int kRows = 64;         // batch rows of a block
+constexpr int kTerms = 3;         // bf16 numbers per coordinate
+constexpr int kDownWaves = 16;    // slices of k
+constexpr int kAhead = 4;         // steps of 32 columns requested at a time
+constexpr int kUpWaves = 4;
+constexpr int kTiles = 4;         // tiles of 16 vocabulary rows per wave
 
-// One wave per row and rank.
-__global__ void __launch_bounds__(kBlock) down_kernel(Args a) {
-  const int lane = lane_id();
-  const int64_t item = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-  if (item >= (int64_t)a.B * a.rank) return;
-  const int b = (int)(item / a.rank), q = (int)(item - (int64_t)b * a.rank);
-  const int n = a.index[b];
-  const bool valid = n >= -1 && n < a.count;
-  if (q == 0 && lane == 0) a.status[b] = valid ? QS_ROW_OK : QS_ROW_BAD_PARAM;
-  if (!valid || n < 0) return;
-  const uint16_t* const x = a.hidden + (size_t)b * a.hidden_stride;
-  const uint16_t* const w = a.down + (size_t)n * a.down_stride + (size_t)q * a.down_row_stride;
-  float sum = 0.0f;
-  for (int k = lane * 8; k < a.K; k += 512) {
-    const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
-    const uint4 wv = *reinterpret_cast<const uint4*>(w + k);
-    const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sum = fmaf(lo(xs[e]), lo(ws[e]), sum);
-      sum = fmaf(hi(xs[e]), hi(ws[e]), sum);
-    }
-  }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  if (lane == 0) a.low[item] = sum * (a.scale ? a.scale[n] : 1.0f);
+// The workspace holds the coordinates as the second product takes them: per tile of
+// 16 batch rows, step of 32 ranks and term the 64 lanes' 8 bf16 numbers, lane
+// (row n, ranks 8 g to 8 g + 7) at 16 g + n.
+constexpr int kStepBytes = kTerms * 64 * 16;
+
+// The adapter of each of a block's rows in its lane; -1: none, or none that exists.
+__device__ __forceinline__ int row_index(const Args& a, int row0, int lane) {
+  const int b = row0 + lane;
+  const int n = b < a.B ? a.index[b] : -1;
+  return n >= 0 && n < a.count ? n : -1;
 }
 
-// One thread per logit.
-template <int DT>
-__global__ void __launch_bounds__(kBlock) up_kernel(Args a, int chunks) {
-  const int b = (int)(blockIdx.x / (unsigned)chunks);
-  const int v = (int)(blockIdx.x - (unsigned)b * (unsigned)chunks) * kBlock + (int)threadIdx.x;
-  if (v >= a.V) return;
-  const int n = a.index[b];
-  const bool adapted = n >= 0 && n < a.count;
-  if (!adapted && a.out == a.logits) return;
-  const uint8_t* const z = a.logits + (size_t)b * a.row_bytes;
-  uint8_t* const out = a.out + (size_t)b * a.out_bytes;
-  float sum = 0.0f;
-  if (adapted) {
-    const uint16_t* const w = a.up + (size_t)n * a.up_stride + (size_t)v * a.up_row_stride;
-    const float* const u = a.low + (size_t)b * a.rank;
-    for (int q = 0; q < a.rank; q += 8) {
-      const uint4 wv = *reinterpret_cast<const uint4*>(w + q);
-      const uint32_t ws[4] = {wv.x, wv.y, wv.z, wv.w};
+// The rows' coordinates. One workgroup per batch row and 16 ranks; the first row of an
+// adapter in its block works for all rows that share it. The waves are slices of k,
+// whose sums meet in LDS in order.
+template <int RT>
+__global__ void __launch_bounds__(kDownWaves * 64) down_kernel(Args a, int steps) {
+  __shared__ f32x4 s_part[kDownWaves][RT][64];
+  const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
+  const int n = lane & 15, kg = lane >> 4;
+  const int b = blockIdx.x, row0 = b & ~(kRows - 1), q0 = (int)blockIdx.y * 16;
+  const int mine = row_index(a, row0, lane);
+  const int own = readlane_u32((uint32_t)mine, b - row0);
+  if (blockIdx.y == 0 && tid == 0) {
+    const int asked = a.index[b];
+    a.status[b] = asked < -1 || asked >= a.count ? QS_ROW_BAD_PARAM : QS_ROW_OK;
+  }
+  const uint64_t members = ballot(mine == own);
+  if (own < 0 || __builtin_ctzll(members) != b - row0) return;
+
+  f32x4 acc[RT];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum = fmaf(lo(ws[e]), u[q + 2 * e], sum);
-        sum = fmaf(hi(ws[e]), u[q + 2 * e + 1], sum);
+  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (q0 < a.rank) {
+    const uint16_t* const d = a.down + (size_t)own * a.down_stride +
+                              (size_t)min(q0 + n, a.rank - 1) * a.down_row_stride + kg * 8;
+    const uint16_t* x[RT];
+    bool has[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      has[t] = (members >> (t * 16 + n)) & 1u;
+      x[t] = a.hidden + (size_t)(row0 + t * 16 + (has[t] ? n : 0)) * a.hidden_stride + kg * 8;
+    }
+    // columns of 32, the waves in turn, so that their loads lie beside each other
+    for (int k0 = w * 32; k0 < a.K; k0 += kAhead * kDownWaves * 32) {
+      uint4 dv[kAhead], xv[kAhead][RT];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = k0 + j * kDownWaves * 32;
+        const bool in = k + kg * 8 < a.K;
+        dv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (in) dv[j] = *reinterpret_cast<const uint4*>(d + k);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          xv[j][t] = make_uint4(0u, 0u, 0u, 0u);
+          if (in && has[t]) xv[j][t] = *reinterpret_cast<const uint4*>(x[t] + k);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (((members >> (t * 16)) & 0xFFFFu) == 0u) continue;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, dv[j]), __builtin_bit_cast(bf16x8, xv[j][t]), acc[t], 0,
+              0, 0);
       }
     }
   }
-  if constexpr (DT == QS_F32) {
-    const float y = reinterpret_cast<const float*>(z)[v];
-    reinterpret_cast<float*>(out)[v] = adapted ? y + sum : y;
-  } else {
-    const uint16_t y = reinterpret_cast<const uint16_t*>(z)[v];
-    if (adapted)
-      reinterpret_cast<__bf16*>(out)[v] = (__bf16)(__uint_as_float((uint32_t)y << 16) + sum);
-    else
-      reinterpret_cast<uint16_t*>(out)[v] = y;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) s_part[w][t][lane] = acc[t];
+  __syncthreads();
+  // a thread to each tile's lane: batch row n, ranks q0 + 4 kg to q0 + 4 kg + 3
+  const int t = w;
+  if (t >= RT || !((members >> (t * 16 + n)) & 1u)) return;
+  f32x4 u = s_part[0][t][lane];
+#pragma unroll
+  for (int k = 1; k < kDownWaves; ++k) u += s_part[k][t][lane];
+  u *= a.scale ? a.scale[own] : 1.0f;
+  const int q = q0 + kg * 4;
+  if (q >= a.rank) u = f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // met by factors of 0
+  uint8_t* const out = a.low + ((size_t)(row0 / 16 + t) * steps + (q >> 5)) * kStepBytes +
+                       (((q & 31) >> 3) * 16 + n) * 16 + (q & 7) * 2;
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k) {
+    const bf16x4 part = __builtin_convertvector(u, bf16x4);
+    *reinterpret_cast<bf16x4*>(out + k * 1024) = part;
+    u -= __builtin_convertvector(part, f32x4);
   }
 }
+
+// The logits. A wave takes kTiles tiles of 16 vocabulary rows and up to RT tiles of 16
+// batch rows: the logits are its accumulators, and it walks the block's adapters. The
+// tiles' rows are dealt out so that a lane holds 4 kTiles consecutive logits of one
+// batch row: product row 4 g + e of tile t is vocabulary row 4 (kTiles g + t) + e.
+template <int DT, int KS, int RT>
+__global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
+  constexpr int kSpan = 16 * kTiles;      // vocabulary rows per wave
+  constexpr int P = DT == QS_F32 ? 4 : 8; // logits per 16 bytes
+  __shared__ uint4 s_low[RT * KS * kTerms * 64];
+  const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
+  const int n = lane & 15, kg = lane >> 4;
+  const int row0 = (int)blockIdx.y * kRows;
+  const int tile = (int)blockIdx.x * kUpWaves + w;
+  const int v0 = tile * kSpan, first = v0 + kg * 4 * kTiles;  // the lane's first logit
+  const int mine = row_index(a, row0, lane);
+  const uint64_t adapted = ballot(mine >= 0);
+  const bool in_place = a.out == a.logits;
+  if (in_place && adapted == 0u) return;
+
+  int own[RT];     // the adapter of this lane's batch row
+  f32x4 y[kTiles][RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    own[t] = __shfl(mine, t * 16 + n, 64);
+    const int b = row0 + t * 16 + n;
+    const bool use = b < a.B && !(in_place && own[t] < 0);
+    const uint8_t* const z = a.logits + (size_t)(use ? b : 0) * a.row_bytes;
+#pragma unroll
+    for (int c = 0; c < 4 * kTiles / P; ++c) {
+      uint4 q = make_uint4(0u, 0u, 0u, 0u);
+      if (use && first + c * P < a.V)
+        q = *reinterpret_cast<const uint4*>(z + (size_t)(first + c * P) * (16 / P));
+      const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const int i = c * P + e;
+        if constexpr (DT == QS_F32) y[i >> 2][t][i & 3] = __uint_as_float(word[e]);
+        else y[i >> 2][t][i & 3] =
+            __uint_as_float((e & 1) ? word[e >> 1] & 0xFFFF0000u : word[e >> 1] << 16);
+      }
+    }
+  }
+  // the coordinates, as they lie
+  const int row_tiles = (min(a.B - row0, kRows) + 15) / 16;
+  for (int i = tid; i < row_tiles * KS * kTerms * 64; i += kUpWaves * 64)
+    s_low[i] = reinterpret_cast<const uint4*>(a.low + (size_t)(row0 / 16) * KS * kStepBytes)[i];
+  __syncthreads();
+  if (tile >= tiles) return;
+
+  for (uint64_t left = adapted; left != 0u;) {
+    const int d = readlane_u32((uint32_t)mine, __builtin_ctzll(left));
+    const uint64_t members = ballot(mine == d);
+    left &= ~members;
+    const uint16_t* const up = a.up + (size_t)d * a.up_stride;
+    bf16x8 f[kTiles][KS];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int v = min(v0 + (n >> 2) * 4 * kTiles + i * 4 + (n & 3), a.V - 1);
+      const uint16_t* const row = up + (size_t)v * a.up_row_stride;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (s * 32 + kg * 8 < a.rank) q = *reinterpret_cast<const uint4*>(row + s * 32 + kg * 8);
+        f[i][s] = __builtin_bit_cast(bf16x8, q);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      if (((members >> (t * 16)) & 0xFFFFu) == 0u) continue;
+      f32x4 acc[kTiles];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) acc[i] = y[i][t];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) {
+          const bf16x8 u =
+              __builtin_bit_cast(bf16x8, s_low[((t * KS + s) * kTerms + k) * 64 + lane]);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[i][s], u, acc[i], 0, 0, 0);
+        }
+      }
+      const bool take = own[t] == d;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][t][e] = take ? acc[i][e] : y[i][t][e];
+      }
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int b = row0 + t * 16 + n;
+    if (b >= a.B || (in_place && own[t] < 0)) continue;
+    uint8_t* const out = a.out + (size_t)b * a.out_bytes;
+#pragma unroll
+    for (int c = 0; c < 4 * kTiles / P; ++c) {
+      const int v = first + c * P;
+      if (v >= a.V) break;
+      uint32_t word[4];
+      if constexpr (DT == QS_F32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) word[e] = __float_as_uint(y[c][t][e]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bf16x4 half = __builtin_convertvector(y[c * 2 + h][t], bf16x4);
+          __builtin_memcpy(word + 2 * h, &half, 8);
+        }
+      }
+      if (a.V - v >= P) {
+        *reinterpret_cast<uint4*>(out + (size_t)v * (16 / P)) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+      } else {  // the row's last logits: what lies behind them stays
+#pragma unroll
+        for (int e = 0; e < P - 1; ++e) {
+          if (v + e < a.V) {
+            if constexpr (DT == QS_F32) reinterpret_cast<uint32_t*>(out)[v + e] = word[e];
+            else reinterpret_cast<uint16_t*>(out)[v + e] =
+                (uint16_t)(word[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int KS>
+void launch_up(const Args& a, hipStream_t st) {
+  const int tiles = (a.V + 16 * kTiles - 1) / (16 * kTiles);
+  const dim3 grid((unsigned)((tiles + kUpWaves - 1) / kUpWaves),
+                  (unsigned)((a.B + kRows - 1) / kRows));
+  const dim3 block(kUpWaves * 64);
+  if (a.B <= 16) hipLaunchKernelGGL((up_kernel<DT, KS, 1>), grid, block, 0, st, a, tiles);
+  else if (a.B <= 32) hipLaunchKernelGGL((up_kernel<DT, KS, 2>), grid, block, 0, st, a, tiles);
+  else hipLaunchKernelGGL((up_kernel<DT, KS, 4>), grid, block, 0, st, a, tiles);
+}
+
+template <int DT>
+void launch_rank(const Args& a, int steps, hipStream_t st) {
+  if (steps == 1) launch_up<DT, 1>(a, st);
+  else if (steps == 2) launch_up<DT, 2>(a, st);
+  else if (steps == 3) launch_up<DT, 3>(a, st);
+  else launch_up<DT, 4>(a, st);
+}
+
+int steps_of(int64_t rank) { return (int)((rank + 31) / 32); }
 
 }  // namespace
 
 size_t workspace_bytes(int64_t B, int64_t rank) {
-  return ((size_t)B * (size_t)rank * sizeof(float) + 255) & ~(size_t)255;
-}
-
-bool grid_fits(int64_t B, int64_t V, int64_t rank) {
-  const int64_t chunks = (V + kBlock - 1) / kBlock;
-  return B * chunks * kBlock < (int64_t)1 << 32 && B * rank * 64 < (int64_t)1 << 32;
+  return (size_t)((B + 15) / 16) * steps_of(rank) * kStepBytes;
 }
 
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
-  const int64_t items = (int64_t)a.B * a.rank;
-  hipLaunchKernelGGL(down_kernel, dim3((unsigned)((items + 3) / 4)), dim3(kBlock), 0, st, a);
+  const int steps = steps_of(a.rank);
+  const dim3 grid((unsigned)a.B, (unsigned)(2 * steps)), block(kDownWaves * 64);
+  if (a.B <= 16) hipLaunchKernelGGL((down_kernel<1>), grid, block, 0, st, a, steps);
+  else if (a.B <= 32) hipLaunchKernelGGL((down_kernel<2>), grid, block, 0, st, a, steps);
+  else hipLaunchKernelGGL((down_kernel<4>), grid, block, 0, st, a, steps);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  const int chunks = (a.V + kBlock - 1) / kBlock;
-  const dim3 grid((unsigned)a.B * (unsigned)chunks);
-  if (dtype == QS_F32)
-    hipLaunchKernelGGL((up_kernel<QS_F32>), grid, dim3(kBlock), 0, st, a, chunks);
-  else
-    hipLaunchKernelGGL((up_kernel<QS_BF16>), grid, dim3(kBlock), 0, st, a, chunks);
+  if (dtype == QS_F32) launch_rank<QS_F32>(a, steps, st);
+  else launch_rank<QS_BF16>(a, steps, st);
   return hipGetLastError();
 }
 

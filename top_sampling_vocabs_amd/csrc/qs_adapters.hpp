@@ -29,12 +29,10 @@ struct Args {
   const int32_t* index;      // [B]; -1: none
   const float* scale;        // [count], optional (NULL: 1)
   int32_t* status;           // [B]
-  float* low;                // workspace: [B][rank], the rows' low-rank coordinates
+  uint8_t* low;              // workspace: the rows' low-rank coordinates
 };
 
 size_t workspace_bytes(int64_t B, int64_t rank);
-// whether the launches' grids hold the batch
-bool grid_fits(int64_t B, int64_t V, int64_t rank);
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st);
 
 }  // namespace adapters

@@ -738,7 +738,6 @@ int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V, int64
     return QS_ERR_INVALID_ARG;
   // in place only row for row: otherwise one row's writes meet another's reads
   if (out == logits && out_stride != row_stride) return QS_ERR_INVALID_ARG;
-  if (!ad::grid_fits(B, V, rank)) return QS_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < ad::workspace_bytes(B, rank))
     return QS_ERR_WORKSPACE;
   ad::Args a;
@@ -762,7 +761,7 @@ int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V, int64
   a.index = index;
   a.scale = scale;
   a.status = row_status;
-  a.low = static_cast<float*>(workspace);
+  a.low = static_cast<uint8_t*>(workspace);
   hipError_t e = ad::launch_adapters(a, dtype, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QS_OK : QS_ERR_HIP;
 }
