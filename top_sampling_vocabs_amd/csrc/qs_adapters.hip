@@ -34,8 +34,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 64;         // batch rows of a block
 constexpr int kTerms = 3;         // bf16 numbers per coordinate
-constexpr int kDownWaves = 16;    // slices of k
-constexpr int kAhead = 4;         // steps of 32 columns requested at a time
+constexpr int kAhead = 8;         // loads of 512 columns that a wave requests at a time
 constexpr int kUpWaves = 4;
 constexpr int kTiles = 4;         // tiles of 16 vocabulary rows per wave
 
@@ -51,82 +50,65 @@ __device__ __forceinline__ int row_index(const Args& a, int row0, int lane) {
   return n >= 0 && n < a.count ? n : -1;
 }
 
-// The rows' coordinates. One workgroup per batch row and 16 ranks; the first row of an
-// adapter in its block works for all rows that share it. The waves are slices of k,
-// whose sums meet in LDS in order.
-template <int RT>
-__global__ void __launch_bounds__(kDownWaves * 64) down_kernel(Args a, int steps) {
-  __shared__ f32x4 s_part[kDownWaves][RT][64];
-  const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
-  const int n = lane & 15, kg = lane >> 4;
-  const int b = blockIdx.x, row0 = b & ~(kRows - 1), q0 = (int)blockIdx.y * 16;
-  const int mine = row_index(a, row0, lane);
-  const int own = readlane_u32((uint32_t)mine, b - row0);
-  if (blockIdx.y == 0 && tid == 0) {
-    const int asked = a.index[b];
-    a.status[b] = asked < -1 || asked >= a.count ? QS_ROW_BAD_PARAM : QS_ROW_OK;
-  }
-  const uint64_t members = ballot(mine == own);
-  if (own < 0 || __builtin_ctzll(members) != b - row0) return;
-
-  f32x4 acc[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (q0 < a.rank) {
-    const uint16_t* const d = a.down + (size_t)own * a.down_stride +
-                              (size_t)min(q0 + n, a.rank - 1) * a.down_row_stride + kg * 8;
-    const uint16_t* x[RT];
-    bool has[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      has[t] = (members >> (t * 16 + n)) & 1u;
-      x[t] = a.hidden + (size_t)(row0 + t * 16 + (has[t] ? n : 0)) * a.hidden_stride + kg * 8;
-    }
-    // columns of 32, the waves in turn, so that their loads lie beside each other
-    for (int k0 = w * 32; k0 < a.K; k0 += kAhead * kDownWaves * 32) {
-      uint4 dv[kAhead], xv[kAhead][RT];
+// The rows' coordinates, a wave to each (row, rank): few rows spread over as many
+// compute units as they have ranks, each wave requests up to kAhead KiB of the factor
+// before it uses any, and rows that share an adapter read it from the L2. (On the matrix
+// cores, 16 ranks and the rows that share an adapter to a workgroup: 1 row of 4096
+// columns, rank 16, 6.5 us, one compute unit's loads; 64 rows of 8192 on adapters of
+// their own, rank 32, 14.2; 64 on 3 of rank 64, 4096 columns, 7.9.)
+__global__ void __launch_bounds__(256) down_kernel(Args a, int steps) {
+  const int lane = lane_id();
+  const int item = uni((int)(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)));
+  const int ranks = steps * 32;            // with zeros behind the last
+  const int b = item / ranks, q = item - b * ranks;
+  if (b >= a.B) return;
+  const int n = a.index[b];
+  const bool valid = n >= -1 && n < a.count;
+  if (q == 0 && lane == 0) a.status[b] = valid ? QS_ROW_OK : QS_ROW_BAD_PARAM;
+  if (!valid || n < 0) return;
+  float u = 0.0f;
+  if (q < a.rank) {
+    const float scale = a.scale ? a.scale[n] : 1.0f;
+    const uint16_t* const x = a.hidden + (size_t)b * a.hidden_stride;
+    const uint16_t* const d =
+        a.down + (size_t)n * a.down_stride + (size_t)q * a.down_row_stride;
+    float sum[2] = {0.0f, 0.0f};
+    for (int k0 = lane * 8; k0 < a.K; k0 += kAhead * 512) {
+      uint4 dv[kAhead], xv[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int k = k0 + j * kDownWaves * 32;
-        const bool in = k + kg * 8 < a.K;
-        dv[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (in) dv[j] = *reinterpret_cast<const uint4*>(d + k);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          xv[j][t] = make_uint4(0u, 0u, 0u, 0u);
-          if (in && has[t]) xv[j][t] = *reinterpret_cast<const uint4*>(x[t] + k);
+        dv[j] = xv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (k0 + j * 512 < a.K) {
+          dv[j] = *reinterpret_cast<const uint4*>(d + k0 + j * 512);
+          xv[j] = *reinterpret_cast<const uint4*>(x + k0 + j * 512);
         }
       }
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        if (((members >> (t * 16)) & 0xFFFFu) == 0u) continue;
+      for (int j = 0; j < kAhead; ++j) {
+        const uint32_t ds[4] = {dv[j].x, dv[j].y, dv[j].z, dv[j].w};
+        const uint32_t xs[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, dv[j]), __builtin_bit_cast(bf16x8, xv[j][t]), acc[t], 0,
-              0, 0);
+        for (int e = 0; e < 4; ++e) {
+          sum[0] = fmaf(__uint_as_float(ds[e] << 16), __uint_as_float(xs[e] << 16), sum[0]);
+          sum[1] = fmaf(__uint_as_float(ds[e] & 0xFFFF0000u), __uint_as_float(xs[e] & 0xFFFF0000u),
+                        sum[1]);
+        }
       }
     }
+    u = sum[0] + sum[1];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) u += __shfl_xor(u, off, 64);
+    u *= scale;
   }
+  if (lane == 0) {
+    uint8_t* const out = a.low + ((size_t)(b / 16) * steps + (q >> 5)) * kStepBytes +
+                         (((q & 31) >> 3) * 16 + (b & 15)) * 16 + (q & 7) * 2;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) s_part[w][t][lane] = acc[t];
-  __syncthreads();
-  // a thread to each tile's lane: batch row n, ranks q0 + 4 kg to q0 + 4 kg + 3
-  const int t = w;
-  if (t >= RT || !((members >> (t * 16 + n)) & 1u)) return;
-  f32x4 u = s_part[0][t][lane];
-#pragma unroll
-  for (int k = 1; k < kDownWaves; ++k) u += s_part[k][t][lane];
-  u *= a.scale ? a.scale[own] : 1.0f;
-  const int q = q0 + kg * 4;
-  if (q >= a.rank) u = f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // met by factors of 0
-  uint8_t* const out = a.low + ((size_t)(row0 / 16 + t) * steps + (q >> 5)) * kStepBytes +
-                       (((q & 31) >> 3) * 16 + n) * 16 + (q & 7) * 2;
-#pragma unroll
-  for (int k = 0; k < kTerms; ++k) {
-    const bf16x4 part = __builtin_convertvector(u, bf16x4);
-    *reinterpret_cast<bf16x4*>(out + k * 1024) = part;
-    u -= __builtin_convertvector(part, f32x4);
+    for (int k = 0; k < kTerms; ++k) {
+      const __bf16 part = (__bf16)u;
+      *reinterpret_cast<__bf16*>(out + k * 1024) = part;
+      u -= (float)part;
+    }
   }
 }
 
@@ -288,10 +270,11 @@ size_t workspace_bytes(int64_t B, int64_t rank) {
 
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
   const int steps = steps_of(a.rank);
-  const dim3 grid((unsigned)a.B, (unsigned)(2 * steps)), block(kDownWaves * 64);
-  if (a.B <= 16) hipLaunchKernelGGL((down_kernel<1>), grid, block, 0, st, a, steps);
-  else if (a.B <= 32) hipLaunchKernelGGL((down_kernel<2>), grid, block, 0, st, a, steps);
-  else hipLaunchKernelGGL((down_kernel<4>), grid, block, 0, st, a, steps);
+  // one wave a workgroup where that spreads few waves over more compute units
+  const int64_t items = (int64_t)a.B * steps * 32;
+  const int waves = items > 1024 ? 4 : 1;
+  hipLaunchKernelGGL(down_kernel, dim3((unsigned)((items + waves - 1) / waves)), dim3(waves * 64), 0,
+                     st, a, steps);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (dtype == QS_F32) launch_rank<QS_F32>(a, steps, st);
   else launch_rank<QS_BF16>(a, steps, st);
