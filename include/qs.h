@@ -619,7 +619,7 @@ QS_API int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, in
  *   y[b][v] = z[b][v] + scale[a] * sum over r of up[a][v][r] *
  *             sum over k of down[a][r][k] * hidden[b][k]
  *
- * logits       [B][row_stride] float32 or bfloat16 (dtype), B at most 2^20, V at most
+ * logits       [B][row_stride] float32 or bfloat16 (dtype), B at most 2^18, V at most
  *              2^24, 16-byte aligned, row_stride * element size a multiple of 16
  * hidden       [B][hidden_stride] bfloat16, the hidden states that z came from; 16-byte
  *              aligned, hidden_stride a multiple of 8 and >= K; K a multiple of 8, at

@@ -87,7 +87,7 @@ HALF = ctypes.c_void_p(0x100008)
 
 
 @pytest.mark.parametrize("kw", [
-    dict(logits=None), dict(logits=ODD), dict(dtype=2), dict(B=-1), dict(B=(1 << 20) + 1),
+    dict(logits=None), dict(logits=ODD), dict(dtype=2), dict(B=-1), dict(B=(1 << 18) + 1),
     dict(V=0), dict(V=(1 << 24) + 1, stride=1 << 25, os=1 << 25), dict(stride=60), dict(stride=65),
     dict(x=None), dict(x=HALF), dict(K=0), dict(K=36), dict(K=65544, xs=65544, drs=65544),
     dict(xs=24), dict(xs=36), dict(down=None), dict(down=HALF), dict(ds=252), dict(ds=-256),
@@ -104,7 +104,7 @@ def test_apply_adapters_rejects_bad_arguments(lib, kw):  # noqa: F811
 def test_adapters_workspace(lib):  # noqa: F811
     assert adapt(lib, B=0, logits=None) == _lib.QS_OK
     f = lib.qs_adapters_workspace_bytes
-    for bad in ((0, 8), (-1, 8), ((1 << 20) + 1, 8), (4, 0), (4, 12), (4, 136), (4, -8)):
+    for bad in ((0, 8), (-1, 8), ((1 << 18) + 1, 8), (4, 0), (4, 12), (4, 136), (4, -8)):
         assert f(*bad) == 0
     need = f(4, 8)
     assert need > 0
@@ -112,7 +112,7 @@ def test_adapters_workspace(lib):  # noqa: F811
     assert adapt(lib, ws=None) == _lib.QS_ERR_WORKSPACE
     assert adapt(lib, ws=ctypes.c_void_p(0x400080)) == _lib.QS_ERR_WORKSPACE
     for rank in range(8, 129, 8):
-        sizes = [f(B, rank) for B in list(range(1, 300)) + [1 << 20]]
+        sizes = [f(B, rank) for B in list(range(1, 300)) + [1 << 18]]
         assert all(a <= b for a, b in zip(sizes, sizes[1:]))
 
 

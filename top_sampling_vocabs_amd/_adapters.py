@@ -4,30 +4,35 @@ The binding of qs_apply_adapters. Like the rest of the binding it only marshals
 arguments; it is loaded on first use, because it needs torch at import.
 """
 
+import functools
+
 import torch
 
 from ._lib import _check_logits, _status, load
 from ._scoring import _addr, _check_out, _check_vec, _code, _enqueue, _refuse_tangents, _wrote
 
 
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes(B, rank):
+    # a pure function of its arguments, asked once for each
+    return load().qs_adapters_workspace_bytes(B, rank)
+
+
 def adapters_workspace_for(logits, rank):
     """A workspace tensor for apply_adapters on these logits. Reuse it across calls on
     one stream, for batches of as many rows or fewer."""
-    n = load().qs_adapters_workspace_bytes(int(logits.shape[0]), int(rank))
-    return torch.empty(n, dtype=torch.uint8, device=logits.device)
+    return torch.empty(_workspace_bytes(int(logits.shape[0]), int(rank)), dtype=torch.uint8,
+                       device=logits.device)
 
 
 def _check_factor(t, name, shape, index):
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.get_device() != index \
-            or t.size(2) > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name} must be a bfloat16 tensor {shape} with unit stride in its last "
-                         f"dimension on cuda:{index}")
-
-
-def _strides(t):
-    """(between adapters, between rows); a dimension of one element counts as dense."""
-    row = t.stride(1) if t.size(1) > 1 else t.size(2)
-    return t.stride(0) if t.size(0) > 1 else 0, row
+    """t's shape and strides, a dimension of one element counted as dense."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.get_device() != index:
+        raise ValueError(f"{name} must be a bfloat16 tensor {shape} on cuda:{index}")
+    (n, rows, columns), (between, row, step) = t.shape, t.stride()
+    if step != 1 and columns > 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return n, rows, columns, between if n > 1 else 0, row if rows > 1 else columns
 
 
 def apply_adapters(logits, hidden, down, up, index, scale=None, *, out=None, workspace=None):
@@ -50,17 +55,16 @@ def apply_adapters(logits, hidden, down, up, index, scale=None, *, out=None, wor
         raise ValueError("hidden must be a bfloat16 tensor [B, K] with unit column stride on "
                          f"cuda:{dev}")
     K = hidden.size(1)
-    _check_factor(down, "down", "[count, rank, K]", dev)
-    _check_factor(up, "up", "[count, V, rank]", dev)
-    count, rank, width = down.shape
-    if width != K or up.shape != (count, V, rank):
+    count, rank, width, down_stride, down_row = _check_factor(down, "down", "[count, rank, K]", dev)
+    held, rows, ranks, up_stride, up_row = _check_factor(up, "up", "[count, V, rank]", dev)
+    if width != K or held != count or rows != V or ranks != rank:
         raise ValueError(f"down must be [count, rank, {K}] and up [count, {V}, rank], got "
                          f"{list(down.shape)} and {list(up.shape)}")
     _check_vec(index, B, torch.int32, dev, "index")
     if scale is not None:
         _check_vec(scale, count, torch.float32, dev, "scale")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (logits, hidden, down, up, scale)):
+    if (logits.requires_grad or hidden.requires_grad or down.requires_grad or up.requires_grad
+            or scale is not None and scale.requires_grad) and torch.is_grad_enabled():
         raise ValueError("apply_adapters has no gradient: call it under torch.no_grad() "
                          "or on detached tensors")
     if out is None:
@@ -69,19 +73,22 @@ def apply_adapters(logits, hidden, down, up, index, scale=None, *, out=None, wor
             or out.get_device() != dev or out.stride(1) != 1:
         raise ValueError("out must have the logits' shape, dtype and device "
                          "and unit column stride")
-    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _check_out(out)
     _refuse_tangents(logits, hidden, down, up, scale, out)
     if workspace is None:
-        workspace = adapters_workspace_for(logits, rank)
-    status = torch.empty(B, dtype=torch.int32, device=logits.device)
+        size = _workspace_bytes(B, rank)
+        workspace = torch.empty(size, dtype=torch.uint8, device=logits.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    status = torch.empty_like(index)
     rc = _enqueue(
         load().qs_apply_adapters, dev,
         logits.data_ptr(), _code(logits, "logits"), B, V, logits.stride(0), hidden.data_ptr(), K,
-        hidden.stride(0) if B > 1 else K, down.data_ptr(), *_strides(down), up.data_ptr(),
-        *_strides(up), count, rank, index.data_ptr(), _addr(scale), out.data_ptr(), out.stride(0),
-        status.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        hidden.stride(0) if B > 1 else K, down.data_ptr(), down_stride, down_row, up.data_ptr(),
+        up_stride, up_row, count, rank, index.data_ptr(), _addr(scale), out.data_ptr(),
+        out.stride(0), status.data_ptr(), workspace.data_ptr(), size)
     if rc:
         _status(rc, "qs_apply_adapters")
     _wrote(out)

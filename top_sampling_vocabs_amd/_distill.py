@@ -5,6 +5,8 @@ binding it only marshals arguments; it is loaded on first use, because it needs
 torch at import.
 """
 
+import functools
+
 import torch
 
 from ._lib import _check_logits, _status, load
@@ -34,12 +36,17 @@ def _check_inputs(logits, teacher_ids, teacher_values, temperature, bitmask):
     return B, V, teacher_ids.size(1), index
 
 
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes(B, V, code):
+    # a pure function of its arguments, asked once for each
+    return load().qs_distill_loss_workspace_bytes(B, V, code)
+
+
 def distill_loss_workspace_for(logits):
     """A workspace tensor for distill_loss on these logits, or None when the call
     needs none. Reuse it across calls on one stream, for batches of as many rows or
     fewer."""
-    n = load().qs_distill_loss_workspace_bytes(int(logits.shape[0]), int(logits.shape[1]),
-                                               _code(logits, "logits"))
+    n = _workspace_bytes(int(logits.shape[0]), int(logits.shape[1]), _code(logits, "logits"))
     return torch.empty(n, dtype=torch.uint8, device=logits.device) if n else None
 
 
@@ -89,7 +96,7 @@ def _forward(logits, ids, values, temperature, bitmask, shape, rest, workspace):
     state = torch.empty((B, STATE), dtype=torch.float32, device=dev)
     status = torch.empty(B, dtype=torch.int32, device=dev)
     if workspace is None:
-        n = lib.qs_distill_loss_workspace_bytes(B, V, code)
+        n = _workspace_bytes(B, V, code)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     rc = _enqueue(

@@ -34,9 +34,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 64;         // batch rows of a block
 constexpr int kTerms = 3;         // bf16 numbers per coordinate
-constexpr int kAhead = 8;         // loads of 512 columns that a wave requests at a time
 constexpr int kUpWaves = 4;
-constexpr int kTiles = 4;         // tiles of 16 vocabulary rows per wave
+constexpr int kTiles = 2;         // tiles of 16 vocabulary rows per wave
+constexpr int kAhead = 8;         // loads of 512 columns that a wave of the first product
+                                  // requests at a time
 
 // The workspace holds the coordinates as the second product takes them: per tile of
 // 16 batch rows, step of 32 ranks and term the 64 lanes' 8 bf16 numbers, lane
@@ -50,12 +51,13 @@ __device__ __forceinline__ int row_index(const Args& a, int row0, int lane) {
   return n >= 0 && n < a.count ? n : -1;
 }
 
-// The rows' coordinates, a wave to each (row, rank): few rows spread over as many
-// compute units as they have ranks, each wave requests up to kAhead KiB of the factor
-// before it uses any, and rows that share an adapter read it from the L2. (On the matrix
-// cores, 16 ranks and the rows that share an adapter to a workgroup: 1 row of 4096
-// columns, rank 16, 6.5 us, one compute unit's loads; 64 rows of 8192 on adapters of
-// their own, rank 32, 14.2; 64 on 3 of rank 64, 4096 columns, 7.9.)
+// The rows' coordinates, a wave to each row and rank: few rows spread over as many
+// compute units as they have ranks, each wave requests up to 8 KiB of the factor before
+// it uses any, and rows that share an adapter read it from the L2. (On the matrix cores,
+// 16 ranks and the rows that share an adapter to a workgroup: 1 row of 4096 columns, rank
+// 16, 6.5 us, one compute unit's loads, against 3.5; 64 rows of 8192 on adapters of their
+// own, rank 32, 14.2 against 10.7; 64 on 3 of rank 64, 4096 columns, 7.9 against 6.1.
+// Four ranks a wave, which reads the hidden state once for them, were up to 2 us slower.)
 __global__ void __launch_bounds__(256) down_kernel(Args a, int steps) {
   const int lane = lane_id();
   const int item = uni((int)(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)));
@@ -113,10 +115,15 @@ __global__ void __launch_bounds__(256) down_kernel(Args a, int steps) {
 }
 
 // The logits. A wave takes kTiles tiles of 16 vocabulary rows and up to RT tiles of 16
-// batch rows: the logits are its accumulators, and it walks the block's adapters. The
-// tiles' rows are dealt out so that a lane holds 4 kTiles consecutive logits of one
-// batch row: product row 4 g + e of tile t is vocabulary row 4 (kTiles g + t) + e.
-template <int DT, int KS, int RT>
+// batch rows: the logits are its accumulators, and it walks the block's adapters, A at a
+// time (2 where their rows are so short, up to rank 16, that one's are too few bytes under
+// way: 64 rows of 151936 on adapters of rank 16 of their own 69 us against 77; of rank 32
+// 130 against 126, of 64 102 against 100). Two tiles leave room for more waves than four
+// (64 rows on 16 adapters of rank 128: 147 us against 172; on 4 of rank 16, float32, 24.5
+// against 33). The tiles' rows are dealt out so that a lane holds 4 kTiles consecutive
+// logits of one batch row: product row 4 g + e of tile t is vocabulary row
+// 4 (kTiles g + t) + e.
+template <int DT, int KS, int RT, int A>
 __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
   constexpr int kSpan = 16 * kTiles;      // vocabulary rows per wave
   constexpr int P = DT == QS_F32 ? 4 : 8; // logits per 16 bytes
@@ -162,44 +169,55 @@ __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
   if (tile >= tiles) return;
 
   for (uint64_t left = adapted; left != 0u;) {
-    const int d = readlane_u32((uint32_t)mine, __builtin_ctzll(left));
-    const uint64_t members = ballot(mine == d);
-    left &= ~members;
-    const uint16_t* const up = a.up + (size_t)d * a.up_stride;
-    bf16x8 f[kTiles][KS];
+    int d[A];
+    uint64_t members[A];
+    bf16x8 f[A][kTiles][KS];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int v = min(v0 + (n >> 2) * 4 * kTiles + i * 4 + (n & 3), a.V - 1);
-      const uint16_t* const row = up + (size_t)v * a.up_row_stride;
+    for (int j = 0; j < A; ++j) {
+      d[j] = -1;
+      members[j] = 0u;
+      if (left == 0u) continue;
+      d[j] = readlane_u32((uint32_t)mine, __builtin_ctzll(left));
+      members[j] = ballot(mine == d[j]);
+      left &= ~members[j];
+      const uint16_t* const up = a.up + (size_t)d[j] * a.up_stride;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (s * 32 + kg * 8 < a.rank) q = *reinterpret_cast<const uint4*>(row + s * 32 + kg * 8);
-        f[i][s] = __builtin_bit_cast(bf16x8, q);
+      for (int i = 0; i < kTiles; ++i) {
+        const int v = min(v0 + (n >> 2) * 4 * kTiles + i * 4 + (n & 3), a.V - 1);
+        const uint16_t* const row = up + (size_t)v * a.up_row_stride;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint4 q = make_uint4(0u, 0u, 0u, 0u);
+          if (s * 32 + kg * 8 < a.rank) q = *reinterpret_cast<const uint4*>(row + s * 32 + kg * 8);
+          f[j][i][s] = __builtin_bit_cast(bf16x8, q);
+        }
       }
     }
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      if (((members >> (t * 16)) & 0xFFFFu) == 0u) continue;
-      f32x4 acc[kTiles];
+    for (int j = 0; j < A; ++j) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) acc[i] = y[i][t];
+      for (int t = 0; t < RT; ++t) {
+        if (((members[j] >> (t * 16)) & 0xFFFFu) == 0u) continue;
+        f32x4 acc[kTiles];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
+        for (int i = 0; i < kTiles; ++i) acc[i] = y[i][t];
 #pragma unroll
-        for (int k = 0; k < kTerms; ++k) {
-          const bf16x8 u =
-              __builtin_bit_cast(bf16x8, s_low[((t * KS + s) * kTerms + k) * 64 + lane]);
+        for (int s = 0; s < KS; ++s) {
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[i][s], u, acc[i], 0, 0, 0);
+          for (int k = 0; k < kTerms; ++k) {
+            const bf16x8 u =
+                __builtin_bit_cast(bf16x8, s_low[((t * KS + s) * kTerms + k) * 64 + lane]);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][i][s], u, acc[i], 0, 0, 0);
+          }
         }
-      }
-      const bool take = own[t] == d;
+        const bool take = own[t] == d[j];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
+        for (int i = 0; i < kTiles; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[i][t][e] = take ? acc[i][e] : y[i][t][e];
+          for (int e = 0; e < 4; ++e) y[i][t][e] = take ? acc[i][e] : y[i][t][e];
+        }
       }
     }
   }
@@ -241,23 +259,24 @@ __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
   }
 }
 
-template <int DT, int KS>
+template <int DT, int KS, int A>
 void launch_up(const Args& a, hipStream_t st) {
   const int tiles = (a.V + 16 * kTiles - 1) / (16 * kTiles);
   const dim3 grid((unsigned)((tiles + kUpWaves - 1) / kUpWaves),
                   (unsigned)((a.B + kRows - 1) / kRows));
   const dim3 block(kUpWaves * 64);
-  if (a.B <= 16) hipLaunchKernelGGL((up_kernel<DT, KS, 1>), grid, block, 0, st, a, tiles);
-  else if (a.B <= 32) hipLaunchKernelGGL((up_kernel<DT, KS, 2>), grid, block, 0, st, a, tiles);
-  else hipLaunchKernelGGL((up_kernel<DT, KS, 4>), grid, block, 0, st, a, tiles);
+  if (a.B <= 16) hipLaunchKernelGGL((up_kernel<DT, KS, 1, A>), grid, block, 0, st, a, tiles);
+  else if (a.B <= 32) hipLaunchKernelGGL((up_kernel<DT, KS, 2, A>), grid, block, 0, st, a, tiles);
+  else hipLaunchKernelGGL((up_kernel<DT, KS, 4, A>), grid, block, 0, st, a, tiles);
 }
 
 template <int DT>
 void launch_rank(const Args& a, int steps, hipStream_t st) {
-  if (steps == 1) launch_up<DT, 1>(a, st);
-  else if (steps == 2) launch_up<DT, 2>(a, st);
-  else if (steps == 3) launch_up<DT, 3>(a, st);
-  else launch_up<DT, 4>(a, st);
+  if (a.rank <= 16) launch_up<DT, 1, 2>(a, st);
+  else if (steps == 1) launch_up<DT, 1, 1>(a, st);
+  else if (steps == 2) launch_up<DT, 2, 1>(a, st);
+  else if (steps == 3) launch_up<DT, 3, 1>(a, st);
+  else launch_up<DT, 4, 1>(a, st);
 }
 
 int steps_of(int64_t rank) { return (int)((rank + 31) / 32); }
@@ -270,8 +289,8 @@ size_t workspace_bytes(int64_t B, int64_t rank) {
 
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
   const int steps = steps_of(a.rank);
-  // one wave a workgroup where that spreads few waves over more compute units
   const int64_t items = (int64_t)a.B * steps * 32;
+  // one wave a workgroup where that spreads few waves over more compute units
   const int waves = items > 1024 ? 4 : 1;
   hipLaunchKernelGGL(down_kernel, dim3((unsigned)((items + waves - 1) / waves)), dim3(waves * 64), 0,
                      st, a, steps);
