@@ -171,21 +171,25 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid,
   // sums over the list: student's weights (below the maximum, and how many are at
   // it), teacher's weights likewise, and teacher's weight times log q - log p but
   // for the two normalisers
+  const double inv_T = 1.0 / T;
   double sum[5] = {0.0, 0.0, 0.0, 0.0, 0.0};
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (!((s.live >> i) & 1u)) continue;
-    const double d = ((double)s.z[i] - (double)m) / T;
-    const double tau = a.rest ? (double)s.t[i] : ((double)s.t[i] - (double)tmax) / T;
+    if (i * THREADS >= a.K) continue;
+    const bool live = (s.live >> i) & 1u;
+    const bool at_m = live && s.z[i] == m, at_t = live && !a.rest && s.t[i] == tmax;
+    sum[1] += __popcll(ballot(at_m));
+    sum[3] += __popcll(ballot(at_t));
+    if (!live) continue;
+    const double d = ((double)s.z[i] - (double)m) * inv_T;
+    const double tau = a.rest ? (double)s.t[i] : ((double)s.t[i] - (double)tmax) * inv_T;
     const double wt = exp(tau);
-    if (s.z[i] == m) sum[1] += 1.0;
-    else sum[0] += exp(d);
-    if (!a.rest && s.t[i] == tmax) sum[3] += 1.0;
-    else sum[2] += wt;
+    if (!at_m) sum[0] += exp(d);
+    if (!at_t) sum[2] += wt;
     if (wt > 0.0) sum[4] += wt * (tau - d);
   }
 #pragma unroll
-  for (int k = 0; k < 5; ++k) sum[k] = wave_sum_f64(sum[k]);
+  for (int k = 0; k < 5; k += 2) sum[k] = wave_sum_f64(sum[k]);
   if constexpr (kWavesHere > 1) {
     if (lane == 0) {
 #pragma unroll
@@ -206,7 +210,7 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid,
   // one token is almost certain), 1 the rest's sum, 2 the teacher's sum likewise,
   // 3 q_R = 2^n (1 + x).
   const double below = sum[0], at = sum[1], cross = sum[4];
-  const double dr = has ? ((double)rest.m - (double)m) / T : 0.0;
+  const double dr = has ? ((double)rest.m - (double)m) * inv_T : 0.0;
   const double f = has ? exp(dr) * (double)rest.S : 0.0;
   const double others = at > 0.0 ? below + (at - 1.0) + f : below + (f - 1.0);
   const double W = sum[2] + sum[3];
