@@ -12,7 +12,7 @@ from ._lib import _check_logits, _status, load
 from ._scoring import _addr, _check_out, _check_vec, _code, _enqueue, _refuse_tangents, _wrote
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _workspace_bytes(B, rank):
     # a pure function of its arguments, asked once for each
     return load().qs_adapters_workspace_bytes(B, rank)

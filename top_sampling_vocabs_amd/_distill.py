@@ -36,7 +36,7 @@ def _check_inputs(logits, teacher_ids, teacher_values, temperature, bitmask):
     return B, V, teacher_ids.size(1), index
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _workspace_bytes(B, V, code):
     # a pure function of its arguments, asked once for each
     return load().qs_distill_loss_workspace_bytes(B, V, code)

@@ -17,7 +17,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
 #include <type_traits>
 
 #include "../../include/qs.h"
@@ -32,8 +31,12 @@ namespace {
 using namespace score;
 
 constexpr int kPartBlock = 256;   // threads of a part's workgroup
-constexpr int kPartLoads = 16;    // 16-byte loads per lane
-constexpr int kShortLoads = 8;    // the same where parts are few
+// 16-byte loads per lane of a part. Few parts are short, so that they fill the chip
+// (1 row of 151936 bf16: 7.2 us with 4 loads, 8.3 with 8, 9.7 with 16; 32 rows 9.0, 9.6
+// and 10.1); many unmasked bf16 rows are cut into long ones (2048 rows of 151936: 110 us
+// with 16, 113 with 8, 117 with 4), whose exponentials are enough to hide their start;
+// masked and fp32 ones are not (2048 masked rows of 100003: 80 with 8, 84 with 16).
+constexpr int kShortLoads = 4, kPartLoads = 8, kLongLoads = 16;
 constexpr int kRowBlock = 1024;   // threads of a whole row's workgroup
 constexpr int kRowLoads = 8;
 constexpr int kSmallBlock = 256;  // threads of a short row's workgroup
@@ -50,19 +53,18 @@ struct Part {
 };
 static_assert(sizeof(Part) == 16, "one 16-byte store");
 
-// Loads per lane of a part: the long parts' workgroups are more than kFewParts
-// (eight per compute unit), or else the row is cut into twice as many.
-constexpr int64_t kFewParts = 2048;
+constexpr int64_t kFewParts = 2048, kManyParts = 4096;  // of kPartLoads loads
 int64_t parts_of(int64_t V, int dtype, int loads) {
   const int64_t n = (int64_t)(dtype == QS_F32 ? 4 : 8) * kPartBlock * loads;
   return (V + n - 1) / n;
 }
-int loads_for(int64_t B, int64_t V, int dtype) {
-  return B * parts_of(V, dtype, kPartLoads) > kFewParts ? kPartLoads : kShortLoads;
+bool one_part(int64_t V, int dtype) {
+  return V <= (int64_t)(dtype == QS_F32 ? 4 : 8) * kRowBlock * kRowLoads;
 }
-int64_t parts_for(int64_t B, int64_t V, int dtype) {
-  if (V <= (int64_t)(dtype == QS_F32 ? 4 : 8) * kRowBlock * kRowLoads) return 1;
-  return parts_of(V, dtype, loads_for(B, V, dtype));
+int loads_for(int64_t B, int64_t V, int dtype, bool mask) {
+  const int64_t n = B * parts_of(V, dtype, kPartLoads);
+  return n <= kFewParts ? kShortLoads
+         : n > kManyParts && dtype == QS_BF16 && !mask ? kLongLoads : kPartLoads;
 }
 
 constexpr uint32_t kBadSlot = 1u, kNonfinite = 2u;
@@ -88,15 +90,23 @@ struct Slots {
       }
     }
   }
-  __device__ __forceinline__ void load(const Args& a, int r, int tid) {
+  // the teacher's values
+  __device__ __forceinline__ void load_values(const Args& a, int r, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      t[i] = -INFINITY;
+      if (id[i] >= 0) t[i] = a.values[(size_t)r * a.K + i * THREADS + tid];
+    }
+  }
+  // the students' logits, and which tokens are legal
+  __device__ __forceinline__ void load_logits(const Args& a, int r, int tid) {
     const uint8_t* const row = a.logits + (size_t)r * a.row_bytes;
     const uint32_t* const mask = a.bitmask ? a.bitmask + (size_t)r * a.bm_stride : nullptr;
     live = 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      z[i] = t[i] = -INFINITY;
+      z[i] = -INFINITY;
       if (id[i] < 0) continue;
-      t[i] = a.values[(size_t)r * a.K + i * THREADS + tid];
       z[i] = logit_at<DT>(row, id[i]);
       if (!mask || ((mask[id[i] >> 5] >> (id[i] & 31)) & 1u)) live |= 1u << i;
     }
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(THREADS)
         dup |= atomicOr(&s_named[d >> 5], bit) & bit;
       }
     }
-    if constexpr (ROW) slots.load(a, r, tid);
+    if constexpr (ROW) slots.load_values(a, r, tid);
   }
   __syncthreads();
 
@@ -351,6 +361,12 @@ __global__ void __launch_bounds__(THREADS)
       for (int e = 0; e < P; ++e) S[e & 1] += exp2_hw((token<DT>(v[u], e) - wave_max) * c);
     }
   }
+  // the named tokens' logits, now that the row's cache lines are here (requested beside
+  // them they are a line apiece more to fetch: 4096 rows of 32000 bf16 with 64 tokens
+  // each 104 us against 99)
+  if constexpr (ROW) {
+    if (finisher) slots.load_logits(a, r, tid);
+  }
   const float Sw = wave_sum_f32(S[0] + S[1]);
   const bool anyw = ballot(any != 0u) != 0, dupw = ballot(dup != 0u) != 0;
   if (lane == 0) {
@@ -388,7 +404,8 @@ __global__ void __launch_bounds__(THREADS)
   slots.load_ids(a, r, tid);
   Part mine{kLowest, 0.0f, 0u, 0u};
   if (lane < parts) mine = p[lane];
-  slots.load(a, r, tid);
+  slots.load_values(a, r, tid);
+  slots.load_logits(a, r, tid);
   const float c = scale_of(a.T ? a.T[r] : 1.0f);
   // every wave joins all parts (the same values in every thread)
   float m = mine.m;
@@ -417,10 +434,10 @@ void launch(const Args& a, int blocks, int parts, int part_loads, Part* wp, hipS
 }
 
 template <int DT>
-hipError_t launch_dt(const Args& a, int B, int parts, Part* wp, hipStream_t st) {
+hipError_t launch_dt(const Args& a, int B, Part* wp, hipStream_t st) {
   constexpr int P = kPer<DT>;
   const bool few = a.K <= 64 * kJoinSlots;  // slots that one wave holds
-  if (parts == 1) {
+  if (one_part(a.V, DT)) {
     auto run = [&](auto threads, auto loads) {
       constexpr int TH = decltype(threads)::value, NL = decltype(loads)::value;
       const int each = (a.V + TH * P - 1) / (TH * P);
@@ -434,12 +451,17 @@ hipError_t launch_dt(const Args& a, int B, int parts, Part* wp, hipStream_t st) 
     return hipGetLastError();
   }
   // parts of equal length, in whole loads
+  const int most = loads_for(B, a.V, DT, a.bitmask != nullptr);
+  const int parts = (int)parts_of(a.V, DT, most);
   const int loads = (a.V + kPartBlock * P - 1) / (kPartBlock * P);
   const int each = (loads + parts - 1) / parts;
-  if (loads_for(B, a.V, DT) == kPartLoads)
-    launch<DT, kPartBlock, kPartLoads, false, kPartBlock>(a, B * parts, parts, each, wp, st);
-  else
-    launch<DT, kPartBlock, kShortLoads, false, kPartBlock>(a, B * parts, parts, each, wp, st);
+  auto run = [&](auto nl) {
+    launch<DT, kPartBlock, decltype(nl)::value, false, kPartBlock>(a, B * parts, parts, each, wp,
+                                                                  st);
+  };
+  if (most == kShortLoads) run(std::integral_constant<int, kShortLoads>());
+  else if (most == kPartLoads) run(std::integral_constant<int, kPartLoads>());
+  else run(std::integral_constant<int, kLongLoads>());
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (few)
     hipLaunchKernelGGL((distill_join_kernel<DT, 64>), dim3((unsigned)B), dim3(64), 0, st, a, parts,
@@ -452,27 +474,25 @@ hipError_t launch_dt(const Args& a, int B, int parts, Part* wp, hipStream_t st) 
 
 }  // namespace
 
-// Enough for every batch of at most B rows: the largest of them whose parts are
-// short has up to twice the parts of a somewhat larger one whose parts are long.
+// Enough for every batch of at most B rows: the largest of them whose parts are short
+// has up to twice the parts of a somewhat larger one whose parts are longer.
 size_t workspace_bytes(int64_t B, int64_t V, int dtype) {
-  const int64_t parts = parts_for(B, V, dtype);
-  if (parts == 1) return 0;
-  const int64_t few = kFewParts / parts_of(V, dtype, kPartLoads);  // rows of the last such batch
-  size_t n = (size_t)B * parts;
-  if (B > few) n = std::max(n, (size_t)few * parts_of(V, dtype, kShortLoads));
-  return (n * sizeof(Part) + 255) & ~(size_t)255;
+  if (one_part(V, dtype)) return 0;
+  const int64_t per_row = parts_of(V, dtype, kPartLoads);
+  const int64_t few = kFewParts / per_row;  // rows of the last batch of short parts
+  int64_t n = B * per_row, short_parts = (B < few ? B : few) * parts_of(V, dtype, kShortLoads);
+  if (n < short_parts) n = short_parts;
+  return ((size_t)n * sizeof(Part) + 255) & ~(size_t)255;
 }
 
 bool grid_fits(int64_t B, int64_t V, int dtype) {
-  const int64_t parts = parts_for(B, V, dtype);
-  return B * parts * (parts == 1 ? kRowBlock : kPartBlock) < (int64_t)1 << 32;
+  if (one_part(V, dtype)) return B * kRowBlock < (int64_t)1 << 32;
+  return B * parts_of(V, dtype, kPartLoads) * kPartBlock < (int64_t)1 << 32;
 }
 
 hipError_t launch_loss(const Args& a, int dtype, int B, void* workspace, hipStream_t st) {
-  const int parts = (int)parts_for(B, a.V, dtype);
   Part* const wp = static_cast<Part*>(workspace);
-  return dtype == QS_F32 ? launch_dt<QS_F32>(a, B, parts, wp, st)
-                         : launch_dt<QS_BF16>(a, B, parts, wp, st);
+  return dtype == QS_F32 ? launch_dt<QS_F32>(a, B, wp, st) : launch_dt<QS_BF16>(a, B, wp, st);
 }
 
 }  // namespace distill
