@@ -211,12 +211,56 @@ def test_rows_do_not_meet(qs, dtype):
 
 
 def test_same_bits(qs):
-    """Twice the same call; a row's bits whatever rows are beside it in its place."""
+    """Twice the same call; and a row's bits whatever rows are beside it, how many there
+    are, and where it stands among them."""
     import torch
-    z, x, down, up, scale, index = inputs(8, 64, 2001, 256, 32, 12)
-    a, _ = run(qs, z, "f32", x, down, up, scale, index)
-    b, _ = run(qs, z, "f32", x, down, up, scale, index)
-    assert torch.equal(a, b)
+    for rank in (8, 32, 72):
+        z, x, down, up, scale, index = inputs(8, 130, 2001, 256, rank, 12)
+        a, _ = run(qs, z, "f32", x, down, up, scale, index)
+        b, _ = run(qs, z, "f32", x, down, up, scale, index)
+        assert torch.equal(a, b)
+        for rows in ([5], [77, 3], list(range(20, 40)), list(range(129, 80, -1))):
+            few, _ = run(qs, z[rows], "f32", x[rows], down, up, scale, index[rows])
+            assert torch.equal(few, a[rows]), (rank, rows)
+
+
+def test_inference_mode(qs):
+    import torch
+    with torch.inference_mode():
+        z, x, down, up, scale, index = inputs(8, 5, 300, 64, 8, 3)
+        got, status = run(qs, z, "bf16", x, down, up, scale, index)
+        assert not status.any()
+    check(z, "bf16", x, down, up, scale, index, got)
+
+
+def test_most_rows(qs):
+    """The largest batch, 2^18 rows on two adapters, some rows without: a tile of 16
+    batch rows at the end of each block of 64, and every row against float64."""
+    import torch
+    B, V, K, rank = 1 << 18, 24, 16, 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.randn(B, V, generator=g, device="cuda")
+    x = torch.randn(B, K, generator=g, device="cuda").bfloat16()
+    down = torch.randn(2, rank, K, generator=g, device="cuda").bfloat16()
+    up = (torch.randn(2, V, rank, generator=g, device="cuda") / 16).bfloat16()
+    index = torch.randint(-1, 2, (B,), generator=g, device="cuda", dtype=torch.int32)
+    out = torch.empty_like(z)
+    status = qs.apply_adapters(z, x, down, up, index, out=out)
+    assert not status.any()
+    want = z.double()
+    size, sums = torch.zeros_like(want), torch.zeros_like(want)
+    for a in range(2):
+        on = (index == a)[:, None]
+        u = x.double() @ down[a].double().t()
+        w = up[a].double()
+        want = torch.where(on, want + u @ w.t(), want)
+        size = torch.where(on, u.abs() @ w.abs().t(), size)
+        # the products that a coordinate is a sum of
+        sums = torch.where(on, (x.double().abs() @ down[a].double().abs().t()) @ w.abs().t(), sums)
+    tol = U * ((K / 16 + 17) * sums + (rank + 6) * (size + z.abs()) + 2 * want.abs()) \
+        + 2.0 ** -16 * size
+    assert bool(((out - want).abs() <= tol).all())
+    assert torch.equal(out[index < 0], z[index < 0])
 
 
 def test_refusals(qs):

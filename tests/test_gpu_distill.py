@@ -61,7 +61,8 @@ def teacher(rng, z, legal, T, K, rest, pad=True):
             tok, slots, v = tok[~gone], slots[~gone], v[~gone]
             v = np.where(rng.random(v.size) < 0.1, -np.inf, v)
         ids[r, slots] = tok
-        values[r, slots] = v
+        with np.errstate(over="ignore"):
+            values[r, slots] = v
     return ids, values
 
 
@@ -203,6 +204,24 @@ def test_row_errors(qs, V, dtype, rest):
     values[25] = -np.inf                   # a teacher without any weight
     _, _, _, out = run(qs, z, dtype, ids, values, T, legal, rest)
     check(z, ids, values, T, legal, rest, out)
+
+
+def test_illegal_slots_count_as_empty(qs):
+    """What a slot of an illegal token holds is not read, nor what an empty one holds;
+    the gradient does not reach them."""
+    z = make(11, 4, 5003, "normal")
+    legal = np.random.default_rng(11).random((4, 5003)) < 0.5
+    legal[:, :4] = [True, False, True, False]
+    ids = np.tile(np.array([0, 1, 2, 3, -1], np.int32), (4, 1))
+    for bad in (np.nan, np.inf, -np.inf, 50.0):
+        for rest in (False, True):
+            values = np.array([[-1.0, bad, -2.0, bad, bad]] * 4, np.float32)
+            none = np.where(np.isin(ids, (1, 3)), -1, ids).astype(np.int32)
+            _, a = check_grad(qs, z, "f32", ids, values, None, legal, rest, np.ones(4, np.float32))
+            _, _, _, out = run(qs, z, "f32", ids, values, None, legal, rest)
+            check(z, ids, values, None, legal, rest, out)
+            _, _, _, same = run(qs, z, "f32", none, values, None, legal, rest)
+            assert all((out[k] == same[k]).all() for k in out)
 
 
 @pytest.mark.parametrize("rest", [False, True])
@@ -392,6 +411,30 @@ def test_grad_long_lists(qs, K, dtype):
         g = rng.normal(0, 1, 4).astype(np.float32)
         for rest in (False, True):
             check_grad(qs, z, dtype, ids, values, None, None, rest, g)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3001, 40003])
+def test_grad_temperatures_and_large_logits(qs, V, dtype, rest):
+    """Every power of ten that a temperature can be; logits up to 1e37 as they are and at
+    temperatures of their own size; incoming gradients up to the largest."""
+    print(f"distill grad temperatures V={V} {dtype} rest={rest}", flush=True)
+    T = np.repeat(10.0 ** np.arange(-37, 39), 3).astype(np.float32)
+    B = T.size
+    rng = np.random.default_rng(V)
+    z, legal = gap_rows(V, B, V)
+    ids, values = teacher(rng, z, legal, T, 6, rest)
+    g = rng.normal(0, 1, B).astype(np.float32)
+    check_grad(qs, z, dtype, ids, values, T, legal, rest, g)
+    e = np.repeat(np.arange(0, 37), 2)
+    B = e.size
+    z, legal = gap_rows(V, B, V)
+    ids, values = teacher(rng, z, legal, None, 6, rest)
+    z = bf16(z * (10.0 ** e)[:, None])
+    T = np.where(np.arange(B) % 2 == 0, 1.0, 10.0 ** e).astype(np.float32)
+    g = np.where(np.arange(B) % 4 < 2, 1.0, 3e38).astype(np.float32)
+    check_grad(qs, z, dtype, ids, values, T, legal, rest, g)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -634,13 +677,69 @@ def test_refusals(qs):
 
 def test_empty_batch(qs):
     import torch
-    lg = torch.empty(0, 64, device="cuda")
-    ids = torch.empty(0, 4, dtype=torch.int32, device="cuda")
-    out = qs.distill_loss(lg, ids, torch.empty(0, 4, device="cuda"))
-    assert out["loss"].shape == (0,) and out["state"].shape == (0, 8)
-    grad = qs.distill_loss_backward(lg, ids, torch.empty(0, 4, device="cuda"), out["state"],
-                                    out["status"], torch.empty(0, device="cuda"))
-    assert grad.shape == (0, 64)
+    for V in (64, 70016):
+        lg = torch.empty(0, V, device="cuda")
+        ids = torch.empty(0, 4, dtype=torch.int32, device="cuda")
+        val = torch.empty(0, 4, device="cuda")
+        assert qs.distill_loss_workspace_for(lg) is None
+        out = qs.distill_loss(lg, ids, val)
+        assert out["loss"].shape == (0,) and out["state"].shape == (0, 8)
+        grad = qs.distill_loss_backward(lg, ids, val, out["state"], out["status"],
+                                        torch.empty(0, device="cuda"))
+        assert grad.shape == (0, V)
+        leaf = lg.clone().requires_grad_()
+        qs.distill_loss(leaf, ids, val)["loss"].sum().backward()
+        assert leaf.grad.shape == (0, V)
+
+
+def test_most_rows(qs):
+    """The largest batch, 2^22 - 1 rows of 7 tokens, two of them listed. Five terms of S_R,
+    so e_S is at most 32 units; a loss is at most 60 or so, a gradient element at most 1."""
+    import torch
+    B, V = (1 << 22) - 1, 7
+    torch.manual_seed(3)
+    z = torch.randn(B, 8, device="cuda").mul_(3).bfloat16()[:, :V]
+    ids = torch.tensor([[4, 1]], dtype=torch.int32, device="cuda").expand(B, 2).contiguous()
+    q = torch.rand(B, 2, device="cuda") * 0.45 + 0.01
+    out = qs.distill_loss(z, ids, q.log(), rest=True)
+    assert not out["status"].any()
+    lp = torch.log_softmax(z.double(), 1)
+    at = ids.long()
+    # the probabilities that the float32 logarithms stand for
+    q = q.log().double().exp()
+    others = torch.tensor([0, 2, 3, 5, 6], device="cuda")
+    lr, qr = torch.logsumexp(lp[:, others], 1), 1 - q.sum(1)
+    want = (q * (q.log() - lp.gather(1, at))).sum(1) + qr * (qr.log() - lr)
+    assert bool(((out["loss"] - want).abs() <= U * (32 + 2 * want.abs())).all())
+    grad = qs.distill_loss_backward(z, ids, q.log().float(), out["state"], out["status"],
+                                    torch.ones(B, device="cuda"), rest=True)
+    want = (lp - lr[:, None]).exp() * (lr.exp() - qr)[:, None]
+    want.scatter_(1, at, lp.gather(1, at).exp() - q)
+    # log p of up to 30 from a state rounded to float32
+    assert bool(((grad - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + 128 * U).all())
+
+
+def test_writes_and_inference_mode(qs):
+    """The gradient written over a buffer counts as a change of it; tensors of inference
+    mode are taken."""
+    import torch
+    B, V = 4, 512
+    ids = torch.tensor([[1, 5, -1]] * B, dtype=torch.int32, device="cuda")
+    val = torch.rand(B, 3, device="cuda").log()
+    g = torch.ones(B, device="cuda")
+    z = torch.randn(B, V, device="cuda").requires_grad_()
+    kept = z.detach()
+    o = qs.distill_loss(kept, ids, val)
+    loss = qs.distill_loss(z, ids, val)["loss"]
+    qs.distill_loss_backward(kept, ids, val, o["state"], o["status"], g, out=kept)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+    with torch.inference_mode():
+        x = torch.randn(B, V, device="cuda")
+        o = qs.distill_loss(x, ids, val, rest=True)
+        qs.distill_loss_backward(x, ids, val, o["state"], o["status"], g, rest=True, out=x)
+    torch.cuda.synchronize()
+    assert not o["status"].any()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

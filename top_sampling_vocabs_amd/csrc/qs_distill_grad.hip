@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kBlock) distill_grad_kernel(GradArgs a, int ch
   const float c = scale_of(T), lsr2 = state[3] * kLog2e;
   // finite where g is, so that a token of no weight gets 0; an infinite or NaN g goes
   // through to every legal token
-  float coef = g * rest_grad / T;
+  float coef = (float)((double)g * (double)rest_grad / (double)T);
   if (fabsf(g) < INFINITY) coef = fminf(fmaxf(coef, -3e38f), 3e38f);
 
 #pragma unroll
