@@ -71,7 +71,9 @@ def parse():
                     help="instead of the headline line, time a decode step of B rows from "
                          "hidden states (V=151936, K=4096, 4-bit output head): head, "
                          "selection, log-probabilities of the drawn tokens with 20 "
-                         "alternatives, and the gradient a training step adds")
+                         "alternatives, and the gradient a training step adds; low-rank "
+                         "adapters of the rows beside the head, and distillation from the "
+                         "20 alternatives with its gradient, are timed beside it")
     ap.add_argument("--ablation", action="store_true",
                     help="instead of the headline line, print one line timing the path "
                          "switches (the Qrita page's ablation runs) on the headline "
@@ -543,10 +545,13 @@ def toplp_bench(args, lib, stream):
 
 def hidden_bench(args):
     """A decode step from hidden states, and the scores' gradient, as one graph of
-    K steps over rotating weights and as each call alone."""
+    K steps over rotating weights and as each call alone; beside them the rows' low-rank
+    adapters (8 of rank 16, a row each in turn) and distillation from the step's own
+    alternatives, forward and backward."""
     import torch
     import top_sampling_vocabs_amd as qs
     B, V, K, group, top_n = args.hidden, 151936, 4096, 128, 20
+    held, rank = 8, 16
     gen = torch.Generator(device="cuda").manual_seed(workloads.BASE_SEED)
     full = lambda v, d: torch.full((B,), v, dtype=d, device="cuda")  # noqa: E731
 
@@ -563,8 +568,14 @@ def hidden_bench(args):
             self.offset = torch.zeros(B, dtype=torch.int64, device="cuda")
             self.g = full(1.0 / B, torch.float32)
             self.logits = torch.empty(B, V, dtype=torch.bfloat16, device="cuda")
-            self.part = "all"
-            self.call()
+            self.moved = torch.empty_like(self.logits)
+            self.down = (torch.randn(held, rank, K, device="cuda", generator=gen)
+                         / K ** 0.5).bfloat16()
+            self.up = (torch.randn(held, V, rank, device="cuda", generator=gen)
+                       / rank ** 0.5).bfloat16()
+            self.index = (torch.arange(B, device="cuda") % held).to(torch.int32)
+            for self.part in ("all", "adapters", "distill"):
+                self.call()
 
         def call(self, stream=None, flags=None):
             part = self.part
@@ -581,10 +592,21 @@ def hidden_bench(args):
                 self.grad = qs.token_logprobs_backward(
                     self.logits, self.tokens, out["row_max"], out["log_sum"], out["status"],
                     self.g, temperature=self.T)
+            if part == "adapters":
+                qs.apply_adapters(self.logits, self.x, self.down, self.up, self.index,
+                                  out=self.moved)
+            if part == "distill":
+                self.loss = qs.distill_loss(self.moved, self.out["top_ids"],
+                                            self.out["top_logprobs"], temperature=self.T, rest=True)
+            if part == "distill_gradient":
+                self.grad = qs.distill_loss_backward(
+                    self.moved, self.out["top_ids"], self.out["top_logprobs"], self.loss["state"],
+                    self.loss["status"], self.g, temperature=self.T, rest=True)
 
     steps = [Step() for _ in range(args.sets)]
     ms = {}
-    for part in ("head", "sample", "score", "gradient", "step", "all"):
+    for part in ("head", "sample", "score", "gradient", "step", "all", "adapters", "distill",
+                 "distill_gradient"):
         for s in steps:
             s.part = part
         for i in range(args.warmup):
@@ -594,6 +616,7 @@ def hidden_bench(args):
         ms[part] = t / args.steps
         for s in steps:
             assert bool((s.out["status"] == 0).all()) and bool((s.tokens >= 0).all())
+            assert bool((s.loss["status"] == 0).all()) and bool((s.loss["loss"] >= 0).all())
         del graph
     weights = V * (K // 2 + 2 * (K // group))
     nbytes = weights + 2 * B * K + 3 * 2 * B * V  # weights, x; logits written, read twice
@@ -607,7 +630,11 @@ def hidden_bench(args):
                                f"log-probabilities with {top_n} alternatives",
                    "head_ms": round(ms["head"], 5), "sample_ms": round(ms["sample"], 5),
                    "score_ms": round(ms["score"], 5), "gradient_ms": round(ms["gradient"], 5),
-                   "step_and_gradient_ms": round(ms["all"], 5), "launch": "graph"},
+                   "step_and_gradient_ms": round(ms["all"], 5),
+                   "adapters": f"{min(B, held)} of rank {rank}",
+                   "adapters_ms": round(ms["adapters"], 5),
+                   "distill_ms": round(ms["distill"], 5),
+                   "distill_gradient_ms": round(ms["distill_gradient"], 5), "launch": "graph"},
         "roofline": {"bound": "hbm", "achieved": round(nbytes / (per * 1e-3) / 1e9, 1),
                      "peak": HBM_PEAK_GBS, "unit": "GB/s",
                      "frac": round(nbytes / (per * 1e-3) / 1e9 / HBM_PEAK_GBS, 5),
