@@ -36,6 +36,7 @@ constexpr int kRows = 64;         // batch rows of a block
 constexpr int kTerms = 3;         // bf16 numbers per coordinate
 constexpr int kUpWaves = 4;
 constexpr int kTiles = 2;         // tiles of 16 vocabulary rows per wave
+constexpr int kWavesWanted = 4096;  // up to which a block's adapters are dealt out
 constexpr int kAhead = 8;         // loads of 512 columns that a wave of the first product
                                   // requests at a time
 
@@ -123,20 +124,44 @@ __global__ void __launch_bounds__(256) down_kernel(Args a, int steps) {
 // against 33). The tiles' rows are dealt out so that a lane holds 4 kTiles consecutive
 // logits of one batch row: product row 4 g + e of tile t is vocabulary row
 // 4 (kTiles g + t) + e.
+//
+// A wave that walks many adapters waits for each one's factors, so where the vocabulary
+// makes few waves a block's adapters are dealt out to up to 64 groups of workgroups, each
+// with the rows of its own (64 rows on adapters of their own of rank 16: 1000 tokens 7.0
+// us against 26.6, 8000 10.8 against 32, 32000 20.7 against 34, 64000 31 against 37; past
+// kWavesWanted, 128256 in two groups, 62 against 57. 3 adapters of rank 64: 9.9 against
+// 12.0, 10.1 against 12.1, 11.7 against 12.7, 15.3 against 15.8 and, past it, 24.5 against
+// 21.0).
 template <int DT, int KS, int RT, int A>
-__global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
+__global__ void __launch_bounds__(kUpWaves * 64)
+    up_kernel(Args a, int tiles, int groups_log2, uint64_t every) {
   constexpr int kSpan = 16 * kTiles;      // vocabulary rows per wave
   constexpr int P = DT == QS_F32 ? 4 : 8; // logits per 16 bytes
   __shared__ uint4 s_low[RT * KS * kTerms * 64];
   const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
   const int n = lane & 15, kg = lane >> 4;
-  const int row0 = (int)blockIdx.y * kRows;
+  const int group = (int)blockIdx.y & ((1 << groups_log2) - 1);
+  const int row0 = ((int)blockIdx.y >> groups_log2) * kRows;
   const int tile = (int)blockIdx.x * kUpWaves + w;
   const int v0 = tile * kSpan, first = v0 + kg * 4 * kTiles;  // the lane's first logit
   const int mine = row_index(a, row0, lane);
-  const uint64_t adapted = ballot(mine >= 0);
-  const bool in_place = a.out == a.logits;
-  if (in_place && adapted == 0u) return;
+  // this workgroup's adapters, by their first rows, and the rows they cover; the first
+  // group copies the rows without an adapter
+  const uint64_t none = ~ballot(mine >= 0);
+  uint64_t leaders = ~none, rows = ~none;
+  if (groups_log2 > 0) {
+    leaders = rows = 0u;
+    for (uint64_t left = ~none & every << group; left != 0u;) {
+      const int l = __builtin_ctzll(left);
+      const uint64_t members = ballot(mine == (int)readlane_u32((uint32_t)mine, l));
+      left &= ~members;
+      if (__builtin_ctzll(members) != l) continue;
+      leaders |= 1ull << l;
+      rows |= members;
+    }
+  }
+  if (group == 0 && a.out != a.logits) rows |= none;
+  if (rows == 0u) return;
 
   int own[RT];     // the adapter of this lane's batch row
   f32x4 y[kTiles][RT];
@@ -144,7 +169,7 @@ __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
   for (int t = 0; t < RT; ++t) {
     own[t] = __shfl(mine, t * 16 + n, 64);
     const int b = row0 + t * 16 + n;
-    const bool use = b < a.B && !(in_place && own[t] < 0);
+    const bool use = b < a.B && ((rows >> (t * 16 + n)) & 1u);
     const uint8_t* const z = a.logits + (size_t)(use ? b : 0) * a.row_bytes;
 #pragma unroll
     for (int c = 0; c < 4 * kTiles / P; ++c) {
@@ -161,14 +186,16 @@ __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
       }
     }
   }
-  // the coordinates, as they lie
-  const int row_tiles = (min(a.B - row0, kRows) + 15) / 16;
-  for (int i = tid; i < row_tiles * KS * kTerms * 64; i += kUpWaves * 64)
-    s_low[i] = reinterpret_cast<const uint4*>(a.low + (size_t)(row0 / 16) * KS * kStepBytes)[i];
+  // their coordinates, as they lie
+  const uint4* const low =
+      reinterpret_cast<const uint4*>(a.low + (size_t)(row0 / 16) * KS * kStepBytes);
+  for (int i = tid; i < RT * KS * kTerms * 64; i += kUpWaves * 64) {
+    if ((rows & ~none) >> (i / (KS * kTerms * 64) * 16 + (i & 15)) & 1u) s_low[i] = low[i];
+  }
   __syncthreads();
   if (tile >= tiles) return;
 
-  for (uint64_t left = adapted; left != 0u;) {
+  for (uint64_t left = leaders; left != 0u;) {
     int d[A];
     uint64_t members[A];
     bf16x8 f[A][kTiles][KS];
@@ -225,7 +252,7 @@ __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int b = row0 + t * 16 + n;
-    if (b >= a.B || (in_place && own[t] < 0)) continue;
+    if (b >= a.B || !((rows >> (t * 16 + n)) & 1u)) continue;
     uint8_t* const out = a.out + (size_t)b * a.out_bytes;
 #pragma unroll
     for (int c = 0; c < 4 * kTiles / P; ++c) {
@@ -262,12 +289,19 @@ __global__ void __launch_bounds__(kUpWaves * 64) up_kernel(Args a, int tiles) {
 template <int DT, int KS, int A>
 void launch_up(const Args& a, hipStream_t st) {
   const int tiles = (a.V + 16 * kTiles - 1) / (16 * kTiles);
+  const int64_t waves = (int64_t)tiles * ((a.B + kRows - 1) / kRows);
+  int groups_log2 = 0;
+  while (groups_log2 < 6 && 1 << groups_log2 < a.B && waves << (groups_log2 + 1) <= kWavesWanted)
+    ++groups_log2;
+  // a row in each group's turn: every 2^groups_log2-th bit
+  const uint64_t every = ~0ull / (~0ull >> (64 - (1 << groups_log2)));
   const dim3 grid((unsigned)((tiles + kUpWaves - 1) / kUpWaves),
-                  (unsigned)((a.B + kRows - 1) / kRows));
+                  (unsigned)((a.B + kRows - 1) / kRows) << groups_log2);
   const dim3 block(kUpWaves * 64);
-  if (a.B <= 16) hipLaunchKernelGGL((up_kernel<DT, KS, 1, A>), grid, block, 0, st, a, tiles);
-  else if (a.B <= 32) hipLaunchKernelGGL((up_kernel<DT, KS, 2, A>), grid, block, 0, st, a, tiles);
-  else hipLaunchKernelGGL((up_kernel<DT, KS, 4, A>), grid, block, 0, st, a, tiles);
+  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, groups_log2, every); };
+  if (a.B <= 16) run(up_kernel<DT, KS, 1, A>);
+  else if (a.B <= 32) run(up_kernel<DT, KS, 2, A>);
+  else run(up_kernel<DT, KS, 4, A>);
 }
 
 template <int DT>
