@@ -435,6 +435,17 @@ def test_sample_hidden_with_adapters(qs):
     plain = qs.sample_hidden(x, codes, scales, None, T, k, p, seed=seed,
                              offset=torch.zeros_like(seed))
     assert "adapter_status" not in plain
+    # logits that went elsewhere would not be the ones that are drawn from
+    with pytest.raises(TypeError):
+        qs.sample_hidden(x, codes, scales, None, T, k, p, seed=seed,
+                         offset=torch.zeros_like(seed),
+                         adapters=dict(down=down, up=up, index=index, out=lg))
+    index[2] = count
+    out = qs.sample_hidden(x, codes, scales, None, T, k, p, seed=seed,
+                           offset=torch.zeros_like(seed),
+                           adapters=dict(down=down, up=up, index=index, scale=scale))
+    assert out["adapter_status"].tolist() == [4 if b == 2 else 0 for b in range(B)]
+    assert torch.equal(out["logits"][2], plain["logits"][2])
 
 
 def test_distill_an_adapter_then_serve_it(qs):

@@ -315,7 +315,7 @@ def sample_hidden(hidden, codes, scales, zeros, temperature, top_k, top_p, bitma
     moved = None
     if adapters is not None:
         from ._adapters import apply_adapters
-        moved = apply_adapters(z, hidden, **adapters)
+        moved = apply_adapters(z, hidden, out=None, **adapters)  # in place, as sample reads z
     out = sample(z, temperature, top_k, top_p, bitmask, **options)
     out["logits"] = z
     if moved is not None:

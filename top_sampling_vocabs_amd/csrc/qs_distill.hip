@@ -190,13 +190,14 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid,
     const bool at_m = live && s.z[i] == m, at_t = live && !a.rest && s.t[i] == tmax;
     sum[1] += __popcll(ballot(at_m));
     sum[3] += __popcll(ballot(at_t));
-    if (!live) continue;
-    const double d = ((double)s.z[i] - (double)m) * inv_T;
-    const double tau = a.rest ? (double)s.t[i] : ((double)s.t[i] - (double)tmax) * inv_T;
-    const double wt = exp(tau);
-    if (!at_m) sum[0] += exp(d);
-    if (!at_t) sum[2] += wt;
-    if (wt > 0.0) sum[4] += wt * (tau - d);
+    if (live) {
+      const double d = ((double)s.z[i] - (double)m) * inv_T;
+      const double tau = a.rest ? (double)s.t[i] : ((double)s.t[i] - (double)tmax) * inv_T;
+      const double wt = exp(tau);
+      if (!at_m) sum[0] += exp(d);
+      if (!at_t) sum[2] += wt;
+      if (wt > 0.0) sum[4] += wt * (tau - d);
+    }
   }
 #pragma unroll
   for (int k = 0; k < 5; k += 2) sum[k] = wave_sum_f64(sum[k]);
