@@ -3,9 +3,9 @@
 Tolerances, with u = 2^-24 (half a float32 step): products of two bf16 values are exact
 in float32. A coordinate (down x) is a sum of K of them, split over lanes, at most
 K / 16 + 16 additions to a lane and the joins: u (K / 16 + 16) sum|down x|; the scale
-one rounding more. Its product with `up` is taken with the coordinate's 16 leading
-bits or more (2^-16 relative), at most rank + 4 additions and the logit's own, and the
-result is rounded once to float32 and once to its type (half a step: u, bf16 2^-8).
+one rounding more. It enters the product with `up` as three bf16 numbers whose sum it
+is, so that there are at most 3 rank additions and the logit's own, and the result is
+rounded once to float32 and once to its type (half a step: u, bf16 2^-8).
 """
 
 import numpy as np
@@ -68,10 +68,9 @@ def check(z, dtype, x, down, up, scale, index, got):
         want = oracle.adapted_row(z[b], x[b], down[a], up[a], s)
         d, w = np.abs(down[a].astype(np.float64)), np.abs(up[a].astype(np.float64))
         u = down[a].astype(np.float64) @ x[b].astype(np.float64)
-        e_u = abs(s) * (U * (K / 16 + 17) * (d @ np.abs(x[b].astype(np.float64))) +
-                        2.0 ** -16 * np.abs(u))
+        e_u = abs(s) * U * (K / 16 + 18) * (d @ np.abs(x[b].astype(np.float64)))
         size = np.abs(z[b].astype(np.float64)) + w @ (abs(s) * np.abs(u))
-        tol = w @ e_u + U * (rank + 6) * size + (U + step) * np.abs(want)
+        tol = w @ e_u + U * (3 * rank + 6) * size + (U + step) * np.abs(want)
         bad = ~(np.abs(g[b] - want) <= 1.01 * tol)
         assert not bad.any(), (b, np.nonzero(bad)[0][:4], g[b][bad][:4], want[bad][:4], tol[bad][:4])
 
@@ -257,8 +256,7 @@ def test_most_rows(qs):
         size = torch.where(on, u.abs() @ w.abs().t(), size)
         # the products that a coordinate is a sum of
         sums = torch.where(on, (x.double().abs() @ down[a].double().abs().t()) @ w.abs().t(), sums)
-    tol = U * ((K / 16 + 17) * sums + (rank + 6) * (size + z.abs()) + 2 * want.abs()) \
-        + 2.0 ** -16 * size
+    tol = U * ((K / 16 + 18) * sums + (3 * rank + 6) * (size + z.abs()) + 2 * want.abs())
     assert bool(((out - want).abs() <= tol).all())
     assert torch.equal(out[index < 0], z[index < 0])
 

