@@ -16,8 +16,8 @@
 //
 // The logits are read once, into registers, all requested before the first is used, so
 // that the maximum comes first and every exponential is taken once. Rows of up to
-// kRowBlock * kRowLoads loads go to one workgroup and one launch; longer ones are split
-// into parts, joined by a second launch.
+// kRowLoads loads go to one workgroup and one launch; longer ones are split into parts,
+// joined by a second launch.
 //
 // Measured: 2048 rows of 151936 bf16 with 64 named tokens each, 100 to 104 us (6.1 TB/s,
 // where a large copy reaches 5.2: bound by the reads) and 9 for the join, 3 to 6 of which
@@ -49,10 +49,8 @@ constexpr int kPartBlock = 256;   // threads of a part's workgroup
 // with 16, 113 with 8, 117 with 4), whose exponentials are enough to hide their start;
 // masked and fp32 ones are not (2048 masked rows of 100003: 80 with 8, 84 with 16).
 constexpr int kShortLoads = 4, kPartLoads = 8, kLongLoads = 16;
-constexpr int kRowBlock = 1024;   // threads of a whole row's workgroup
-constexpr int kRowLoads = 8;
-constexpr int kSmallBlock = 256;  // threads of a short row's workgroup
-constexpr int kSmallLoads = 4;
+constexpr int kRowLoads = 8192;   // 16-byte loads of a row that goes to one workgroup
+constexpr int kRowBlock = 1024;   // threads of the largest workgroup
 constexpr int kJoinSlots = 4;     // slots per thread of the join
 constexpr float kLowest = -3.402823466e38f;
 
@@ -71,7 +69,7 @@ int64_t parts_of(int64_t V, int dtype, int loads) {
   return (V + n - 1) / n;
 }
 bool one_part(int64_t V, int dtype) {
-  return V <= (int64_t)(dtype == QS_F32 ? 4 : 8) * kRowBlock * kRowLoads;
+  return V <= (int64_t)(dtype == QS_F32 ? 4 : 8) * kRowLoads;
 }
 int loads_for(int64_t B, int64_t V, int dtype, bool mask) {
   const int64_t n = B * parts_of(V, dtype, kPartLoads);
@@ -446,6 +444,14 @@ void launch(const Args& a, int blocks, int parts, int part_loads, Part* wp, hipS
                        parts, part_loads, wp);
 }
 
+template <int N> using Int = std::integral_constant<int, N>;
+
+// A whole row's workgroup holds the row and little more, so that where rows are many
+// others load while its one wave finishes it. (bf16, 32 named tokens, 1 and 4096 rows:
+// 1000 tokens 4.6 and 9.4 us with 128 threads x 1 load, 5.3 and 19 with 256 x 4; 16000
+// tokens 5.8 and 31 with 512 x 4, 8.8 and 96 with 1024 x 8; 32000 tokens 6.8 and 52 with
+// 512 x 8, 8.8 and 97 with 1024 x 8; 3000 tokens 5.0 and 14.4 with 256 x 2, 5.3 and 12.1
+// with 128 x 4; 65536 tokens 8.8 and 123 with 1024 x 8, 9.1 and 102 with 512 x 16.)
 template <int DT>
 hipError_t launch_dt(const Args& a, int B, Part* wp, hipStream_t st) {
   constexpr int P = kPer<DT>;
@@ -457,11 +463,18 @@ hipError_t launch_dt(const Args& a, int B, Part* wp, hipStream_t st) {
       if (few) launch<DT, TH, NL, true, 64>(a, B, 1, each, nullptr, st);
       else launch<DT, TH, NL, true, TH>(a, B, 1, each, nullptr, st);
     };
-    if (a.V <= kSmallBlock * kSmallLoads * P)
-      run(std::integral_constant<int, kSmallBlock>(), std::integral_constant<int, kSmallLoads>());
-    else
-      run(std::integral_constant<int, kRowBlock>(), std::integral_constant<int, kRowLoads>());
-    return hipGetLastError();
+    const int n = (a.V + P - 1) / P;  // 16-byte loads of a row
+    auto pick = [&](auto threads, auto loads) {
+      if (n > decltype(threads)::value * decltype(loads)::value) return false;
+      run(threads, loads);
+      return true;
+    };
+    const bool done = pick(Int<128>(), Int<1>()) || pick(Int<128>(), Int<2>()) ||
+                      (B <= 512 ? pick(Int<256>(), Int<2>()) : pick(Int<128>(), Int<4>())) ||
+                      pick(Int<256>(), Int<4>()) || pick(Int<512>(), Int<4>()) ||
+                      pick(Int<512>(), Int<8>()) ||
+                      (B <= 256 ? pick(Int<1024>(), Int<8>()) : pick(Int<512>(), Int<16>()));
+    return done ? hipGetLastError() : hipErrorInvalidValue;
   }
   // parts of equal length, in whole loads
   const int most = loads_for(B, a.V, DT, a.bitmask != nullptr);
@@ -472,9 +485,9 @@ hipError_t launch_dt(const Args& a, int B, Part* wp, hipStream_t st) {
     launch<DT, kPartBlock, decltype(nl)::value, false, kPartBlock>(a, B * parts, parts, each, wp,
                                                                   st);
   };
-  if (most == kShortLoads) run(std::integral_constant<int, kShortLoads>());
-  else if (most == kPartLoads) run(std::integral_constant<int, kPartLoads>());
-  else run(std::integral_constant<int, kLongLoads>());
+  if (most == kShortLoads) run(Int<kShortLoads>());
+  else if (most == kPartLoads) run(Int<kPartLoads>());
+  else run(Int<kLongLoads>());
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (few)
     hipLaunchKernelGGL((distill_join_kernel<DT, 64>), dim3((unsigned)B), dim3(64), 0, st, a, parts,
