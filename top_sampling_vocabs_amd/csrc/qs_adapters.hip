@@ -10,18 +10,21 @@
 // The second product runs on the matrix cores (16x16x32) with the factor's rows on one
 // side and 16 rows of the batch on the other. A product's column depends on its own
 // batch row alone, so an adapter is multiplied with all 16 and taken by the rows that
-// are its own: no gathering of rows by adapter, and what another row holds (an
-// infinity, uninitialised scratch) cannot reach a result. The coordinates are float32;
-// each is cut into three bf16 numbers of 8 bits, whose sum is it, so that products are
-// exact: three products cost nothing beside the factors' bytes (one rounded to bf16
-// would cost the result 2^-8 of the adapter's share). Sums are held in float32, and each
-// logit is rounded once.
+// are its own; what another row holds (an infinity, uninitialised scratch) cannot reach
+// a result. The first launch also puts each block's rows in the order of their adapters,
+// so that an adapter meets few tiles of 16 (64 rows of 151936 bf16 on 8 adapters in turn,
+// of rank 16 20.0 us against 26.7 in the batch's own order, of rank 8 17.7 against 26.4;
+// on 16 of rank 32, fp32, 40 against 47). The coordinates are float32; each is cut into
+// three bf16 numbers of 8 bits, whose sum is it, so that products are exact: three
+// products cost nothing beside the factors' bytes (one rounded to bf16 would cost the
+// result 2^-8 of the adapter's share). Sums are held in float32, and each logit is
+// rounded once.
 //
 // Measured (first and second launch): 64 rows of 151936 bf16 on adapters of their own of
-// rank 32, 8192 columns, 11 and 118 us (5.6 TB/s in the second, where a large copy reaches
-// 5.2); on three of rank 64, 4096 columns, 5.6 and 19.9 us (4.9 TB/s); 16 rows of 128256
-// fp32, each its own of rank 32, 3.9 and 23.5 us (6.2 TB/s); 1 row of 151936, rank 16, 3.5
-// and 3.9 us, two dependent loads each.
+// rank 32, 8192 columns, 10.5 and 116 us (5.7 TB/s in the second, where a large copy
+// reaches 5.2); on three of rank 64, 4096 columns, 5.7 and 20.4 us (4.8 TB/s); 16 rows of
+// 128256 fp32, each its own of rank 32, 4.0 and 24 us (6.1 TB/s); 1 row of 151936, rank
+// 16, 3.4 and 4.0 us, two dependent loads each.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -46,16 +49,62 @@ constexpr int kWavesWanted = 4096;  // up to which a block's adapters are dealt 
 constexpr int kAhead = 8;         // loads of 512 columns that a wave of the first product
                                   // requests at a time
 
-// The workspace holds the coordinates as the second product takes them: per tile of
-// 16 batch rows, step of 32 ranks and term the 64 lanes' 8 bf16 numbers, lane
-// (row n, ranks 8 g to 8 g + 7) at 16 g + n.
-constexpr int kStepBytes = kTerms * 64 * 16;
+// The workspace holds, per tile of 16 batch rows, the coordinates as the second
+// product's operands: lane (row n, group g) of an operand has 8 bf16 numbers at 16 g + n.
+// Past rank 16 there are kTerms operands per step of 32 ranks, one per term, group g
+// with ranks 8 g to 8 g + 7. Shorter ranks leave groups free: of rank 16 the first
+// operand holds the first two terms, the second the third; of rank 8 one holds all.
+constexpr int kOperandBytes = 64 * 16;
+int operands_of(int64_t rank) {
+  return rank <= 8 ? 1 : rank <= 16 ? 2 : (int)((rank + 31) / 32) * kTerms;
+}
+// Coordinates per row, with the zeros behind the last (and in unused groups).
+int places_of(int64_t rank) {
+  return rank <= 8 ? 16 : (int)((rank + 31) / 32) * 32;
+}
 
-// The adapter of each of a block's rows in its lane; -1: none, or none that exists.
-__device__ __forceinline__ int row_index(const Args& a, int row0, int lane) {
-  const int b = row0 + lane;
-  const int n = b < a.B ? a.index[b] : -1;
-  return n >= 0 && n < a.count ? n : -1;
+// Behind them the plan of each block of kRows batch rows: its rows in the order of
+// their adapters (first come, first), those without one last.
+struct Plan {
+  int32_t row[kRows];      // the row's place in the block | its adapter's number << 16
+                           // (kNoAdapter without one); -1 behind the last
+  int32_t adapter[kRows];  // the adapters
+  int32_t span[kRows];     // their first row | the one behind their last << 16; 0: no more
+};
+constexpr int kNoAdapter = 0x7FFF;
+
+__device__ __forceinline__ void write_plan(const Args& a, int row0, Plan* plan) {
+  const int lane = lane_id(), rows = min(a.B - row0, kRows);
+  const int asked = lane < rows ? a.index[row0 + lane] : -1;
+  const bool adapted = asked >= 0 && asked < a.count;
+  const int mine = adapted ? asked : -1;
+  if (lane < rows) a.status[row0 + lane] = adapted || asked == -1 ? QS_ROW_OK : QS_ROW_BAD_PARAM;
+  // the rows that share this lane's adapter: every row's is compared with every other's,
+  // without a chain from one to the next (a walk from adapter to adapter took 6 us for 64)
+  uint32_t same[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+    same[j >> 5] |= mine == (int)readlane_u32((uint32_t)mine, j) ? 1u << (j & 31) : 0u;
+  const uint64_t members = (uint64_t)same[1] << 32 | same[0], below = (1ull << lane) - 1ull;
+  const int leader = __builtin_ctzll(members), size = __popcll(members);
+  const bool leads = adapted && leader == lane;
+  const uint64_t leaders = ballot(leads);
+  const int adapters = __popcll(leaders), number = __popcll(leaders & below);
+  const int end = (int)scan_incl_u32(leads ? (uint32_t)size : 0u), first = end - size;
+  const int total = __popcll(ballot(adapted));
+  const uint64_t none = ballot(!adapted && lane < rows);
+  const int my_number = __shfl(number, leader, 64), my_first = __shfl(first, leader, 64);
+  const int at = adapted ? my_first + __popcll(members & below)
+                 : lane < rows ? total + __popcll(none & below) : lane;
+  plan->row[at] = lane < rows ? lane | (adapted ? my_number : kNoAdapter) << 16 : -1;
+  if (leads) {
+    plan->adapter[number] = mine;
+    plan->span[number] = first | end << 16;
+  }
+  if (lane >= adapters) {
+    plan->adapter[lane] = -1;
+    plan->span[lane] = 0;
+  }
 }
 
 // The rows' coordinates, a wave to each row and rank: few rows spread over as many
@@ -65,16 +114,19 @@ __device__ __forceinline__ int row_index(const Args& a, int row0, int lane) {
 // 16, 6.5 us, one compute unit's loads, against 3.5; 64 rows of 8192 on adapters of their
 // own, rank 32, 14.2 against 10.7; 64 on 3 of rank 64, 4096 columns, 7.9 against 6.1.
 // Four ranks a wave, which reads the hidden state once for them, were up to 2 us slower.)
-__global__ void __launch_bounds__(256) down_kernel(Args a, int steps) {
+__global__ void __launch_bounds__(256)
+    down_kernel(Args a, int places, int operands, int blocks, Plan* plans) {
   const int lane = lane_id();
-  const int item = uni((int)(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)));
-  const int ranks = steps * 32;            // with zeros behind the last
-  const int b = item / ranks, q = item - b * ranks;
+  if ((int)blockIdx.x < blocks) {  // the first workgroups lay the blocks' plans
+    if (threadIdx.x < 64) write_plan(a, (int)blockIdx.x * kRows, plans + blockIdx.x);
+    return;
+  }
+  const int item =
+      uni((int)((blockIdx.x - blocks) * (blockDim.x >> 6) + (threadIdx.x >> 6)));
+  const int b = item / places, q = item - b * places;
   if (b >= a.B) return;
   const int n = a.index[b];
-  const bool valid = n >= -1 && n < a.count;
-  if (q == 0 && lane == 0) a.status[b] = valid ? QS_ROW_OK : QS_ROW_BAD_PARAM;
-  if (!valid || n < 0) return;
+  if (n < 0 || n >= a.count) return;
   float u = 0.0f;
   if (q < a.rank) {
     const float scale = a.scale ? a.scale[n] : 1.0f;
@@ -109,78 +161,82 @@ __global__ void __launch_bounds__(256) down_kernel(Args a, int steps) {
     for (int off = 32; off > 0; off >>= 1) u += __shfl_xor(u, off, 64);
     u *= scale;
   }
-  if (lane == 0) {
-    uint8_t* const out = a.low + ((size_t)(b / 16) * steps + (q >> 5)) * kStepBytes +
-                         (((q & 31) >> 3) * 16 + (b & 15)) * 16 + (q & 7) * 2;
+  if (lane != 0) return;
+  uint8_t* const out =
+      a.low + (size_t)(b / 16) * operands * kOperandBytes + (b & 15) * 16 + (q & 7) * 2;
+  // the group (of all operands' groups) that holds the coordinate's term k
+  const int g = q >> 3;
 #pragma unroll
-    for (int k = 0; k < kTerms; ++k) {
-      const __bf16 part = (__bf16)u;
-      *reinterpret_cast<__bf16*>(out + k * 1024) = part;
-      u -= (float)part;
-    }
+  for (int k = 0; k < kTerms; ++k) {
+    const int to = operands == 1 ? (q < 8 ? k : 3)
+                   : operands == 2 ? (q < 16 ? 2 * k + g : 4 + g)
+                                   : (g >> 2) * 4 * kTerms + 4 * k + (g & 3);
+    const __bf16 part = (__bf16)u;
+    *reinterpret_cast<__bf16*>(out + to * 256) = part;
+    u -= (float)part;
   }
 }
 
 // The logits. A wave takes kTiles tiles of 16 vocabulary rows and up to RT tiles of 16
 // batch rows: the logits are its accumulators, and it walks the block's adapters, A at a
 // time (2 where their rows are so short, up to rank 16, that one's are too few bytes under
-// way: 64 rows of 151936 on adapters of rank 16 of their own 69 us against 77; of rank 32
-// 130 against 126, of 64 102 against 100). Two tiles leave room for more waves than four
-// (64 rows on 16 adapters of rank 128: 147 us against 172; on 4 of rank 16, float32, 24.5
-// against 33). The tiles' rows are dealt out so that a lane holds 4 kTiles consecutive
-// logits of one batch row: product row 4 g + e of tile t is vocabulary row
+// way: 64 rows of 151936 on adapters of rank 16 of their own 70 us, 77 with one at a time,
+// 86 with four; of rank 32 126 with one, 131 with two). Two tiles leave room for more
+// waves than four (64 rows on 16 adapters of rank 128: 147 us against 172; on 4 of rank
+// 16, fp32, 24.5 against 33). The tiles' rows are dealt out so that a lane holds 4 kTiles
+// consecutive logits of one batch row: product row 4 g + e of tile t is vocabulary row
 // 4 (kTiles g + t) + e.
 //
 // A wave that walks many adapters waits for each one's factors, so where the vocabulary
 // makes few waves a block's adapters are dealt out to up to 64 groups of workgroups, each
-// with the rows of its own (64 rows on adapters of their own of rank 16: 1000 tokens 7.0
-// us against 26.6, 8000 10.8 against 32, 32000 20.7 against 34, 64000 31 against 37; past
-// kWavesWanted, 128256 in two groups, 62 against 57. 3 adapters of rank 64: 9.9 against
-// 12.0, 10.1 against 12.1, 11.7 against 12.7, 15.3 against 15.8 and, past it, 24.5 against
-// 21.0).
-template <int DT, int KS, int RT, int A>
+// with the rows of its own (64 rows on adapters of their own of rank 16: 1000 tokens 7.1
+// us against 26.6 in one group, 8000 10.1 against 32, 32000 18.8 against 34, 64000 28.4
+// against 37). Past kWavesWanted that costs more than it gives (64000 tokens in four
+// groups 30.6, 128256 in two 57.0 against 55.7).
+template <int DT, int KS, int OPS, int RT, int A>
 __global__ void __launch_bounds__(kUpWaves * 64)
-    up_kernel(Args a, int tiles, int groups_log2, uint64_t every) {
+    up_kernel(Args a, int tiles, int groups_log2, const Plan* plans) {
   constexpr int kSpan = 16 * kTiles;      // vocabulary rows per wave
   constexpr int P = DT == QS_F32 ? 4 : 8; // logits per 16 bytes
-  __shared__ uint4 s_low[RT * KS * kTerms * 64];
+  __shared__ uint4 s_low[RT * OPS * 64];
   const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
   const int n = lane & 15, kg = lane >> 4;
   const int group = (int)blockIdx.y & ((1 << groups_log2) - 1);
-  const int row0 = ((int)blockIdx.y >> groups_log2) * kRows;
+  const int block = (int)blockIdx.y >> groups_log2, row0 = block * kRows;
   const int tile = (int)blockIdx.x * kUpWaves + w;
   const int v0 = tile * kSpan, first = v0 + kg * 4 * kTiles;  // the lane's first logit
-  const int mine = row_index(a, row0, lane);
-  // this workgroup's adapters, by their first rows, and the rows they cover; the first
-  // group copies the rows without an adapter
-  const uint64_t none = ~ballot(mine >= 0);
-  uint64_t leaders = ~none, rows = ~none;
-  if (groups_log2 > 0) {
-    leaders = rows = 0u;
-    for (uint64_t left = ~none & every << group; left != 0u;) {
-      const int l = __builtin_ctzll(left);
-      const uint64_t members = ballot(mine == (int)readlane_u32((uint32_t)mine, l));
-      left &= ~members;
-      if (__builtin_ctzll(members) != l) continue;
-      leaders |= 1ull << l;
-      rows |= members;
-    }
-  }
-  if (group == 0 && a.out != a.logits) rows |= none;
-  if (rows == 0u) return;
+  const int planned = plans[block].row[lane], adapter = plans[block].adapter[lane],
+            span = plans[block].span[lane];
+  // the block's coordinates, as they lie
+  const uint4* const low =
+      reinterpret_cast<const uint4*>(a.low + (size_t)(row0 / 16) * OPS * kOperandBytes);
+  const int items = (min(a.B - row0, kRows) + 15) / 16 * OPS * 64;
+#pragma unroll
+  for (int i = tid; i < RT * OPS * 64; i += kUpWaves * 64)
+    if (i < items) s_low[i] = low[i];
+  const int adapters = __popcll(ballot(span != 0));
+  const bool copies = group == 0 && a.out != a.logits;  // the rows without an adapter
+  if (group >= adapters && !copies) return;
 
-  int own[RT];     // the adapter of this lane's batch row
+  // this lane's batch rows, in the plan's order: their adapters' numbers (-1: not this
+  // workgroup's), and their logits
+  int row[RT], number[RT], place[RT];
   f32x4 y[kTiles][RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    own[t] = __shfl(mine, t * 16 + n, 64);
-    const int b = row0 + t * 16 + n;
-    const bool use = b < a.B && ((rows >> (t * 16 + n)) & 1u);
-    const uint8_t* const z = a.logits + (size_t)(use ? b : 0) * a.row_bytes;
+    const int p = __shfl(planned, t * 16 + n, 64);
+    number[t] = p >> 16;
+    const bool here = p >= 0 && (number[t] == kNoAdapter
+                                     ? copies
+                                     : (number[t] & ((1 << groups_log2) - 1)) == group);
+    if (!here) number[t] = -1;
+    row[t] = row0 + (p & 0xFFFF);
+    place[t] = ((p & 0xFFFF) >> 4 & 3) * OPS * 64 + kg * 16 + (p & 15);  // of its coordinates
+    const uint8_t* const z = a.logits + (size_t)(here ? row[t] : 0) * a.row_bytes;
 #pragma unroll
     for (int c = 0; c < 4 * kTiles / P; ++c) {
       uint4 q = make_uint4(0u, 0u, 0u, 0u);
-      if (use && first + c * P < a.V)
+      if (here && first + c * P < a.V)
         q = *reinterpret_cast<const uint4*>(z + (size_t)(first + c * P) * (16 / P));
       const uint32_t word[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -192,64 +248,57 @@ __global__ void __launch_bounds__(kUpWaves * 64)
       }
     }
   }
-  // their coordinates, as they lie
-  const uint4* const low =
-      reinterpret_cast<const uint4*>(a.low + (size_t)(row0 / 16) * KS * kStepBytes);
-  for (int i = tid; i < RT * KS * kTerms * 64; i += kUpWaves * 64) {
-    if ((rows & ~none) >> (i / (KS * kTerms * 64) * 16 + (i & 15)) & 1u) s_low[i] = low[i];
-  }
   __syncthreads();
   if (tile >= tiles) return;
 
-  for (uint64_t left = leaders; left != 0u;) {
-    int d[A];
-    uint64_t members[A];
+  for (int i0 = group; i0 < adapters; i0 += A << groups_log2) {
+    int at[A], end[A];
     bf16x8 f[A][kTiles][KS];
 #pragma unroll
     for (int j = 0; j < A; ++j) {
-      d[j] = -1;
-      members[j] = 0u;
-      if (left == 0u) continue;
-      d[j] = readlane_u32((uint32_t)mine, __builtin_ctzll(left));
-      members[j] = ballot(mine == d[j]);
-      left &= ~members[j];
-      const uint16_t* const up = a.up + (size_t)d[j] * a.up_stride;
+      const int i = i0 + (j << groups_log2);
+      at[j] = end[j] = 0;
+      if (i >= adapters) continue;
+      const int where = (int)readlane_u32((uint32_t)span, i);
+      at[j] = where & 0xFFFF;
+      end[j] = where >> 16;
+      const uint16_t* const up = a.up + (size_t)readlane_u32((uint32_t)adapter, i) * a.up_stride;
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const int v = min(v0 + (n >> 2) * 4 * kTiles + i * 4 + (n & 3), a.V - 1);
-        const uint16_t* const row = up + (size_t)v * a.up_row_stride;
+      for (int k = 0; k < kTiles; ++k) {
+        const int v = min(v0 + (n >> 2) * 4 * kTiles + k * 4 + (n & 3), a.V - 1);
+        const uint16_t* const r = up + (size_t)v * a.up_row_stride;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
+          // groups beside the terms' read the same ranks again
+          const int c = OPS == 1 ? 0 : OPS == 2 ? (kg & 1) * 8 : s * 32 + kg * 8;
           uint4 q = make_uint4(0u, 0u, 0u, 0u);
-          if (s * 32 + kg * 8 < a.rank) q = *reinterpret_cast<const uint4*>(row + s * 32 + kg * 8);
-          f[j][i][s] = __builtin_bit_cast(bf16x8, q);
+          if (c < a.rank) q = *reinterpret_cast<const uint4*>(r + c);
+          f[j][k][s] = __builtin_bit_cast(bf16x8, q);
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < A; ++j) {
+      const int i = i0 + (j << groups_log2);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        if (((members[j] >> (t * 16)) & 0xFFFFu) == 0u) continue;
+        if (t * 16 >= end[j] || t * 16 + 16 <= at[j]) continue;
         f32x4 acc[kTiles];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) acc[i] = y[i][t];
+        for (int k = 0; k < kTiles; ++k) acc[k] = y[k][t];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
+        for (int o = 0; o < OPS; ++o) {
+          const bf16x8 u = __builtin_bit_cast(bf16x8, s_low[place[t] + o * 64]);
 #pragma unroll
-          for (int k = 0; k < kTerms; ++k) {
-            const bf16x8 u =
-                __builtin_bit_cast(bf16x8, s_low[((t * KS + s) * kTerms + k) * 64 + lane]);
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][i][s], u, acc[i], 0, 0, 0);
-          }
+          for (int k = 0; k < kTiles; ++k)
+            acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][k][OPS <= 2 ? 0 : o / kTerms], u,
+                                                             acc[k], 0, 0, 0);
         }
-        const bool take = own[t] == d[j];
+        const bool take = number[t] == i;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
+        for (int k = 0; k < kTiles; ++k) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[i][t][e] = take ? acc[i][e] : y[i][t][e];
+          for (int e = 0; e < 4; ++e) y[k][t][e] = take ? acc[k][e] : y[k][t][e];
         }
       }
     }
@@ -257,9 +306,8 @@ __global__ void __launch_bounds__(kUpWaves * 64)
 
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const int b = row0 + t * 16 + n;
-    if (b >= a.B || !((rows >> (t * 16 + n)) & 1u)) continue;
-    uint8_t* const out = a.out + (size_t)b * a.out_bytes;
+    if (number[t] < 0) continue;
+    uint8_t* const out = a.out + (size_t)row[t] * a.out_bytes;
 #pragma unroll
     for (int c = 0; c < 4 * kTiles / P; ++c) {
       const int v = first + c * P;
@@ -292,51 +340,55 @@ __global__ void __launch_bounds__(kUpWaves * 64)
   }
 }
 
-template <int DT, int KS, int A>
-void launch_up(const Args& a, hipStream_t st) {
+template <int DT, int KS, int OPS, int A>
+void launch_up(const Args& a, const Plan* plans, hipStream_t st) {
   const int tiles = (a.V + 16 * kTiles - 1) / (16 * kTiles);
-  const int64_t waves = (int64_t)tiles * ((a.B + kRows - 1) / kRows);
+  const int blocks = (a.B + kRows - 1) / kRows;
   int groups_log2 = 0;
-  while (groups_log2 < 6 && 1 << groups_log2 < a.B && waves << (groups_log2 + 1) <= kWavesWanted)
+  while (groups_log2 < 6 && 1 << groups_log2 < a.B &&
+         (int64_t)tiles * blocks << (groups_log2 + 1) <= kWavesWanted)
     ++groups_log2;
-  // a row in each group's turn: every 2^groups_log2-th bit
-  const uint64_t every = ~0ull / (~0ull >> (64 - (1 << groups_log2)));
-  const dim3 grid((unsigned)((tiles + kUpWaves - 1) / kUpWaves),
-                  (unsigned)((a.B + kRows - 1) / kRows) << groups_log2);
+  const dim3 grid((unsigned)((tiles + kUpWaves - 1) / kUpWaves), (unsigned)blocks << groups_log2);
   const dim3 block(kUpWaves * 64);
-  auto run = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, groups_log2, every); };
-  if (a.B <= 16) run(up_kernel<DT, KS, 1, A>);
-  else if (a.B <= 32) run(up_kernel<DT, KS, 2, A>);
-  else run(up_kernel<DT, KS, 4, A>);
+  auto run = [&](auto* kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, groups_log2, plans);
+  };
+  if (a.B <= 16) run(up_kernel<DT, KS, OPS, 1, A>);
+  else if (a.B <= 32) run(up_kernel<DT, KS, OPS, 2, A>);
+  else run(up_kernel<DT, KS, OPS, 4, A>);
 }
 
 template <int DT>
-void launch_rank(const Args& a, int steps, hipStream_t st) {
-  if (a.rank <= 16) launch_up<DT, 1, 2>(a, st);
-  else if (steps == 1) launch_up<DT, 1, 1>(a, st);
-  else if (steps == 2) launch_up<DT, 2, 1>(a, st);
-  else if (steps == 3) launch_up<DT, 3, 1>(a, st);
-  else launch_up<DT, 4, 1>(a, st);
+void launch_rank(const Args& a, const Plan* plans, hipStream_t st) {
+  if (a.rank <= 8) launch_up<DT, 1, 1, 2>(a, plans, st);
+  else if (a.rank <= 16) launch_up<DT, 1, 2, 2>(a, plans, st);
+  else if (a.rank <= 32) launch_up<DT, 1, kTerms, 1>(a, plans, st);
+  else if (a.rank <= 64) launch_up<DT, 2, 2 * kTerms, 1>(a, plans, st);
+  else if (a.rank <= 96) launch_up<DT, 3, 3 * kTerms, 1>(a, plans, st);
+  else launch_up<DT, 4, 4 * kTerms, 1>(a, plans, st);
 }
 
-int steps_of(int64_t rank) { return (int)((rank + 31) / 32); }
+size_t low_bytes(int64_t B, int64_t rank) {
+  return (size_t)((B + 15) / 16) * operands_of(rank) * kOperandBytes;
+}
 
 }  // namespace
 
 size_t workspace_bytes(int64_t B, int64_t rank) {
-  return (size_t)((B + 15) / 16) * steps_of(rank) * kStepBytes;
+  return low_bytes(B, rank) + (size_t)((B + kRows - 1) / kRows) * sizeof(Plan);
 }
 
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
-  const int steps = steps_of(a.rank);
-  const int64_t items = (int64_t)a.B * steps * 32;
+  Plan* const plans = reinterpret_cast<Plan*>(a.low + low_bytes(a.B, a.rank));
+  const int places = places_of(a.rank), blocks = (a.B + kRows - 1) / kRows;
+  const int64_t items = (int64_t)a.B * places;
   // one wave a workgroup where that spreads few waves over more compute units
   const int waves = items > 1024 ? 4 : 1;
-  hipLaunchKernelGGL(down_kernel, dim3((unsigned)((items + waves - 1) / waves)), dim3(waves * 64), 0,
-                     st, a, steps);
+  hipLaunchKernelGGL(down_kernel, dim3((unsigned)(blocks + (items + waves - 1) / waves)),
+                     dim3(waves * 64), 0, st, a, places, operands_of(a.rank), blocks, plans);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  if (dtype == QS_F32) launch_rank<QS_F32>(a, steps, st);
-  else launch_rank<QS_BF16>(a, steps, st);
+  if (dtype == QS_F32) launch_rank<QS_F32>(a, plans, st);
+  else launch_rank<QS_BF16>(a, plans, st);
   return hipGetLastError();
 }
 

@@ -23,7 +23,7 @@
 // where a large copy reaches 5.2: bound by the reads) and 9 for the join, 3 to 6 of which
 // are the named tokens' 131072 cache lines; 64 rows of 128256 fp32, 7.2 us and 4.4; one
 // row of 32000 fp32, 6.6 us, its latency (11.2 with all 16 waves finishing the row and its
-// logarithms one after another); 37 masked rows of 32003 bf16, 9.4 us. One workgroup a row
+// logarithms one after another); 37 masked rows of 32003 bf16, 7.5 us. One workgroup a row
 // that walks it with a running maximum took 206 us for the 2048 rows.
 
 #include <hip/hip_runtime.h>
