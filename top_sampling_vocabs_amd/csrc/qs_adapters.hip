@@ -224,14 +224,14 @@ __global__ void __launch_bounds__(kUpWaves * 64)
   f32x4 y[kTiles][RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const int p = __shfl(planned, t * 16 + n, 64);
+    const int p = __shfl(planned, t * 16 + n, 64), r = p < 0 ? 0 : p & 0xFFFF;
     number[t] = p >> 16;
     const bool here = p >= 0 && (number[t] == kNoAdapter
                                      ? copies
                                      : (number[t] & ((1 << groups_log2) - 1)) == group);
     if (!here) number[t] = -1;
-    row[t] = row0 + (p & 0xFFFF);
-    place[t] = ((p & 0xFFFF) >> 4 & 3) * OPS * 64 + kg * 16 + (p & 15);  // of its coordinates
+    row[t] = row0 + r;
+    place[t] = (r >> 4) * OPS * 64 + kg * 16 + (r & 15);  // of its coordinates
     const uint8_t* const z = a.logits + (size_t)(here ? row[t] : 0) * a.row_bytes;
 #pragma unroll
     for (int c = 0; c < 4 * kTiles / P; ++c) {
