@@ -132,6 +132,22 @@ def test_batches(qs, B, kind):
     check(z, "bf16", x, down, up, None, index, again)
 
 
+@pytest.mark.parametrize("B,count", [(65, 1), (320, 64), (700, 5), (4096, 300), (4161, 3),
+                                     (9000, 70)])
+def test_more_rows_than_a_block(qs, B, count):
+    """Batches whose rows are put in order over blocks of 64 (and over 4096 rows, one order
+    behind another), with rows without an adapter and bad indexes among them."""
+    print(f"adapters B={B} count={count}", flush=True)
+    z, x, down, up, scale, index = inputs(B, B, 70, 32, 16, count)
+    index[::17] = count + 3
+    index[5::23] = -5
+    bad = (index < -1) | (index >= count)
+    for in_place in (True, False):
+        got, status = run(qs, z, "bf16", x, down, up, scale, index, in_place=in_place)
+        assert np.array_equal(status.cpu().numpy(), np.where(bad, 4, 0))
+        check(z, "bf16", x, down, up, scale, index, got)
+
+
 def test_bad_indexes(qs):
     """An index that is no adapter leaves the row as it is and is reported."""
     z, x, down, up, scale, index = inputs(1, 9, 300, 64, 16, 4)

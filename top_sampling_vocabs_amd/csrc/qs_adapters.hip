@@ -3,28 +3,31 @@
 //   y[b][v] = z[b][v] + scale[a] sum_r up[a][v][r] u[b][r],
 //   u[b][r] = sum_k down[a][r][k] x[b][k].
 // Two launches: the rows' low-rank coordinates scale * u, then their product with the
-// up factors on top of the logits. Every used adapter is read once per 64 rows,
-// however they share it; what bounds the calls is reading the up factors, and the
+// up factors on top of the logits. Every used adapter is read once per 64 rows that use
+// it, wherever they stand; what bounds the calls is reading the up factors, and the
 // logits read and written.
 //
 // The second product runs on the matrix cores (16x16x32) with the factor's rows on one
 // side and 16 rows of the batch on the other. A product's column depends on its own
 // batch row alone, so an adapter is multiplied with all 16 and taken by the rows that
 // are its own; what another row holds (an infinity, uninitialised scratch) cannot reach
-// a result. The first launch also puts each block's rows in the order of their adapters,
-// so that an adapter meets few tiles of 16 (64 rows of 151936 bf16 on 8 adapters in turn,
-// of rank 16 20.0 us against 26.7 in the batch's own order, of rank 8 17.7 against 26.4;
-// on 16 of rank 32, fp32, 40 against 47). The coordinates are float32; each is cut into
-// three bf16 numbers of 8 bits, whose sum is it, so that products are exact: three
-// products cost nothing beside the factors' bytes (one rounded to bf16 would cost the
-// result 2^-8 of the adapter's share). Sums are held in float32, and each logit is
-// rounded once.
+// a result. The first launch also puts the rows in the order of their adapters, so that
+// an adapter meets few blocks of 64 rows (512 rows of 151936 on 64 adapters of rank 16:
+// 147 us against 498 with an order in each block alone; 320 rows 125 against 313; on 8 of
+// them, whose factors the L2 held either way, 512 rows 121 against 111) and few tiles of 16
+// (64 rows of 151936 bf16 on 8 adapters in turn, of rank 16 20.0 us against 26.7 in the
+// batch's own order, of rank 8 17.7 against 26.4; on 16 of rank 32, fp32, 40 against 47).
+// The coordinates are float32; each is cut into three bf16 numbers of 8 bits, whose sum is
+// it, so that products are exact: three products cost nothing beside the factors' bytes
+// (one rounded to bf16 would cost the result 2^-8 of the adapter's share). Sums are held in
+// float32, and each logit is rounded once.
 //
 // Measured (first and second launch): 64 rows of 151936 bf16 on adapters of their own of
 // rank 32, 8192 columns, 10.5 and 116 us (5.7 TB/s in the second, where a large copy
 // reaches 5.2); on three of rank 64, 4096 columns, 5.7 and 20.4 us (4.8 TB/s); 16 rows of
 // 128256 fp32, each its own of rank 32, 4.0 and 24 us (6.1 TB/s); 1 row of 151936, rank
-// 16, 3.4 and 4.0 us, two dependent loads each.
+// 16, 3.4 and 4.0 us, two dependent loads each. Both together, 151936 bf16, 2048 columns:
+// 2048 rows on one adapter of rank 16 324 us, on 64 of them 460 (3.9 and 3.4 TB/s).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -42,6 +45,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 64;         // batch rows of a block
+constexpr int kNone = 0x7FFF;     // in place of an adapter's number
 constexpr int kTerms = 3;         // bf16 numbers per coordinate
 constexpr int kUpWaves = 4;
 constexpr int kTiles = 2;         // tiles of 16 vocabulary rows per wave
@@ -63,22 +67,22 @@ int places_of(int64_t rank) {
   return rank <= 8 ? 16 : (int)((rank + 31) / 32) * 32;
 }
 
-// Behind them the plan of each block of kRows batch rows: its rows in the order of
-// their adapters (first come, first), those without one last.
+// Behind them, for a batch of at most kRows rows, its plan: the rows in the order of
+// their adapters (first come, first), those without one last, and the adapters (found
+// again by every workgroup of the second launch, as for more rows, 0.3 to 0.6 us more).
 struct Plan {
   int32_t row[kRows];      // the row's place in the block | its adapter's number << 16
-                           // (kNoAdapter without one); -1 behind the last
+                           // (kNone without one); -1 behind the last
   int32_t adapter[kRows];  // the adapters
   int32_t span[kRows];     // their first row | the one behind their last << 16; 0: no more
 };
-constexpr int kNoAdapter = 0x7FFF;
 
-__device__ __forceinline__ void write_plan(const Args& a, int row0, Plan* plan) {
-  const int lane = lane_id(), rows = min(a.B - row0, kRows);
-  const int asked = lane < rows ? a.index[row0 + lane] : -1;
+__device__ __forceinline__ void write_plan(const Args& a, Plan* plan) {
+  const int lane = lane_id(), rows = a.B;
+  const int asked = lane < rows ? a.index[lane] : -1;
   const bool adapted = asked >= 0 && asked < a.count;
   const int mine = adapted ? asked : -1;
-  if (lane < rows) a.status[row0 + lane] = adapted || asked == -1 ? QS_ROW_OK : QS_ROW_BAD_PARAM;
+  if (lane < rows) a.status[lane] = adapted || asked == -1 ? QS_ROW_OK : QS_ROW_BAD_PARAM;
   // the rows that share this lane's adapter: every row's is compared with every other's,
   // without a chain from one to the next (a walk from adapter to adapter took 6 us for 64)
   uint32_t same[2] = {0u, 0u};
@@ -96,7 +100,7 @@ __device__ __forceinline__ void write_plan(const Args& a, int row0, Plan* plan) 
   const int my_number = __shfl(number, leader, 64), my_first = __shfl(first, leader, 64);
   const int at = adapted ? my_first + __popcll(members & below)
                  : lane < rows ? total + __popcll(none & below) : lane;
-  plan->row[at] = lane < rows ? lane | (adapted ? my_number : kNoAdapter) << 16 : -1;
+  plan->row[at] = lane < rows ? lane | (adapted ? my_number : kNone) << 16 : -1;
   if (leads) {
     plan->adapter[number] = mine;
     plan->span[number] = first | end << 16;
@@ -107,6 +111,43 @@ __device__ __forceinline__ void write_plan(const Args& a, int row0, Plan* plan) 
   }
 }
 
+// For more rows the order of all of them by adapter, those without one last (of more than
+// kOrdered rows each so many in an order of their own).
+struct Place {
+  int32_t row, adapter;  // adapter -1: none, or none that exists
+};
+constexpr int kOrdered = 4096;
+
+// 64 rows' places: every row's key is compared with every other's; the four waves of a
+// workgroup share the keys.
+__device__ __forceinline__ void place_rows(const Args& a, int row0, Place* order) {
+  __shared__ uint32_t s_count[256];
+  const int lane = lane_id(), w = uni((int)(threadIdx.x >> 6));
+  const int segment = row0 & ~(kOrdered - 1), end = min(segment + kOrdered, a.B);
+  auto key_of = [&](int r, int n) {  // behind the last row: behind every key
+    return r >= end ? 0xFFFFFFFFu : n >= 0 && n < a.count ? (uint32_t)n : 0x80000000u;
+  };
+  const int r = row0 + lane, asked = r < end ? a.index[r] : -1;
+  const uint32_t mine = key_of(r, asked);
+  uint32_t count = 0u;
+  for (int j0 = segment + w * 64; j0 < end; j0 += 256) {
+    const uint32_t keys = key_of(j0 + lane, j0 + lane < end ? a.index[j0 + lane] : -1);
+    // among equals the row that comes first
+    const uint32_t than = j0 < row0 ? mine + 1u : mine;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      const uint32_t k = readlane_u32(keys, j);
+      count += k < than || (j0 == row0 && k == mine && j < lane) ? 1u : 0u;
+    }
+  }
+  s_count[threadIdx.x] = count;
+  __syncthreads();
+  if (w != 0 || r >= end) return;
+  for (int k = 1; k < 4; ++k) count += s_count[k * 64 + lane];
+  a.status[r] = asked == -1 || mine != 0x80000000u ? QS_ROW_OK : QS_ROW_BAD_PARAM;
+  order[segment + (int)count] = Place{r, mine == 0x80000000u ? -1 : asked};
+}
+
 // The rows' coordinates, a wave to each row and rank: few rows spread over as many
 // compute units as they have ranks, each wave requests up to 8 KiB of the factor before
 // it uses any, and rows that share an adapter read it from the L2. (On the matrix cores,
@@ -114,11 +155,13 @@ __device__ __forceinline__ void write_plan(const Args& a, int row0, Plan* plan) 
 // 16, 6.5 us, one compute unit's loads, against 3.5; 64 rows of 8192 on adapters of their
 // own, rank 32, 14.2 against 10.7; 64 on 3 of rank 64, 4096 columns, 7.9 against 6.1.
 // Four ranks a wave, which reads the hidden state once for them, were up to 2 us slower.)
+template <bool WIDE>
 __global__ void __launch_bounds__(256)
-    down_kernel(Args a, int places, int operands, int blocks, Plan* plans) {
+    down_kernel(Args a, int places, int operands, int blocks, void* order) {
   const int lane = lane_id();
-  if ((int)blockIdx.x < blocks) {  // the first workgroups lay the blocks' plans
-    if (threadIdx.x < 64) write_plan(a, (int)blockIdx.x * kRows, plans + blockIdx.x);
+  if ((int)blockIdx.x < blocks) {  // the first workgroups put the rows in order
+    if constexpr (WIDE) place_rows(a, (int)blockIdx.x * 64, static_cast<Place*>(order));
+    else if (threadIdx.x < 64) write_plan(a, static_cast<Plan*>(order));
     return;
   }
   const int item =
@@ -193,45 +236,85 @@ __global__ void __launch_bounds__(256)
 // us against 26.6 in one group, 8000 10.1 against 32, 32000 18.8 against 34, 64000 28.4
 // against 37). Past kWavesWanted that costs more than it gives (64000 tokens in four
 // groups 30.6, 128256 in two 57.0 against 55.7).
-template <int DT, int KS, int OPS, int RT, int A>
+template <int DT, int KS, int OPS, int RT, int A, bool WIDE>
 __global__ void __launch_bounds__(kUpWaves * 64)
-    up_kernel(Args a, int tiles, int groups_log2, const Plan* plans) {
+    up_kernel(Args a, int tiles, int parts, int groups_log2, const void* order) {
   constexpr int kSpan = 16 * kTiles;      // vocabulary rows per wave
   constexpr int P = DT == QS_F32 ? 4 : 8; // logits per 16 bytes
   __shared__ uint4 s_low[RT * OPS * 64];
   const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
   const int n = lane & 15, kg = lane >> 4;
-  const int group = (int)blockIdx.y & ((1 << groups_log2) - 1);
-  const int block = (int)blockIdx.y >> groups_log2, row0 = block * kRows;
-  const int tile = (int)blockIdx.x * kUpWaves + w;
+  // of many blocks those of a tile beside each other, so that factors that several of
+  // them read are in the L2
+  const int part = WIDE ? (int)(blockIdx.x % (unsigned)parts) : (int)blockIdx.y;
+  const int group = part & ((1 << groups_log2) - 1), row0 = (part >> groups_log2) * kRows;
+  const int tile =
+      (WIDE ? (int)(blockIdx.x / (unsigned)parts) : (int)blockIdx.x) * kUpWaves + w;
   const int v0 = tile * kSpan, first = v0 + kg * 4 * kTiles;  // the lane's first logit
-  const int planned = plans[block].row[lane], adapter = plans[block].adapter[lane],
-            span = plans[block].span[lane];
-  // the block's coordinates, as they lie
-  const uint4* const low =
-      reinterpret_cast<const uint4*>(a.low + (size_t)(row0 / 16) * OPS * kOperandBytes);
-  const int items = (min(a.B - row0, kRows) + 15) / 16 * OPS * 64;
-#pragma unroll
-  for (int i = tid; i < RT * OPS * 64; i += kUpWaves * 64)
-    if (i < items) s_low[i] = low[i];
-  const int adapters = __popcll(ballot(span != 0));
+  const int rows = min(a.B - row0, kRows);
+  const uint4* const low = reinterpret_cast<const uint4*>(a.low);
   const bool copies = group == 0 && a.out != a.logits;  // the rows without an adapter
+  auto of_group = [&](int number) { return (number & ((1 << groups_log2) - 1)) == group; };
+  // the lane's place in the order: its row and its adapter's number in the block (-1: not
+  // this workgroup's row, kNone: no adapter); the lane's adapter and the places it has
+  int mine_row, mine_number, adapter, span, adapters;
+  if constexpr (!WIDE) {
+    const Plan* const plan = static_cast<const Plan*>(order);
+    const int p = plan->row[lane];
+    adapter = plan->adapter[lane];
+    span = plan->span[lane];
+    // the coordinates as they lie
+    const int items = (rows + 15) / 16 * OPS * 64;
+#pragma unroll
+    for (int i0 = 0; i0 < RT * OPS * 64; i0 += kUpWaves * 64)
+      if (i0 + tid < items) s_low[i0 + tid] = low[i0 + tid];
+    adapters = __popcll(ballot(span != 0));
+    mine_row = p < 0 ? 0 : p & 0xFFFF;
+    mine_number = p >> 16;
+  } else {
+    Place p{0, -1};
+    if (lane < rows) p = static_cast<const Place*>(order)[row0 + lane];
+    const int before = __shfl_up(p.adapter, 1, 64);
+    const uint64_t starts = ballot(p.adapter >= 0 && (lane == 0 || before != p.adapter));
+    const int number = __popcll(starts & (~0ull >> (63 - lane))) - 1;
+    const int total = __popcll(ballot(p.adapter >= 0));
+    adapters = __popcll(starts);
+    mine_row = p.row;
+    mine_number = lane >= rows ? -1 : p.adapter < 0 ? kNone : number;
+    __shared__ int s_adapter[64], s_span[64];
+    if (w == 0 && ((starts >> lane) & 1u)) {
+      const uint64_t later = starts & (~1ull << lane);
+      const int end = later != 0u ? __builtin_ctzll(later) : total;
+      s_adapter[number] = p.adapter;
+      s_span[number] = lane | end << 16;
+    }
+    __syncthreads();
+    adapter = s_adapter[lane];
+    span = s_span[lane];
+  }
   if (group >= adapters && !copies) return;
+  if (mine_number == kNone ? !copies : !of_group(mine_number)) mine_number = -1;
+  if constexpr (WIDE) {  // the coordinates from where they lie
+    for (int i0 = 0; i0 < RT * OPS * 64; i0 += kUpWaves * 64) {
+      const int i = i0 + tid, t = i / (OPS * 64), o = (i >> 6) % OPS;
+      const int r = __shfl(mine_row, t * 16 + (i & 15), 64);
+      const int number = __shfl(mine_number, t * 16 + (i & 15), 64);
+      if (number >= 0 && number != kNone)
+        s_low[i] = low[((size_t)(r >> 4) * OPS + o) * 64 + (lane & 48) + (r & 15)];
+    }
+    static_assert(RT == 4, "whole turns");
+  }
 
-  // this lane's batch rows, in the plan's order: their adapters' numbers (-1: not this
-  // workgroup's), and their logits
+  // this lane's batch rows, in that order, and their logits
   int row[RT], number[RT], place[RT];
   f32x4 y[kTiles][RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const int p = __shfl(planned, t * 16 + n, 64), r = p < 0 ? 0 : p & 0xFFFF;
-    number[t] = p >> 16;
-    const bool here = p >= 0 && (number[t] == kNoAdapter
-                                     ? copies
-                                     : (number[t] & ((1 << groups_log2) - 1)) == group);
-    if (!here) number[t] = -1;
-    row[t] = row0 + r;
-    place[t] = (r >> 4) * OPS * 64 + kg * 16 + (r & 15);  // of its coordinates
+    row[t] = __shfl(mine_row, t * 16 + n, 64);
+    number[t] = __shfl(mine_number, t * 16 + n, 64);
+    place[t] = WIDE ? t * OPS * 64 + lane
+                    : (row[t] >> 4) * OPS * 64 + kg * 16 + (row[t] & 15);  // of its coordinates
+    const bool here = number[t] >= 0;
     const uint8_t* const z = a.logits + (size_t)(here ? row[t] : 0) * a.row_bytes;
 #pragma unroll
     for (int c = 0; c < 4 * kTiles / P; ++c) {
@@ -341,31 +424,34 @@ __global__ void __launch_bounds__(kUpWaves * 64)
 }
 
 template <int DT, int KS, int OPS, int A>
-void launch_up(const Args& a, const Plan* plans, hipStream_t st) {
+void launch_up(const Args& a, const void* order, hipStream_t st) {
   const int tiles = (a.V + 16 * kTiles - 1) / (16 * kTiles);
   const int blocks = (a.B + kRows - 1) / kRows;
   int groups_log2 = 0;
   while (groups_log2 < 6 && 1 << groups_log2 < a.B &&
          (int64_t)tiles * blocks << (groups_log2 + 1) <= kWavesWanted)
     ++groups_log2;
-  const dim3 grid((unsigned)((tiles + kUpWaves - 1) / kUpWaves), (unsigned)blocks << groups_log2);
+  const unsigned across = (unsigned)((tiles + kUpWaves - 1) / kUpWaves);
+  const unsigned parts = (unsigned)blocks << groups_log2;
+  const dim3 grid = a.B > kRows ? dim3(across * parts) : dim3(across, parts);
   const dim3 block(kUpWaves * 64);
   auto run = [&](auto* kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, groups_log2, plans);
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, (int)parts, groups_log2, order);
   };
-  if (a.B <= 16) run(up_kernel<DT, KS, OPS, 1, A>);
-  else if (a.B <= 32) run(up_kernel<DT, KS, OPS, 2, A>);
-  else run(up_kernel<DT, KS, OPS, 4, A>);
+  if (a.B <= 16) run(up_kernel<DT, KS, OPS, 1, A, false>);
+  else if (a.B <= 32) run(up_kernel<DT, KS, OPS, 2, A, false>);
+  else if (a.B <= kRows) run(up_kernel<DT, KS, OPS, 4, A, false>);
+  else run(up_kernel<DT, KS, OPS, 4, A, true>);
 }
 
 template <int DT>
-void launch_rank(const Args& a, const Plan* plans, hipStream_t st) {
-  if (a.rank <= 8) launch_up<DT, 1, 1, 2>(a, plans, st);
-  else if (a.rank <= 16) launch_up<DT, 1, 2, 2>(a, plans, st);
-  else if (a.rank <= 32) launch_up<DT, 1, kTerms, 1>(a, plans, st);
-  else if (a.rank <= 64) launch_up<DT, 2, 2 * kTerms, 1>(a, plans, st);
-  else if (a.rank <= 96) launch_up<DT, 3, 3 * kTerms, 1>(a, plans, st);
-  else launch_up<DT, 4, 4 * kTerms, 1>(a, plans, st);
+void launch_rank(const Args& a, const void* order, hipStream_t st) {
+  if (a.rank <= 8) launch_up<DT, 1, 1, 2>(a, order, st);
+  else if (a.rank <= 16) launch_up<DT, 1, 2, 2>(a, order, st);
+  else if (a.rank <= 32) launch_up<DT, 1, kTerms, 1>(a, order, st);
+  else if (a.rank <= 64) launch_up<DT, 2, 2 * kTerms, 1>(a, order, st);
+  else if (a.rank <= 96) launch_up<DT, 3, 3 * kTerms, 1>(a, order, st);
+  else launch_up<DT, 4, 4 * kTerms, 1>(a, order, st);
 }
 
 size_t low_bytes(int64_t B, int64_t rank) {
@@ -375,20 +461,31 @@ size_t low_bytes(int64_t B, int64_t rank) {
 }  // namespace
 
 size_t workspace_bytes(int64_t B, int64_t rank) {
-  return low_bytes(B, rank) + (size_t)((B + kRows - 1) / kRows) * sizeof(Plan);
+  // a plan is larger than the order of 64 rows; sizes grow with B
+  return low_bytes(B, rank) + sizeof(Plan) + (B > kRows ? (size_t)B * sizeof(Place) : 0);
+}
+
+bool grid_fits(int64_t B, int64_t V) {
+  const int64_t parts = (V + 16 * kTiles * kUpWaves - 1) / (16 * kTiles * kUpWaves);
+  return parts * ((B + kRows - 1) / kRows) * kUpWaves * 64 < (int64_t)1 << 32;
 }
 
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
-  Plan* const plans = reinterpret_cast<Plan*>(a.low + low_bytes(a.B, a.rank));
+  void* const order = a.low + low_bytes(a.B, a.rank);
   const int places = places_of(a.rank), blocks = (a.B + kRows - 1) / kRows;
   const int64_t items = (int64_t)a.B * places;
   // one wave a workgroup where that spreads few waves over more compute units
   const int waves = items > 1024 ? 4 : 1;
-  hipLaunchKernelGGL(down_kernel, dim3((unsigned)(blocks + (items + waves - 1) / waves)),
-                     dim3(waves * 64), 0, st, a, places, operands_of(a.rank), blocks, plans);
+  const dim3 grid((unsigned)(blocks + (items + waves - 1) / waves)), block(waves * 64);
+  if (blocks > 1)  // 65 rows or more are more than 1024 items
+    hipLaunchKernelGGL((down_kernel<true>), grid, block, 0, st, a, places, operands_of(a.rank),
+                       blocks, order);
+  else
+    hipLaunchKernelGGL((down_kernel<false>), grid, block, 0, st, a, places, operands_of(a.rank),
+                       blocks, order);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
-  if (dtype == QS_F32) launch_rank<QS_F32>(a, plans, st);
-  else launch_rank<QS_BF16>(a, plans, st);
+  if (dtype == QS_F32) launch_rank<QS_F32>(a, order, st);
+  else launch_rank<QS_BF16>(a, order, st);
   return hipGetLastError();
 }
 

@@ -29,10 +29,13 @@ struct Args {
   const int32_t* index;      // [B]; -1: none
   const float* scale;        // [count], optional (NULL: 1)
   int32_t* status;           // [B]
-  uint8_t* low;              // workspace: the rows' low-rank coordinates
+  uint8_t* low;              // workspace: the rows' low-rank coordinates and order
 };
 
 size_t workspace_bytes(int64_t B, int64_t rank);
+// whether one workgroup per tiles and block of rows fits one launch grid (batches past
+// that, 2^37 logits, are larger than the memory)
+bool grid_fits(int64_t B, int64_t V);
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st);
 
 }  // namespace adapters

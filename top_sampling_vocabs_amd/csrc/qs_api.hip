@@ -738,6 +738,7 @@ int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V, int64
     return QS_ERR_INVALID_ARG;
   // in place only row for row: otherwise one row's writes meet another's reads
   if (out == logits && out_stride != row_stride) return QS_ERR_INVALID_ARG;
+  if (!ad::grid_fits(B, V)) return QS_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < ad::workspace_bytes(B, rank))
     return QS_ERR_WORKSPACE;
   ad::Args a;
