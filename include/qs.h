@@ -642,9 +642,11 @@ QS_API int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, in
  * workspace    qs_adapters_workspace_bytes(B, rank) bytes of device scratch, 256-byte
  *              aligned, as for qs_filter_mask
  * Sums are held in float32; each logit is rounded once. A row's result depends on its
- * own hidden state, logits and adapter alone. The same call gives the same bits. Made
- * for the 1 to 64 rows of a decode step; more rows read each used adapter about once per
- * 64 rows that use it. Two kernel launches on `stream`; nothing is allocated. */
+ * own hidden state, logits and adapter alone; an infinity among them gives what the
+ * formula does, but one in up only a logit that is not finite (infinite or NaN). The
+ * same call gives the same bits. Made for the 1 to 64 rows of a decode step; more rows
+ * read each used adapter about once per 64 rows that use it. Two kernel launches on
+ * `stream`; nothing is allocated. */
 QS_API size_t qs_adapters_workspace_bytes(int64_t B, int64_t rank);
 QS_API int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V,
                       int64_t row_stride, const void* hidden, int64_t K,

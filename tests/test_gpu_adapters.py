@@ -225,6 +225,49 @@ def test_rows_do_not_meet(qs, dtype):
             assert np.array_equal(got[b], want[b], equal_nan=True), b
 
 
+@pytest.mark.parametrize("rank", [8, 16, 24, 40, 128])
+def test_infinite_coordinates(qs, rank):
+    """An infinite coordinate times the factors is what the formula says: infinities, and
+    NaN where they cancel or meet a 0."""
+    B, V, K, count = 3, 70, 64, 2
+    z, x, down, up, scale, index = inputs(rank, B, V, K, rank, count)
+    index[:] = [0, 1, -1]
+    x[0, 5] = np.inf          # with factors of either sign
+    scale[1] = np.inf
+    up[:, :30] = np.abs(up[:, :30])
+    up[:, 30:60] = -np.abs(up[:, 30:60])
+    up[0, 3, rank // 2] = 0
+    down[0, :, 5] = 0.5
+    down[1] = np.abs(down[1])
+    x[1] = np.abs(x[1])
+    got, status = run(qs, z, "f32", x, down, up, scale, index)
+    assert (status.cpu() == 0).all()
+    got = got.cpu().numpy()
+    for b in (0, 1):
+        assert (got[b, 30:60] == -np.inf).all(), b
+        assert (np.delete(got[b, :30], 3) == np.inf).all(), b
+        with np.errstate(invalid="ignore"):
+            mixed = up[b, 60:].astype(np.float64) @ np.full(rank, np.inf)
+        assert np.array_equal(got[b, 60:].astype(np.float64), mixed, equal_nan=True), b
+    assert np.isnan(got[0, 3]) and got[1, 3] == np.inf
+    assert np.array_equal(got[2], z[2])
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_largest_coordinates(qs, rank, sign):
+    """Coordinates past the largest bf16 number: 2^127 (1 + 255/256 + 1/512)."""
+    B, V, K, count = 2, 40, 16, 1
+    z, x, down, up, scale, index = inputs(9, B, V, K, rank, count)
+    x[:], down[:] = 0, 0
+    x[:, 0], x[:, 1] = sign * 2.0 ** 127, sign * 2.0 ** 120
+    down[:, :, 0], down[:, :, 1] = 1.9921875, 0.75
+    up = half(up * 2.0 ** -126)
+    index[:] = 0
+    got, _ = run(qs, z, "f32", x, down, up, None, index)
+    check(z, "f32", x, down, up, None, index, got)
+
+
 def test_same_bits(qs):
     """Twice the same call; and a row's bits whatever rows are beside it, how many there
     are, and where it stands among them."""

@@ -214,9 +214,11 @@ __global__ void __launch_bounds__(256)
     const int to = operands == 1 ? (q < 8 ? k : 3)
                    : operands == 2 ? (q < 16 ? 2 * k + g : 4 + g)
                                    : (g >> 2) * 4 * kTerms + 4 * k + (g & 3);
-    const __bf16 part = (__bf16)u;
-    *reinterpret_cast<__bf16*>(out + to * 256) = part;
-    u -= (float)part;
+    // the upper half of the bits: rounded it could pass the largest number
+    const uint32_t part = __float_as_uint(u) & 0xFFFF0000u;
+    *reinterpret_cast<uint16_t*>(out + to * 256) = (uint16_t)(part >> 16);
+    // an infinity's (or NaN's) other terms are 0, so that its products are the formula's
+    u = fabsf(u) < INFINITY ? u - __uint_as_float(part) : 0.0f;
   }
 }
 
