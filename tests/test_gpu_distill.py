@@ -675,6 +675,25 @@ def test_refusals(qs):
             qs.distill_loss_backward(dual, *back[1:])
 
 
+def test_temperature_gets_no_gradient(qs):
+    """A temperature that asks for a gradient is refused, not left without one; outside
+    of grad mode it is a number like any other."""
+    import torch
+    lg = torch.randn(2, 64, device="cuda")
+    ids = torch.arange(4, dtype=torch.int32, device="cuda").repeat(2, 1)
+    val = torch.zeros(2, 4, device="cuda")
+    T = torch.full((2,), 0.7, device="cuda", requires_grad=True)
+    for z in (lg, lg.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="temperature"):
+            qs.distill_loss(z, ids, val, temperature=T)
+    want = qs.distill_loss(lg, ids, val, temperature=T.detach())
+    with torch.no_grad():
+        got = qs.distill_loss(lg, ids, val, temperature=T)
+        qs.distill_loss_backward(lg, ids, val, got["state"], got["status"],
+                                 torch.ones(2, device="cuda"), temperature=T)
+    assert torch.equal(got["loss"], want["loss"])
+
+
 def test_empty_batch(qs):
     import torch
     for V in (64, 70016):

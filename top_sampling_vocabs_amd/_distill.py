@@ -31,8 +31,11 @@ def _check_inputs(logits, teacher_ids, teacher_values, temperature, bitmask):
             or teacher_values.get_device() != index or not teacher_values.is_contiguous():
         raise ValueError("teacher_values must be a contiguous float32 tensor in the shape of "
                          f"teacher_ids on cuda:{index}")
-    if teacher_values.requires_grad and torch.is_grad_enabled():
-        raise ValueError("the teacher gets no gradient: detach teacher_values")
+    if torch.is_grad_enabled():
+        if teacher_values.requires_grad:
+            raise ValueError("the teacher gets no gradient: detach teacher_values")
+        if temperature is not None and temperature.requires_grad:
+            raise ValueError("temperature gets no gradient: detach it")
     return B, V, teacher_ids.size(1), index
 
 
@@ -63,8 +66,9 @@ def distill_loss(logits, teacher_ids, teacher_values, *, temperature=None, bitma
     tokens. rest=True: they are its log-probabilities (token_logprobs' top_ids and
     top_logprobs are such lists), and the probability that they leave is compared
     with what the student gives all other tokens. Returns a dict of device tensors:
-    loss [B], status [B] and state [B, 8] (for distill_loss_backward). Enqueued on the
-    current stream.
+    loss [B] (NaN on rows whose status is not ROW_OK: leave them out of a sum),
+    status [B] and state [B, 8] (for distill_loss_backward). Enqueued on the current
+    stream.
 
     If logits require a gradient, loss carries it (to the logits only; a second
     derivative and forward mode are not available). To capture a training step in a
