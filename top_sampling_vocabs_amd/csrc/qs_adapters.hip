@@ -24,13 +24,17 @@
 //
 // Measured (first and second launch): 64 rows of 151936 bf16 on adapters of their own of
 // rank 32, 8192 columns, 10.5 and 116 us (5.7 TB/s in the second, where a large copy
-// reaches 5.2); on three of rank 64, 4096 columns, 5.7 and 20.4 us (4.8 TB/s); 16 rows of
-// 128256 fp32, each its own of rank 32, 4.0 and 24 us (6.1 TB/s); 1 row of 151936, rank
-// 16, 3.4 and 4.0 us, two dependent loads each. Both together, 151936 bf16, 2048 columns:
-// 2048 rows on one adapter of rank 16 324 us, on 64 of them 460 (3.9 and 3.4 TB/s).
+// reaches 5.2); on three of rank 64, 4096 columns, 5.6 and 18.5 us (5.3 TB/s); 16 rows of
+// 128256 fp32, each its own of rank 32, 4.0 and 22.6 us (6.4 TB/s); 1 row of 151936, rank
+// 16, 3.4 and 3.8 us, two dependent loads each. Both together, 151936 bf16, 2048 columns:
+// 512 rows on 8 and 64 adapters of rank 16 103 and 136 us, 2048 rows on one and 64 of them
+// 296 and 362 (4.2 and 4.3 TB/s), on 4 of rank 64 436 (3.1 TB/s: the products and the
+// coordinates' way to them).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "../../include/qs.h"
 #include "qs_adapters.hpp"
@@ -43,15 +47,18 @@ namespace {
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 64;         // batch rows of a block
-constexpr int kNone = 0x7FFF;     // in place of an adapter's number
+constexpr int kNone = 0x1FFF;     // in place of an adapter's number
+constexpr int kRowBits = 18;      // of a row's number beside an adapter's
 constexpr int kTerms = 3;         // bf16 numbers per coordinate
 constexpr int kUpWaves = 4;
 constexpr int kTiles = 2;         // tiles of 16 vocabulary rows per wave
 constexpr int kWavesWanted = 4096;  // up to which a block's adapters are dealt out
 constexpr int kAhead = 8;         // loads of 512 columns that a wave of the first product
                                   // requests at a time
+constexpr int kWideRanks = 4;     // ranks per wave of it in larger batches
 
 // The workspace holds, per tile of 16 batch rows, the coordinates as the second
 // product's operands: lane (row n, group g) of an operand has 8 bf16 numbers at 16 g + n.
@@ -153,8 +160,11 @@ __device__ __forceinline__ void place_rows(const Args& a, int row0, Place* order
 // it uses any, and rows that share an adapter read it from the L2. (On the matrix cores,
 // 16 ranks and the rows that share an adapter to a workgroup: 1 row of 4096 columns, rank
 // 16, 6.5 us, one compute unit's loads, against 3.5; 64 rows of 8192 on adapters of their
-// own, rank 32, 14.2 against 10.7; 64 on 3 of rank 64, 4096 columns, 7.9 against 6.1.
-// Four ranks a wave, which reads the hidden state once for them, were up to 2 us slower.)
+// own, rank 32, 14.2 against 10.7; 64 on 3 of rank 64, 4096 columns, 7.9 against 6.1.)
+// Four ranks a wave, which reads the hidden state once for them, were up to 2 us slower
+// there, but larger batches are bound by what the L2 gives: 2048 rows of 2048 columns on 4
+// adapters of rank 64 have 502 us in all with one rank a wave, 468 with two, 459 with four,
+// 457 with eight; 2048 rows of 32000 on 8 of rank 16 114, 96, 94 and 94.
 template <bool WIDE>
 __global__ void __launch_bounds__(256)
     down_kernel(Args a, int places, int operands, int blocks, void* order) {
@@ -164,47 +174,77 @@ __global__ void __launch_bounds__(256)
     else if (threadIdx.x < 64) write_plan(a, static_cast<Plan*>(order));
     return;
   }
+  constexpr int R = WIDE ? kWideRanks : 1, kLoads = kAhead / R;
   const int item =
       uni((int)((blockIdx.x - blocks) * (blockDim.x >> 6) + (threadIdx.x >> 6)));
-  const int b = item / places, q = item - b * places;
+  const int b = item / (places / R), q0 = (item - b * (places / R)) * R;
   if (b >= a.B) return;
   const int n = a.index[b];
   if (n < 0 || n >= a.count) return;
   float u = 0.0f;
-  if (q < a.rank) {
+  int q = q0;  // the rank that u is of
+  if (q0 < a.rank) {
     const float scale = a.scale ? a.scale[n] : 1.0f;
     const uint16_t* const x = a.hidden + (size_t)b * a.hidden_stride;
     const uint16_t* const d =
-        a.down + (size_t)n * a.down_stride + (size_t)q * a.down_row_stride;
-    float sum[2] = {0.0f, 0.0f};
-    for (int k0 = lane * 8; k0 < a.K; k0 += kAhead * 512) {
-      uint4 dv[kAhead], xv[kAhead];
+        a.down + (size_t)n * a.down_stride + (size_t)q0 * a.down_row_stride;
+    float sum[R][2];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        dv[j] = xv[j] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < R; ++i) sum[i][0] = sum[i][1] = 0.0f;
+    for (int k0 = lane * 8; k0 < a.K; k0 += kLoads * 512) {
+      uint4 dv[R][kLoads], xv[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        xv[j] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < R; ++i) dv[i][j] = make_uint4(0u, 0u, 0u, 0u);
         if (k0 + j * 512 < a.K) {
-          dv[j] = *reinterpret_cast<const uint4*>(d + k0 + j * 512);
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+            dv[i][j] = *reinterpret_cast<const uint4*>(d + (size_t)i * a.down_row_stride + k0 +
+                                                       j * 512);
           xv[j] = *reinterpret_cast<const uint4*>(x + k0 + j * 512);
         }
       }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const uint32_t ds[4] = {dv[j].x, dv[j].y, dv[j].z, dv[j].w};
+      for (int j = 0; j < kLoads; ++j) {
         const uint32_t xs[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum[0] = fmaf(__uint_as_float(ds[e] << 16), __uint_as_float(xs[e] << 16), sum[0]);
-          sum[1] = fmaf(__uint_as_float(ds[e] & 0xFFFF0000u), __uint_as_float(xs[e] & 0xFFFF0000u),
-                        sum[1]);
+        for (int i = 0; i < R; ++i) {
+          const uint32_t ds[4] = {dv[i][j].x, dv[i][j].y, dv[i][j].z, dv[i][j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[i][0] = fmaf(__uint_as_float(ds[e] << 16), __uint_as_float(xs[e] << 16), sum[i][0]);
+            sum[i][1] = fmaf(__uint_as_float(ds[e] & 0xFFFF0000u),
+                             __uint_as_float(xs[e] & 0xFFFF0000u), sum[i][1]);
+          }
         }
       }
     }
-    u = sum[0] + sum[1];
+    float v[R];
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) u += __shfl_xor(u, off, 64);
+    for (int i = 0; i < R; ++i) v[i] = sum[i][0] + sum[i][1];
+    // summed over the lanes, of several ranks each half of the lanes going on with half of
+    // them; the same pairs for any R, so a row's bits are the same in any batch
+    int off = 32;
+#pragma unroll
+    for (int left = R / 2; left > 0; left >>= 1, off >>= 1) {
+      const bool upper = (lane & off) != 0;
+#pragma unroll
+      for (int i = 0; i < left; ++i) {
+        const float other = __shfl_xor(upper ? v[i] : v[i + left], off, 64);
+        v[i] = (upper ? v[i + left] : v[i]) + other;
+      }
+      q += upper ? left : 0;
+    }
+    u = v[0];
+#pragma unroll
+    for (int o = 32 / R; o > 0; o >>= 1) u += __shfl_xor(u, o, 64);
     u *= scale;
+  } else {
+    q += lane / (64 / R);
   }
-  if (lane != 0) return;
+  if ((lane & (64 / R - 1)) != 0) return;
   uint8_t* const out =
       a.low + (size_t)(b / 16) * operands * kOperandBytes + (b & 15) * 16 + (q & 7) * 2;
   // the group (of all operands' groups) that holds the coordinate's term k
@@ -238,24 +278,28 @@ __global__ void __launch_bounds__(256)
 // us against 26.6 in one group, 8000 10.1 against 32, 32000 18.8 against 34, 64000 28.4
 // against 37). Past kWavesWanted that costs more than it gives (64000 tokens in four
 // groups 30.6, 128256 in two 57.0 against 55.7).
+//
+// A workgroup requests the coordinates, and then its logits, all at once: one after
+// another, as a loop over them came out, they were a chain of up to 12 loads (64 rows on 3
+// adapters of rank 64: 24.9 us against 23.4 for both launches; on 64 of rank 16, 128256
+// tokens, 55.5 against 52.9).
 template <int DT, int KS, int OPS, int RT, int A, bool WIDE>
 __global__ void __launch_bounds__(kUpWaves * 64)
-    up_kernel(Args a, int tiles, int parts, int groups_log2, const void* order) {
+    up_kernel(Args a, int tiles, int turns, int groups_log2, const void* order) {
   constexpr int kSpan = 16 * kTiles;      // vocabulary rows per wave
   constexpr int P = DT == QS_F32 ? 4 : 8; // logits per 16 bytes
-  __shared__ uint4 s_low[RT * OPS * 64];
+  constexpr int kLow = RT * OPS * 64, kParts = (kLow + kUpWaves * 64 - 1) / (kUpWaves * 64);
+  __shared__ uint4 s_low[kLow];
+  uint4 part_low[kParts];  // this thread's share of the coordinates on their way there
   const int tid = threadIdx.x, lane = lane_id(), w = uni(tid >> 6);
   const int n = lane & 15, kg = lane >> 4;
-  // of many blocks those of a tile beside each other, so that factors that several of
-  // them read are in the L2
-  const int part = WIDE ? (int)(blockIdx.x % (unsigned)parts) : (int)blockIdx.y;
+  const int part = (int)blockIdx.y;
   const int group = part & ((1 << groups_log2) - 1), row0 = (part >> groups_log2) * kRows;
-  const int tile =
-      (WIDE ? (int)(blockIdx.x / (unsigned)parts) : (int)blockIdx.x) * kUpWaves + w;
-  const int v0 = tile * kSpan, first = v0 + kg * 4 * kTiles;  // the lane's first logit
+  int tile = (int)blockIdx.x * turns * kUpWaves + w;
   const int rows = min(a.B - row0, kRows);
   const uint4* const low = reinterpret_cast<const uint4*>(a.low);
   const bool copies = group == 0 && a.out != a.logits;  // the rows without an adapter
+  auto row_of = [](int mine) { return mine & ((1 << kRowBits) - 1); };
   auto of_group = [&](int number) { return (number & ((1 << groups_log2) - 1)) == group; };
   // the lane's place in the order: its row and its adapter's number in the block (-1: not
   // this workgroup's row, kNone: no adapter); the lane's adapter and the places it has
@@ -268,8 +312,7 @@ __global__ void __launch_bounds__(kUpWaves * 64)
     // the coordinates as they lie
     const int items = (rows + 15) / 16 * OPS * 64;
 #pragma unroll
-    for (int i0 = 0; i0 < RT * OPS * 64; i0 += kUpWaves * 64)
-      if (i0 + tid < items) s_low[i0 + tid] = low[i0 + tid];
+    for (int k = 0; k < kParts; ++k) part_low[k] = low[min(k * kUpWaves * 64 + tid, items - 1)];
     adapters = __popcll(ballot(span != 0));
     mine_row = p < 0 ? 0 : p & 0xFFFF;
     mine_number = p >> 16;
@@ -294,134 +337,161 @@ __global__ void __launch_bounds__(kUpWaves * 64)
     adapter = s_adapter[lane];
     span = s_span[lane];
   }
-  if (group >= adapters && !copies) return;
   if (mine_number == kNone ? !copies : !of_group(mine_number)) mine_number = -1;
   if constexpr (WIDE) {  // the coordinates from where they lie
-    for (int i0 = 0; i0 < RT * OPS * 64; i0 += kUpWaves * 64) {
-      const int i = i0 + tid, t = i / (OPS * 64), o = (i >> 6) % OPS;
-      const int r = __shfl(mine_row, t * 16 + (i & 15), 64);
-      const int number = __shfl(mine_number, t * 16 + (i & 15), 64);
-      if (number >= 0 && number != kNone)
-        s_low[i] = low[((size_t)(r >> 4) * OPS + o) * 64 + (lane & 48) + (r & 15)];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const int i = k * kUpWaves * 64 + tid, o = (i >> 6) % OPS;
+      const int r = __shfl(mine_row, i / (OPS * 64) * 16 + (i & 15), 64);
+      part_low[k] = low[((size_t)(r >> 4) * OPS + o) * 64 + (lane & 48) + (r & 15)];
     }
     static_assert(RT == 4, "whole turns");
   }
 
   // this lane's batch rows, in that order, and their logits
-  int row[RT], number[RT], place[RT];
+  int mine[RT], place[RT];  // row | adapter's number in the block << kRowBits
   f32x4 y[kTiles][RT];
+  int v0, first;  // the tile's and the lane's first logit
+  auto load_logits = [&](auto start) {
+    v0 = tile * kSpan;
+    first = v0 + kg * 4 * kTiles;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    row[t] = __shfl(mine_row, t * 16 + n, 64);
-    number[t] = __shfl(mine_number, t * 16 + n, 64);
-    place[t] = WIDE ? t * OPS * 64 + lane
-                    : (row[t] >> 4) * OPS * 64 + kg * 16 + (row[t] & 15);  // of its coordinates
-    const bool here = number[t] >= 0;
-    const uint8_t* const z = a.logits + (size_t)(here ? row[t] : 0) * a.row_bytes;
+    for (int t = 0; t < RT; ++t) {
+      if constexpr (start) {
+        mine[t] = __shfl(mine_row | mine_number << kRowBits, t * 16 + n, 64);
+        place[t] = WIDE ? t * OPS * 64 + lane  // of its coordinates
+                        : (row_of(mine[t]) >> 4) * OPS * 64 + kg * 16 + (mine[t] & 15);
+      } else {
+        // worked out again in every turn: the rows' addresses held from one to the next
+        // cost a wave of five
+        asm volatile("" : "+v"(mine[t]));
+      }
+      // lanes without a row keep what their registers hold (never stored): a value of their
+      // own would make the requests wait for one another
+      u32x4 q[4 * kTiles / P];
 #pragma unroll
-    for (int c = 0; c < 4 * kTiles / P; ++c) {
-      uint4 q = make_uint4(0u, 0u, 0u, 0u);
-      if (here && first + c * P < a.V)
-        q = *reinterpret_cast<const uint4*>(z + (size_t)(first + c * P) * (16 / P));
-      const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+      for (int c = 0; c < 4 * kTiles / P; ++c) q[c] = __builtin_nondeterministic_value(q[c]);
+      if (mine[t] >= 0) {
+        const uint8_t* const z = a.logits + (size_t)row_of(mine[t]) * a.row_bytes;
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        const int i = c * P + e;
-        if constexpr (DT == QS_F32) y[i >> 2][t][i & 3] = __uint_as_float(word[e]);
-        else y[i >> 2][t][i & 3] =
-            __uint_as_float((e & 1) ? word[e >> 1] & 0xFFFF0000u : word[e >> 1] << 16);
+        for (int c = 0; c < 4 * kTiles / P; ++c) {
+          const int v = first + c * P < a.V ? first + c * P : 0;
+          q[c] = *reinterpret_cast<const u32x4*>(z + (size_t)v * (16 / P));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4 * kTiles / P; ++c) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const int i = c * P + e;
+          if constexpr (DT == QS_F32) y[i >> 2][t][i & 3] = __uint_as_float(q[c][e]);
+          else y[i >> 2][t][i & 3] =
+              __uint_as_float((e & 1) ? q[c][e >> 1] & 0xFFFF0000u : q[c][e >> 1] << 16);
+        }
       }
     }
+  };
+  load_logits(std::true_type{});
+  // not earlier: this workgroup's loads would wait for the answer
+  if (group >= adapters && !copies) return;
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) {
+    const int i = k * kUpWaves * 64 + tid;
+    if (kLow % (kUpWaves * 64) == 0 || i < kLow) s_low[i] = part_low[k];
   }
   __syncthreads();
-  if (tile >= tiles) return;
-
-  for (int i0 = group; i0 < adapters; i0 += A << groups_log2) {
-    int at[A], end[A];
-    bf16x8 f[A][kTiles][KS];
+  for (;;) {
+    if (tile >= tiles) return;
+    for (int i0 = group; i0 < adapters; i0 += A << groups_log2) {
+      int at[A], end[A];
+      bf16x8 f[A][kTiles][KS];
 #pragma unroll
-    for (int j = 0; j < A; ++j) {
-      const int i = i0 + (j << groups_log2);
-      at[j] = end[j] = 0;
-      if (i >= adapters) continue;
-      const int where = (int)readlane_u32((uint32_t)span, i);
-      at[j] = where & 0xFFFF;
-      end[j] = where >> 16;
-      const uint16_t* const up = a.up + (size_t)readlane_u32((uint32_t)adapter, i) * a.up_stride;
-#pragma unroll
-      for (int k = 0; k < kTiles; ++k) {
-        const int v = min(v0 + (n >> 2) * 4 * kTiles + k * 4 + (n & 3), a.V - 1);
-        const uint16_t* const r = up + (size_t)v * a.up_row_stride;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          // groups beside the terms' read the same ranks again
-          const int c = OPS == 1 ? 0 : OPS == 2 ? (kg & 1) * 8 : s * 32 + kg * 8;
-          uint4 q = make_uint4(0u, 0u, 0u, 0u);
-          if (c < a.rank) q = *reinterpret_cast<const uint4*>(r + c);
-          f[j][k][s] = __builtin_bit_cast(bf16x8, q);
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < A; ++j) {
-      const int i = i0 + (j << groups_log2);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        if (t * 16 >= end[j] || t * 16 + 16 <= at[j]) continue;
-        f32x4 acc[kTiles];
-#pragma unroll
-        for (int k = 0; k < kTiles; ++k) acc[k] = y[k][t];
-#pragma unroll
-        for (int o = 0; o < OPS; ++o) {
-          const bf16x8 u = __builtin_bit_cast(bf16x8, s_low[place[t] + o * 64]);
-#pragma unroll
-          for (int k = 0; k < kTiles; ++k)
-            acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][k][OPS <= 2 ? 0 : o / kTerms], u,
-                                                             acc[k], 0, 0, 0);
-        }
-        const bool take = number[t] == i;
+      for (int j = 0; j < A; ++j) {
+        const int i = i0 + (j << groups_log2);
+        at[j] = end[j] = 0;
+        if (i >= adapters) continue;
+        const int where = (int)readlane_u32((uint32_t)span, i);
+        at[j] = where & 0xFFFF;
+        end[j] = where >> 16;
+        const uint16_t* const up = a.up + (size_t)readlane_u32((uint32_t)adapter, i) * a.up_stride;
 #pragma unroll
         for (int k = 0; k < kTiles; ++k) {
+          const int v = min(v0 + (n >> 2) * 4 * kTiles + k * 4 + (n & 3), a.V - 1);
+          const uint16_t* const r = up + (size_t)v * a.up_row_stride;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[k][t][e] = take ? acc[k][e] : y[k][t][e];
+          for (int s = 0; s < KS; ++s) {
+            // groups beside the terms' or past the rank read others' ranks again: their
+            // coordinates are 0
+            const int at_rank = OPS == 1 ? 0 : OPS == 2 ? (kg & 1) * 8 : s * 32 + kg * 8;
+            const uint4 q = *reinterpret_cast<const uint4*>(r + (at_rank < a.rank ? at_rank : 0));
+            f[j][k][s] = __builtin_bit_cast(bf16x8, q);
+          }
         }
       }
-    }
-  }
-
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    if (number[t] < 0) continue;
-    uint8_t* const out = a.out + (size_t)row[t] * a.out_bytes;
+      for (int j = 0; j < A; ++j) {
+        const int i = i0 + (j << groups_log2);
 #pragma unroll
-    for (int c = 0; c < 4 * kTiles / P; ++c) {
-      const int v = first + c * P;
-      if (v >= a.V) break;
-      uint32_t word[4];
-      if constexpr (DT == QS_F32) {
+        for (int t = 0; t < RT; ++t) {
+          if (t * 16 >= end[j] || t * 16 + 16 <= at[j]) continue;
+          f32x4 acc[kTiles];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) word[e] = __float_as_uint(y[c][t][e]);
-      } else {
+          for (int k = 0; k < kTiles; ++k) acc[k] = y[k][t];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bf16x4 half = __builtin_convertvector(y[c * 2 + h][t], bf16x4);
-          __builtin_memcpy(word + 2 * h, &half, 8);
-        }
-      }
-      if (a.V - v >= P) {
-        *reinterpret_cast<uint4*>(out + (size_t)v * (16 / P)) =
-            make_uint4(word[0], word[1], word[2], word[3]);
-      } else {  // the row's last logits: what lies behind them stays
+          for (int o = 0; o < OPS; ++o) {
+            const bf16x8 u = __builtin_bit_cast(bf16x8, s_low[place[t] + o * 64]);
 #pragma unroll
-        for (int e = 0; e < P - 1; ++e) {
-          if (v + e < a.V) {
-            if constexpr (DT == QS_F32) reinterpret_cast<uint32_t*>(out)[v + e] = word[e];
-            else reinterpret_cast<uint16_t*>(out)[v + e] =
-                (uint16_t)(word[e >> 1] >> (16 * (e & 1)));
+            for (int k = 0; k < kTiles; ++k)
+              acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][k][OPS <= 2 ? 0 : o / kTerms], u,
+                                                               acc[k], 0, 0, 0);
+          }
+          const bool take = mine[t] >> kRowBits == i;
+#pragma unroll
+          for (int k = 0; k < kTiles; ++k) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[k][t][e] = take ? acc[k][e] : y[k][t][e];
           }
         }
       }
     }
+
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      if (mine[t] < 0) continue;
+      uint8_t* const out = a.out + (size_t)row_of(mine[t]) * a.out_bytes;
+#pragma unroll
+      for (int c = 0; c < 4 * kTiles / P; ++c) {
+        const int v = first + c * P;
+        if (v >= a.V) break;
+        uint32_t word[4];
+        if constexpr (DT == QS_F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) word[e] = __float_as_uint(y[c][t][e]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bf16x4 half = __builtin_convertvector(y[c * 2 + h][t], bf16x4);
+            __builtin_memcpy(word + 2 * h, &half, 8);
+          }
+        }
+        if (a.V - v >= P) {
+          *reinterpret_cast<uint4*>(out + (size_t)v * (16 / P)) =
+              make_uint4(word[0], word[1], word[2], word[3]);
+        } else {  // the row's last logits: what lies behind them stays
+#pragma unroll
+          for (int e = 0; e < P - 1; ++e) {
+            if (v + e < a.V) {
+              if constexpr (DT == QS_F32) reinterpret_cast<uint32_t*>(out)[v + e] = word[e];
+              else reinterpret_cast<uint16_t*>(out)[v + e] =
+                  (uint16_t)(word[e >> 1] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+    }
+    if (!WIDE || --turns == 0) return;
+    tile += kUpWaves;
+    load_logits(std::false_type{});
   }
 }
 
@@ -433,12 +503,23 @@ void launch_up(const Args& a, const void* order, hipStream_t st) {
   while (groups_log2 < 6 && 1 << groups_log2 < a.B &&
          (int64_t)tiles * blocks << (groups_log2 + 1) <= kWavesWanted)
     ++groups_log2;
-  const unsigned across = (unsigned)((tiles + kUpWaves - 1) / kUpWaves);
-  const unsigned parts = (unsigned)blocks << groups_log2;
-  const dim3 grid = a.B > kRows ? dim3(across * parts) : dim3(across, parts);
+  // Of many rows a workgroup takes several tiles per wave one after another, so that the
+  // order and the coordinates (rank 64: 24 KiB for 16 KiB of bf16 logits) are fetched once
+  // for them, as long as enough workgroups are left. (2048 rows of 151936 on 4 adapters of
+  // rank 64, 38000 workgroups: 487 us with 1 tile, 459 with 2, 438 with 4; on 64 of rank 16
+  // 421, 392, 396; 256 rows of 32000 on 8 of rank 128, 1000 workgroups, 40, 34, 35; 128 rows
+  // of 151936 on 64 of rank 16, 2374 workgroups, 83, 87, 104.)
+  int turns = 1;
+  if (a.B > kRows) {
+    const int64_t workgroups = (int64_t)((tiles + kUpWaves - 1) / kUpWaves) * blocks;
+    if (a.rank > 32) turns = workgroups >= 4000 ? 4 : workgroups >= 1000 ? 2 : 1;
+    else turns = workgroups >= 4000 ? 2 : 1;
+  }
+  const int each = kUpWaves * turns;
+  const dim3 grid((unsigned)((tiles + each - 1) / each), (unsigned)blocks << groups_log2);
   const dim3 block(kUpWaves * 64);
   auto run = [&](auto* kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, (int)parts, groups_log2, order);
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles, turns, groups_log2, order);
   };
   if (a.B <= 16) run(up_kernel<DT, KS, OPS, 1, A, false>);
   else if (a.B <= 32) run(up_kernel<DT, KS, OPS, 2, A, false>);
@@ -475,11 +556,11 @@ bool grid_fits(int64_t B, int64_t V) {
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
   void* const order = a.low + low_bytes(a.B, a.rank);
   const int places = places_of(a.rank), blocks = (a.B + kRows - 1) / kRows;
-  const int64_t items = (int64_t)a.B * places;
+  const int64_t items = (int64_t)a.B * places / (a.B > kRows ? kWideRanks : 1);
   // one wave a workgroup where that spreads few waves over more compute units
-  const int waves = items > 1024 ? 4 : 1;
+  const int waves = items > 1024 || a.B > kRows ? 4 : 1;
   const dim3 grid((unsigned)(blocks + (items + waves - 1) / waves)), block(waves * 64);
-  if (blocks > 1)  // 65 rows or more are more than 1024 items
+  if (a.B > kRows)
     hipLaunchKernelGGL((down_kernel<true>), grid, block, 0, st, a, places, operands_of(a.rank),
                        blocks, order);
   else
