@@ -52,6 +52,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kRows = 64;         // batch rows of a block
 constexpr int kNone = 0x1FFF;     // in place of an adapter's number
 constexpr int kRowBits = 18;      // of a row's number beside an adapter's
+static_assert(kMaxB <= 1 << kRowBits && kNone < 1 << (31 - kRowBits), "in 31 bits");
 constexpr int kTerms = 3;         // bf16 numbers per coordinate
 constexpr int kUpWaves = 4;
 constexpr int kTiles = 2;         // tiles of 16 vocabulary rows per wave
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(kUpWaves * 64)
             const bf16x8 u = __builtin_bit_cast(bf16x8, s_low[place[t] + o * 64]);
 #pragma unroll
             for (int k = 0; k < kTiles; ++k)
-              acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][k][OPS <= 2 ? 0 : o / kTerms], u,
-                                                               acc[k], 0, 0, 0);
+              acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  f[j][k][OPS <= 2 ? 0 : o / kTerms], u, acc[k], 0, 0, 0);
           }
           const bool take = mine[t] >> kRowBits == i;
 #pragma unroll
