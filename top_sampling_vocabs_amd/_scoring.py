@@ -90,7 +90,7 @@ def _check_row_inputs(logits, tokens, temperature, bitmask):
 def _padded_rows(B, V, dtype, device):
     """[B, V] uninitialised, rows starting 16 bytes aligned."""
     width = V + -V % (4 if dtype is torch.float32 else 8)
-    t = torch.empty((B, width), dtype=dtype, device=device)
+    t = torch.empty(B, width, dtype=dtype, device=device)
     return t if width == V else t.as_strided((B, V), (width, 1))
 
 
