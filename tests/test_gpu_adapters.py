@@ -277,7 +277,8 @@ def test_same_bits(qs):
         a, _ = run(qs, z, "f32", x, down, up, scale, index)
         b, _ = run(qs, z, "f32", x, down, up, scale, index)
         assert torch.equal(a, b)
-        for rows in ([5], [77, 3], list(range(20, 40)), list(range(129, 80, -1))):
+        for rows in ([5], [77, 3], list(range(20, 40)), list(range(129, 80, -1)),
+                     list(range(60, 124))):
             few, _ = run(qs, z[rows], "f32", x[rows], down, up, scale, index[rows])
             assert torch.equal(few, a[rows]), (rank, rows)
 

@@ -24,7 +24,7 @@
 //
 // Measured (first and second launch): 64 rows of 151936 bf16 on adapters of their own of
 // rank 32, 8192 columns, 10.5 and 116 us (5.7 TB/s in the second, where a large copy
-// reaches 5.2); on three of rank 64, 4096 columns, 5.6 and 18.5 us (5.3 TB/s); 16 rows of
+// reaches 5.2); on three of rank 64, 4096 columns, 5.8 and 18.3 us (5.3 TB/s); 16 rows of
 // 128256 fp32, each its own of rank 32, 4.0 and 22.6 us (6.4 TB/s); 1 row of 151936, rank
 // 16, 3.4 and 3.8 us, two dependent loads each. Both together, 151936 bf16, 2048 columns:
 // 512 rows on 8 and 64 adapters of rank 16 103 and 136 us, 2048 rows on one and 64 of them
@@ -57,9 +57,9 @@ constexpr int kTerms = 3;         // bf16 numbers per coordinate
 constexpr int kUpWaves = 4;
 constexpr int kTiles = 2;         // tiles of 16 vocabulary rows per wave
 constexpr int kWavesWanted = 4096;  // up to which a block's adapters are dealt out
+constexpr int kManyCoordinates = 4096;  // from which a wave of the first product takes two
 constexpr int kAhead = 8;         // loads of 512 columns that a wave of the first product
                                   // requests at a time
-constexpr int kWideRanks = 4;     // ranks per wave of it in larger batches
 
 // The workspace holds, per tile of 16 batch rows, the coordinates as the second
 // product's operands: lane (row n, group g) of an operand has 8 bf16 numbers at 16 g + n.
@@ -156,17 +156,20 @@ __device__ __forceinline__ void place_rows(const Args& a, int row0, Place* order
   order[segment + (int)count] = Place{r, mine == 0x80000000u ? -1 : asked};
 }
 
-// The rows' coordinates, a wave to each row and rank: few rows spread over as many
+// The rows' coordinates, a wave to each row and rank or few ranks: few rows spread over as many
 // compute units as they have ranks, each wave requests up to 8 KiB of the factor before
 // it uses any, and rows that share an adapter read it from the L2. (On the matrix cores,
 // 16 ranks and the rows that share an adapter to a workgroup: 1 row of 4096 columns, rank
 // 16, 6.5 us, one compute unit's loads, against 3.5; 64 rows of 8192 on adapters of their
 // own, rank 32, 14.2 against 10.7; 64 on 3 of rank 64, 4096 columns, 7.9 against 6.1.)
-// Four ranks a wave, which reads the hidden state once for them, were up to 2 us slower
-// there, but larger batches are bound by what the L2 gives: 2048 rows of 2048 columns on 4
-// adapters of rank 64 have 502 us in all with one rank a wave, 468 with two, 459 with four,
-// 457 with eight; 2048 rows of 32000 on 8 of rank 16 114, 96, 94 and 94.
-template <bool WIDE>
+// A wave with R ranks reads the hidden state once for them. That leaves fewer waves to
+// wait for memory, but from 4096 coordinates on the L2's rate bounds the kernel: both
+// launches for 1000 tokens, 4096 columns, on 3 shared adapters, 64 rows of rank 32 7.6 us
+// with one rank a wave, 7.8 with two, 8.5 with four; of rank 64 9.2, 8.7 and 9.3; of rank
+// 128 12.2, 11.0 and 11.3; on 64 adapters of rank 32, 8192 columns, 13.5, 13.8 and 15.5.
+// Past 64 rows four: 2048 rows of 151936 tokens, 2048 columns, on 4 adapters of rank 64 502
+// us with one, 468 with two, 459 with four, 457 with eight.
+template <bool WIDE, int R>
 __global__ void __launch_bounds__(256)
     down_kernel(Args a, int places, int operands, int blocks, void* order) {
   const int lane = lane_id();
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(256)
     else if (threadIdx.x < 64) write_plan(a, static_cast<Plan*>(order));
     return;
   }
-  constexpr int R = WIDE ? kWideRanks : 1, kLoads = kAhead / R;
+  constexpr int kLoads = kAhead / R;
   const int item =
       uni((int)((blockIdx.x - blocks) * (blockDim.x >> 6) + (threadIdx.x >> 6)));
   const int b = item / (places / R), q0 = (item - b * (places / R)) * R;
@@ -557,16 +560,16 @@ bool grid_fits(int64_t B, int64_t V) {
 hipError_t launch_adapters(const Args& a, int dtype, hipStream_t st) {
   void* const order = a.low + low_bytes(a.B, a.rank);
   const int places = places_of(a.rank), blocks = (a.B + kRows - 1) / kRows;
-  const int64_t items = (int64_t)a.B * places / (a.B > kRows ? kWideRanks : 1);
-  // one wave a workgroup where that spreads few waves over more compute units
-  const int waves = items > 1024 || a.B > kRows ? 4 : 1;
-  const dim3 grid((unsigned)(blocks + (items + waves - 1) / waves)), block(waves * 64);
-  if (a.B > kRows)
-    hipLaunchKernelGGL((down_kernel<true>), grid, block, 0, st, a, places, operands_of(a.rank),
-                       blocks, order);
-  else
-    hipLaunchKernelGGL((down_kernel<false>), grid, block, 0, st, a, places, operands_of(a.rank),
-                       blocks, order);
+  auto run = [&](auto* kernel, int ranks) {
+    const int64_t items = (int64_t)a.B * places / ranks;
+    // one wave a workgroup where that spreads few waves over more compute units
+    const int waves = items > 1024 || a.B > kRows ? 4 : 1;
+    const dim3 grid((unsigned)(blocks + (items + waves - 1) / waves)), block(waves * 64);
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, a, places, operands_of(a.rank), blocks, order);
+  };
+  if (a.B > kRows) run(down_kernel<true, 4>, 4);
+  else if (a.B * a.rank >= kManyCoordinates) run(down_kernel<false, 2>, 2);
+  else run(down_kernel<false, 1>, 1);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (dtype == QS_F32) launch_rank<QS_F32>(a, order, st);
   else launch_rank<QS_BF16>(a, order, st);
