@@ -283,6 +283,42 @@ def test_same_bits(qs):
             assert torch.equal(few, a[rows]), (rank, rows)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V,rank,count", [(1025, 32003, 8, 40), (1025, 32003, 40, 3),
+                                            (257, 32003, 72, 7), (65, 128259, 128, 2)])
+def test_large_batches_match_small_ones(qs, B, V, rank, count, dtype):
+    """Batches so large that a workgroup goes over several tiles of the vocabulary give
+    every row the bits that it has among 64 or fewer; rows without an adapter stay."""
+    import torch
+    print(f"adapters B={B} V={V} rank={rank} {dtype}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(B + rank)
+    kind = torch.float32 if dtype == "f32" else torch.bfloat16
+
+    def rand(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen)
+
+    width = (V + 7) // 8 * 8
+    z = rand(B, width).to(kind)
+    x, down, up = (t.bfloat16() for t in (rand(B, 64), rand(count, rank, 64) / 8,
+                                          rand(count, V, rank) / rank ** 0.5))
+    index = torch.randint(-1, count, (B,), device="cuda", generator=gen, dtype=torch.int32)
+    scale = torch.rand(count, device="cuda", generator=gen) + 0.5
+    want = z.clone()
+    for at in range(0, B, 50):
+        rows = slice(at, at + 50)
+        qs.apply_adapters(want[rows, :V], x[rows], down, up, index[rows].contiguous(), scale)
+    out = torch.full_like(z, 7.0)
+    status = qs.apply_adapters(z[:, :V], x, down, up, index, scale, out=out[:, :V])
+    assert not status.any()
+    assert torch.equal(out[:, :V], want[:, :V])
+    assert bool((out[:, V:] == 7.0).all())
+    assert torch.equal(out[index < 0][:, :V], z[index < 0][:, :V])
+    assert not torch.equal(out[index >= 0][:, :V], z[index >= 0][:, :V])
+    kept = z.clone()
+    qs.apply_adapters(z[:, :V], x, down, up, index, scale)
+    assert torch.equal(z[:, :V], want[:, :V]) and torch.equal(z[:, V:], kept[:, V:])
+
+
 def test_inference_mode(qs):
     import torch
     with torch.inference_mode():
