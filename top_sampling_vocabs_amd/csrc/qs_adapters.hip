@@ -156,6 +156,16 @@ __device__ __forceinline__ void place_rows(const Args& a, int row0, Place* order
   order[segment + (int)count] = Place{r, mine == 0x80000000u ? -1 : asked};
 }
 
+// The sum over 16 neighbouring lanes, in each of them.
+__device__ __forceinline__ float sum_of_16(float v) {
+  auto add = [&](uint32_t other) { v += __uint_as_float(other); };
+  add(dpp_u32<kDppXor1>(__float_as_uint(v)));
+  add(dpp_u32<kDppXor2>(__float_as_uint(v)));
+  add(dpp_u32<kDppHalfMirror>(__float_as_uint(v)));
+  add(dpp_u32<kDppMirror>(__float_as_uint(v)));
+  return v;
+}
+
 // The rows' coordinates, a wave to each row and rank or few ranks: few rows spread over as many
 // compute units as they have ranks, each wave requests up to 8 KiB of the factor before
 // it uses any, and rows that share an adapter read it from the L2. (On the matrix cores,
@@ -243,8 +253,8 @@ __global__ void __launch_bounds__(256)
     }
     u = v[0];
 #pragma unroll
-    for (int o = 32 / R; o > 0; o >>= 1) u += __shfl_xor(u, o, 64);
-    u *= scale;
+    for (int o = 32 / R; o >= 16; o >>= 1) u += __shfl_xor(u, o, 64);
+    u = sum_of_16(u) * scale;
   } else {
     q += lane / (64 / R);
   }
