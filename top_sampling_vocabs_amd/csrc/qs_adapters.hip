@@ -70,9 +70,9 @@ constexpr int kOperandBytes = 64 * 16;
 int operands_of(int64_t rank) {
   return rank <= 8 ? 1 : rank <= 16 ? 2 : (int)((rank + 31) / 32) * kTerms;
 }
-// Coordinates per row, with the zeros behind the last (and in unused groups).
+// Coordinates per row, with the zeros behind the last.
 int places_of(int64_t rank) {
-  return rank <= 8 ? 16 : (int)((rank + 31) / 32) * 32;
+  return rank <= 16 ? (int)rank : (int)((rank + 31) / 32) * 32;
 }
 
 // Behind them, for a batch of at most kRows rows, its plan: the rows in the order of
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(256)
   const int g = q >> 3;
 #pragma unroll
   for (int k = 0; k < kTerms; ++k) {
-    const int to = operands == 1 ? (q < 8 ? k : 3)
-                   : operands == 2 ? (q < 16 ? 2 * k + g : 4 + g)
+    const int to = operands == 1 ? k
+                   : operands == 2 ? 2 * k + g
                                    : (g >> 2) * 4 * kTerms + 4 * k + (g & 3);
     // the upper half of the bits: rounded it could pass the largest number
     const uint32_t part = __float_as_uint(u) & 0xFFFF0000u;
@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(256)
     // an infinity's (or NaN's) other terms are 0, so that its products are the formula's
     u = fabsf(u) < INFINITY ? u - __uint_as_float(part) : 0.0f;
   }
+  // the groups that short ranks leave free
+  if (operands <= 2) *reinterpret_cast<uint16_t*>(out + (operands == 1 ? 3 : 6 + g) * 256) = 0;
 }
 
 // The logits. A wave takes kTiles tiles of 16 vocabulary rows and up to RT tiles of 16
