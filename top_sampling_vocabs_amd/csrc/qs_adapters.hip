@@ -27,8 +27,8 @@
 // reaches 5.2); on three of rank 64, 4096 columns, 5.8 and 18.3 us (5.3 TB/s); 16 rows of
 // 128256 fp32, each its own of rank 32, 4.0 and 22.6 us (6.4 TB/s); 1 row of 151936, rank
 // 16, 3.4 and 3.8 us, two dependent loads each. Both together, 151936 bf16, 2048 columns:
-// 512 rows on 8 and 64 adapters of rank 16 103 and 136 us, 2048 rows on one and 64 of them
-// 296 and 362 (4.2 and 4.3 TB/s), on 4 of rank 64 436 (3.1 TB/s: the products and the
+// 512 rows on 8 and 64 adapters of rank 16 102 and 135 us, 2048 rows on one and 64 of them
+// 295 and 361 (4.3 and 4.4 TB/s), on 4 of rank 64 434 (3.1 TB/s: the products and the
 // coordinates' way to them).
 
 #include <hip/hip_runtime.h>
@@ -166,8 +166,8 @@ __device__ __forceinline__ float sum_of_16(float v) {
   return v;
 }
 
-// The rows' coordinates, a wave to each row and rank or few ranks: few rows spread over as many
-// compute units as they have ranks, each wave requests up to 8 KiB of the factor before
+// The rows' coordinates, a wave to each row and rank or few ranks: few rows spread over as
+// many compute units as they have ranks, each wave requests up to 8 KiB of the factor before
 // it uses any, and rows that share an adapter read it from the L2. (On the matrix cores,
 // 16 ranks and the rows that share an adapter to a workgroup: 1 row of 4096 columns, rank
 // 16, 6.5 us, one compute unit's loads, against 3.5; 64 rows of 8192 on adapters of their
