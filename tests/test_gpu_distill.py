@@ -917,3 +917,38 @@ def test_longest_row(qs):
     named = np.array([np.exp(-30.0) / S - 0.25, 1.0 / S - 0.5])
     wanted = np.array([w[0], w[1], named[0], w[1], named[1]])
     assert (np.abs(got - wanted) <= (2.0 ** -8 + 2e-4) * np.abs(wanted)).all(), (got, wanted)
+
+
+def few_in_a_list(rng, B, V, K, rest, span):
+    """Lists of K tokens anywhere; rest: of probability 0.6 together, else logits of
+    either sign up to `span`."""
+    ids = np.stack([rng.permutation(V)[:K] for _ in range(B)]).astype(np.int32)
+    values = np.log(0.6 * rng.dirichlet(np.ones(K), B)) if rest else rng.uniform(-span, span, (B, K))
+    return ids, values.astype(np.float32)
+
+
+def far_apart(V):
+    """Finite logits further apart than float32's largest value, and temperatures that weigh
+    them all: in any order (every wave has both ends), falling, and in two halves (waves
+    and parts lie apart)."""
+    T = np.repeat(np.array([1e36, 4e36, 1e37, 1e38, 1.2e38, 1.3e38, 2e38, 3.4e38], np.float32), 3)
+    rng = np.random.default_rng(V)
+    z = rng.uniform(-3.3e38, 3.3e38, (T.size, V))
+    z[1::3] = np.linspace(3.3e38, -3.3e38, V)
+    z[2::3] = np.where(np.arange(V) < V // 2, -3.3e38, 3.3e38)
+    return rng, bf16(z), T
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 500, 1000, 3001, 20001, 70003])
+def test_largest_temperatures(qs, V, dtype, rest):
+    """Temperatures up to float32's largest value. log2(e) / T is below the least normal
+    float32 from 1.2e38 on, where it is still good to 2^-22.5 of itself: 2 u |a| more than
+    above, and |a| is below 5.6 there, 12 units against the 128 and more that a sum's
+    tolerance has for its additions."""
+    print(f"distill largest temperatures V={V} {dtype} rest={rest}", flush=True)
+    rng, z, T = far_apart(V)
+    ids, values = few_in_a_list(rng, T.size, V, 5, rest, 3e38)
+    _, _, _, out = run(qs, z, dtype, ids, values, T, None, rest)
+    check(z, ids, values, T, None, rest, out)

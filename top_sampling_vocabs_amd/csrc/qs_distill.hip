@@ -79,6 +79,14 @@ int loads_for(int64_t B, int64_t V, int dtype, bool mask) {
 
 constexpr uint32_t kBadSlot = 1u, kNonfinite = 2u;
 
+// The exponent of a wave's or a part's sum against the row's. From halves: finite logits
+// may lie further apart than float32's largest value, at temperatures where that is
+// little. (A difference inside a wave that passes it is either taken by a multiply-add or
+// an exponent past 2^24.)
+__device__ __forceinline__ float apart(float m, float top, float c) {
+  return fmaxf((0.5f * m - 0.5f * top) * c * 2.0f, -200.0f);
+}
+
 // A thread's slots j = i * THREADS + tid: the teacher's value and the student's logit
 // of those that name a legal token.
 template <int DT, int THREADS, int N>
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(THREADS)
     p.dup |= s_dup[q];
   }
 #pragma unroll
-  for (int q = 0; q < kWavesHere; ++q) p.S += s_S[q] * exp2_hw(rel(s_m[q], p.m, c));
+  for (int q = 0; q < kWavesHere; ++q) p.S += s_S[q] * exp2_hw(apart(s_m[q], p.m, c));
   if constexpr (ROW) {
     finish_row<DT, FT, N>(a, r, tid, slots, p, s_fin);
   } else {
@@ -427,8 +435,8 @@ __global__ void __launch_bounds__(THREADS)
     dup |= p[k].dup;
   }
   m = wave_max_f32(m);
-  float S = mine.S * exp2_hw(rel(mine.m, m, c));
-  for (int k = lane + 64; k < parts; k += 64) S += p[k].S * exp2_hw(rel(p[k].m, m, c));
+  float S = mine.S * exp2_hw(apart(mine.m, m, c));
+  for (int k = lane + 64; k < parts; k += 64) S += p[k].S * exp2_hw(apart(p[k].m, m, c));
   const Part rest{m, wave_sum_f32(S), ballot(any != 0u) != 0, ballot(dup != 0u) != 0};
   finish_row<DT, THREADS, kJoinSlots>(a, r, tid, slots, rest, s_fin);
 }
