@@ -952,3 +952,16 @@ def test_largest_temperatures(qs, V, dtype, rest):
     ids, values = few_in_a_list(rng, T.size, V, 5, rest, 3e38)
     _, _, _, out = run(qs, z, dtype, ids, values, T, None, rest)
     check(z, ids, values, T, None, rest, out)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 1000, 3001, 40003])
+def test_grad_at_largest_temperatures(qs, V, dtype, rest):
+    """The same rows' gradient, incoming gradients large enough that their quotients by T are
+    normal numbers; the 2 u |a| of such temperatures are within the tolerance's 8."""
+    print(f"distill grad largest temperatures V={V} {dtype} rest={rest}", flush=True)
+    rng, z, T = far_apart(V)
+    ids, values = few_in_a_list(rng, T.size, V, 5, rest, 3e38)
+    g = (1e36 * rng.normal(0, 1, T.size)).astype(np.float32)
+    check_grad(qs, z, dtype, ids, values, T, None, rest, g)

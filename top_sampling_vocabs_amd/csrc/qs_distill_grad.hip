@@ -92,6 +92,10 @@ __global__ void __launch_bounds__(kBlock) distill_grad_kernel(GradArgs a, int ch
   const float m = state[0], ls = state[1], mr = state[2], rest_grad = state[4], tmax = state[5],
               tls = state[6], over = state[7];
   const float c = scale_of(T), lsr2 = state[3] * kLog2e;
+  // Differences from m_R at temperatures that weigh ones past float32's largest value are
+  // taken as halves: the factor is exact, and 1 elsewhere, where it changes no bit.
+  const bool far = c < 1e-30f;
+  const float h = far ? 0.5f : 1.0f, mr_h = mr * h, c_h = far ? 2.0f * c : c;
   // finite where g is, so that a token of no weight gets 0; an infinite or NaN g goes
   // through to every legal token
   float coef = (float)((double)g * (double)rest_grad / (double)T);
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(kBlock) distill_grad_kernel(GradArgs a, int ch
     float x[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      const float l = fmaxf((token<DT>(v[u], e) - mr) * c - lsr2, -200.0f);
+      const float l = fmaxf(fmaf(fmaf(token<DT>(v[u], e), h, -mr_h), c_h, -lsr2), -200.0f);
       x[e] = exp2_hw(l) * coef;
     }
     uint32_t o[4];
