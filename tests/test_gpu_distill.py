@@ -965,3 +965,23 @@ def test_grad_at_largest_temperatures(qs, V, dtype, rest):
     ids, values = few_in_a_list(rng, T.size, V, 5, rest, 3e38)
     g = (1e36 * rng.normal(0, 1, T.size)).astype(np.float32)
     check_grad(qs, z, dtype, ids, values, T, None, rest, g)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3001, 40003])
+def test_grad_past_the_largest_factor(qs, V, dtype, rest):
+    """Rows whose factor g (Q p_R - q_R) / T passes float32's largest value while their
+    elements, each its share of it, do not: they are the formula's all the same."""
+    print(f"distill grad factor V={V} {dtype} rest={rest}", flush=True)
+    rng = np.random.default_rng(V)
+    T = np.array([1.0, 1.0, 0.9, 1e-2, 1e-2, 1e-3, 2.0 ** -20, 1e-38], np.float32)
+    g = np.array([3.4e38, -3.4e38, 3.4e38, 2e37, -2e36, 1e37, 3e33, 100.0], np.float32)
+    B = T.size
+    z = make(V, B, V, "normal")
+    z[4:] = -2.5                           # tokens that share the mass at any temperature
+    ids, values = few_in_a_list(rng, B, V, 5, rest, 3.0)
+    check_grad(qs, z, dtype, ids, values, T, None, rest, g)
+    legal = rng.random((B, V)) < 0.5
+    legal[:, :2] = True
+    check_grad(qs, z, dtype, ids, values, T, legal, rest, g)

@@ -96,10 +96,18 @@ __global__ void __launch_bounds__(kBlock) distill_grad_kernel(GradArgs a, int ch
   // taken as halves: the factor is exact, and 1 elsewhere, where it changes no bit.
   const bool far = c < 1e-30f;
   const float h = far ? 0.5f : 1.0f, mr_h = mr * h, c_h = far ? 2.0f * c : c;
-  // finite where g is, so that a token of no weight gets 0; an infinite or NaN g goes
-  // through to every legal token
-  float coef = (float)((double)g * (double)rest_grad / (double)T);
-  if (fabsf(g) < INFINITY) coef = fminf(fmaxf(coef, -3e38f), 3e38f);
+  // finite where g is, so that a token of no weight gets 0: of a factor past the largest
+  // value a power of two goes into the exponents, so that what has a small share of it
+  // gets that; an infinite or NaN g goes through to every legal token
+  const double factor = (double)g * (double)rest_grad / (double)T;
+  float coef = (float)factor, bias = -lsr2;
+  if (__builtin_expect(ballot(fabsf(coef) > 3e38f && fabsf(g) < INFINITY) != 0, 0)) {
+    const int n = __builtin_amdgcn_frexp_exp(factor) - 127;  // coef from 2^126 up
+    const double sum = n - (double)lsr2;
+    bias = (float)sum;
+    // the bias's rounding is taken back
+    coef = (float)(ldexp(factor, -n) * (1.0 + 0.6931471805599453 * (sum - (double)bias)));
+  }
 
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kBlock) distill_grad_kernel(GradArgs a, int ch
     float x[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      const float l = fmaxf(fmaf(fmaf(token<DT>(v[u], e), h, -mr_h), c_h, -lsr2), -200.0f);
+      const float l = fmaxf(fmaf(fmaf(token<DT>(v[u], e), h, -mr_h), c_h, bias), -200.0f);
       x[e] = exp2_hw(l) * coef;
     }
     uint32_t o[4];
