@@ -283,6 +283,54 @@ def test_same_bits(qs):
             assert torch.equal(few, a[rows]), (rank, rows)
 
 
+@pytest.mark.parametrize("K", [520, 1032, 2056, 4104, 8192])
+@pytest.mark.parametrize("B,rank", [(64, 64), (64, 128), (65, 64), (130, 16), (130, 64)])
+def test_widths_of_several_ranks_a_wave(qs, B, rank, K):
+    """Widths over several requests of a wave, and over several turns of its loop, where a
+    wave takes two ranks (64 rows) or four (more)."""
+    print(f"adapters B={B} rank={rank} K={K}", flush=True)
+    case = inputs(K + B, B, 72, K, rank, 3)
+    got, status = run(qs, case[0], "f32", *case[1:])
+    assert not status.any()
+    check(case[0], "f32", *case[1:], got)
+
+
+@pytest.mark.parametrize("rank", [8, 64, 128])
+@pytest.mark.parametrize("K", [1032, 2056, 4104])
+def test_same_bits_of_wide_rows(qs, K, rank):
+    """A row's bits with one, two and four ranks a wave, in batches of any size."""
+    import torch
+    z, x, down, up, scale, index = inputs(K, 150, 333, K, rank, 5)
+    a, _ = run(qs, z, "f32", x, down, up, scale, index)
+    for rows in ([5], list(range(20, 40)), list(range(60, 124)), list(range(149, 80, -1))):
+        few, _ = run(qs, z[rows], "f32", x[rows], down, up, scale, index[rows])
+        assert torch.equal(few, a[rows]), (K, rank, rows)
+
+
+@pytest.mark.parametrize("rank", [8, 40, 128])
+def test_large_batches_of_wide_rows(qs, rank):
+    """A thousand rows of several thousand columns against the same rows among 50."""
+    import torch
+    B, V, K, count = 1025, 4001, 4104, 6
+    print(f"adapters B={B} K={K} rank={rank}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(rank)
+
+    def rand(*shape):
+        return torch.randn(*shape, device="cuda", generator=gen)
+
+    z = rand(B, V + 7).bfloat16()[:, :V]
+    x, down, up = (t.bfloat16() for t in (rand(B, K), rand(count, rank, K) / K ** 0.5,
+                                          rand(count, V, rank) / rank ** 0.5))
+    index = torch.randint(-1, count, (B,), device="cuda", generator=gen, dtype=torch.int32)
+    out = torch.empty_strided(z.shape, z.stride(), dtype=z.dtype, device="cuda")
+    status = qs.apply_adapters(z, x, down, up, index, out=out)
+    assert not status.any()
+    for at in range(0, B, 50):
+        rows = slice(at, at + 50)
+        qs.apply_adapters(z[rows], x[rows], down, up, index[rows].contiguous())
+    assert torch.equal(out, z)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("B,V,rank,count", [(1025, 32003, 8, 40), (1025, 32003, 40, 3),
                                             (257, 32003, 72, 7), (65, 128259, 128, 2)])
