@@ -985,3 +985,98 @@ def test_grad_past_the_largest_factor(qs, V, dtype, rest):
     legal = rng.random((B, V)) < 0.5
     legal[:, :2] = True
     check_grad(qs, z, dtype, ids, values, T, legal, rest, g)
+
+
+def rows_on_gpu(seed, B, V, dtype, masked):
+    """A large batch made on the GPU: its logits, mask words (or None), and a function that
+    gives given rows of both as the checks take them."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    kind = torch.float32 if dtype == "f32" else torch.bfloat16
+    lg = torch.empty(B, -(-V // 8) * 8, dtype=kind, device="cuda")
+    for at in range(0, B, 64):
+        lg[at:at + 64] = 3 * torch.randn(lg[at:at + 64].shape, generator=gen, device="cuda")
+    words = None
+    if masked:
+        words = torch.randint(-2 ** 31, 2 ** 31, (B, -(-V // 32)), generator=gen, device="cuda")
+        words = words.to(torch.int32)
+
+    def rows(at):
+        z = lg[at, :V].float().cpu().numpy()
+        if words is None:
+            return z, None
+        bits = words[at].cpu().numpy().view(np.uint8)
+        return z, np.unpackbits(bits, axis=1, bitorder="little")[:, :V].astype(bool)
+
+    return lg[:, :V], words, rows
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("B,V,dtype,masked", [
+    (600, 1500, "f32", False), (600, 1500, "f32", True),          # whole rows, 128 threads
+    (600, 3001, "bf16", False), (600, 3001, "bf16", True),
+    (600, 6000, "bf16", True), (600, 9001, "f32", False), (600, 20001, "bf16", True),
+    (300, 20001, "f32", False), (300, 20001, "f32", True),        # 512 threads, 16 loads
+    (300, 40003, "bf16", False), (300, 40003, "bf16", True),
+    (300, 151936, "bf16", False), (300, 151936, "bf16", True),    # parts of 8 loads
+    (700, 100003, "bf16", True), (200, 128259, "f32", False), (200, 128259, "f32", True),
+    (600, 151936, "bf16", False),                                 # parts of 16
+])
+def test_many_rows(qs, B, V, dtype, masked, rest):
+    """Batches that are cut in other ways than a few rows are, values of every kind of
+    magnitude in every lane: some rows against the oracle, the gradient too."""
+    import torch
+    print(f"distill many rows B={B} V={V} {dtype} masked={masked} rest={rest}", flush=True)
+    rng = np.random.default_rng(B + V)
+    lg, words, rows = rows_on_gpu(B + V, B, V, dtype, masked)
+    ids = ((rng.integers(0, V, B)[:, None] + np.arange(33) * (V // 40)) % V).astype(np.int32)
+    ids[::3, 5:9] = -1
+    values = np.log(0.7 * rng.dirichlet(np.ones(33), B)).astype(np.float32)
+    T = rng.uniform(0.4, 2.0, B).astype(np.float32)
+    g = rng.normal(0, 1, B).astype(np.float32)
+    t, d = args_of(ids, values, T)
+    d["bitmask"] = words
+    out = qs.distill_loss(lg, *t, rest=rest, **d)
+    grad = qs.distill_loss_backward(lg, *t, out["state"], out["status"],
+                                    torch.from_numpy(g).cuda(), rest=rest, **d)
+    torch.cuda.synchronize()
+    assert not out["status"].any()
+    at = np.unique(np.concatenate(([0, 1, B // 2, B - 2, B - 1], rng.integers(0, B, 4))))
+    pick = torch.from_numpy(at).cuda()
+    z, legal = rows(pick)
+    some = {k: v[pick] for k, v in out.items()}
+    check(z, ids[at], values[at], T[at], legal, rest, some)
+    compare_grad(z, dtype, ids[at], values[at], T[at], legal, rest, g[at], some, grad[pick])
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V", [(3, 3001), (3, 6000), (3, 9001), (3, 20001), (3, 40003),
+                                 (300, 20001), (300, 40003), (600, 3001)])
+def test_long_lists_of_any_row(qs, B, V, dtype, rest):
+    """Lists longer than one wave's slots, worked out by all waves of a row's workgroup
+    (128 to 1024 threads) or of the join's."""
+    import torch
+    print(f"distill long lists B={B} V={V} {dtype} rest={rest}", flush=True)
+    rng = np.random.default_rng(B + V)
+    lg, _, rows = rows_on_gpu(B + V, B, V, dtype, False)
+    at = np.unique([0, B // 2, B - 1])
+    pick = torch.from_numpy(at).cuda()
+    z, _ = rows(pick)
+    for K in (257, 513, 700, 1024):
+        # distinct tokens, close together and far apart
+        step = rng.choice([1, max(V // 1100, 1)], B)
+        ids = ((rng.integers(0, V, B)[:, None] + np.arange(K) * step[:, None]) % V).astype(np.int32)
+        ids = rng.permuted(ids, axis=1)
+        ids[:, 100:110] = -1
+        values = np.log(0.9 * rng.dirichlet(np.ones(K), B)).astype(np.float32)
+        values[:, K - 1] = -np.inf
+        t, _ = args_of(ids, values)
+        out = qs.distill_loss(lg, *t, rest=rest)
+        torch.cuda.synchronize()
+        assert not out["status"].any()
+        check(z, ids[at], values[at], None, None, rest, {k: v[pick] for k, v in out.items()})
+        # a token named twice is found wherever its slots are
+        ids[:, K - 1] = ids[:, 3]
+        again = qs.distill_loss(lg, torch.from_numpy(ids).cuda(), t[1], rest=rest)
+        assert bool((again["status"] == oracle.ROW_BAD_PARAM).all())
