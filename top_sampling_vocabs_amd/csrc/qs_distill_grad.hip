@@ -37,9 +37,6 @@ constexpr int kBlock = 256;
 constexpr int kLoads = 4;                     // 16-byte loads per lane
 constexpr int kSlots = kSlotsMax / kBlock;    // slots per thread
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
 template <int DT, bool MASK>
 __global__ void __launch_bounds__(kBlock) distill_grad_kernel(GradArgs a, int chunks) {
   constexpr int P = kPer<DT>, kSpan = kBlock * kLoads * P;

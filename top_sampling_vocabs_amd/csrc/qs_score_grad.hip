@@ -33,6 +33,7 @@
 #include "../../include/qs.h"
 #include "qs_device.hpp"
 #include "qs_score.hpp"
+#include "qs_softmax.hpp"
 
 namespace qs {
 namespace score {
@@ -40,11 +41,6 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kLoads = 4;  // 16-byte loads per lane
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-template <int DT> constexpr int kPer = DT == QS_F32 ? 4 : 8;  // tokens per 16-byte load
 
 // x within +-most; as it is where `keep` is set (fmaxf would turn a NaN into -most)
 __device__ __forceinline__ float clamp_to(float x, float most, bool keep) {
@@ -85,9 +81,9 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   }
 
   const float T = a.T ? a.T[r] : 1.0f;
-  const float c = fminf(fmaxf(1.4426950408889634f / T, 1.4e-45f), 3.4e38f);
+  const float c = scale_of(T);
   const float m = a.row_max[r];
-  const float ls = a.log_sum[r], ls2 = ls * 1.4426950408889634f;
+  const float ls = a.log_sum[r], ls2 = ls * kLog2e;
   float gs = 0.0f;
   int only = -1;
   if constexpr (ONE) {
@@ -138,7 +134,7 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
   // and NaN go through to every legal token
   const bool lost = !(fabsf(gs) < INFINITY && fabsf(gH) < INFINITY && fabsf(H) < INFINITY);
   const float A = clamp_to(-(gs + gH * H) / T, 3e38f, lost);
-  const float Bc = clamp_to(-gH * 0.6931471805599453f / T, 1e36f, lost);
+  const float Bc = clamp_to(-gH * kLn2 / T, 1e36f, lost);
 
   auto logit = [](const uint32_t* w, int e) {
     if constexpr (DT == QS_F32) return __uint_as_float(w[e]);
@@ -158,9 +154,7 @@ __global__ void __launch_bounds__(kBlock) grad_kernel(GradArgs a, int chunks) {
     slots = s_slots;
     for (int j = tid; j < slots; j += kBlock) {
       const int d = s_slot[j].x, i = begin + d;
-      float z;
-      if constexpr (DT == QS_F32) z = reinterpret_cast<const float*>(row)[i];
-      else z = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
+      const float z = logit_at<DT>(row, i);
       bool is_legal = true;
       if constexpr (MASK)
         is_legal = (a.bitmask[(size_t)r * a.bm_stride + (i >> 5)] >> (i & 31)) & 1u;

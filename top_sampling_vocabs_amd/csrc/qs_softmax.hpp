@@ -12,6 +12,9 @@ namespace qs {
 namespace score {
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // |k_w| up to which exponents may be taken against k_w: its rounding, the exponent
