@@ -576,8 +576,9 @@ QS_API int qs_head_logits(const void* hidden, int64_t B, int64_t K, int64_t hidd
  *                twice; a legal token's value that is NaN or +inf, or with rest = 1
  *                above 1), then as for qs_filter_mask. An error row gets NaN in loss and
  *                row_state.
- * A slot that names an illegal token counts as empty. workspace:
- * qs_distill_loss_workspace_bytes(B, V, dtype) bytes, 256-byte aligned (NULL / 0 when
+ * A slot that names an illegal token counts as empty. Finite logits may be any; a T
+ * below 4.3e-39 weighs the rest's tokens against each other as that one does.
+ * workspace: qs_distill_loss_workspace_bytes(B, V, dtype) bytes, 256-byte aligned (NULL / 0 when
  * that is 0), as for qs_token_logprobs; the size for B rows does for any smaller
  * batch. Logits are read once, in float32 sums joined in a fixed order (the same call
  * gives the same bits); what a row does with its slots is done in float64. Nothing is
@@ -603,8 +604,10 @@ QS_API int qs_distill_loss(const void* logits, int dtype, int64_t B, int64_t V,
  *               dtype, 0 on rows whose row_status is not QS_ROW_OK, it may be the
  *               logits' own buffer
  * Computed in float32 (named tokens in float64), rounded to float32 and once to the
- * dtype. An infinite or NaN incoming gradient leaves no legal token of its row a
- * finite gradient. One kernel launch on `stream`; nothing is allocated. */
+ * dtype; a row's factors may pass float32's largest value where its elements do not. A
+ * p_i / p_R below 2^-126 may count as 0. An infinite or NaN incoming gradient leaves no
+ * legal token of its row a finite gradient. One kernel launch on `stream`; nothing is
+ * allocated. */
 QS_API int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, int64_t V,
                       int64_t row_stride, const float* temperature, const uint32_t* bitmask,
                       int64_t bitmask_stride, const int32_t* teacher_ids,
@@ -616,8 +619,8 @@ QS_API int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, in
 /* Low-rank adapters of many requests beside a shared output projection: each row's
  * logits z (qs_head_logits', or any projection's) moved by its own adapter a =
  * index[b]:
- *   y[b][v] = z[b][v] + scale[a] * sum over r of up[a][v][r] *
- *             sum over k of down[a][r][k] * hidden[b][k]
+ *   y[b][v] = z[b][v] + sum over r of up[a][v][r] * u[b][r],
+ *   u[b][r] = scale[a] * sum over k of down[a][r][k] * hidden[b][k]
  *
  * logits       [B][row_stride] float32 or bfloat16 (dtype), B at most 2^18, V at most
  *              2^24, 16-byte aligned, row_stride * element size a multiple of 16
@@ -641,12 +644,15 @@ QS_API int qs_distill_loss_backward(const void* logits, int dtype, int64_t B, in
  * row_status   [B] int32 out: QS_ROW_OK, or QS_ROW_BAD_PARAM for another index (y = z)
  * workspace    qs_adapters_workspace_bytes(B, rank) bytes of device scratch, 256-byte
  *              aligned, as for qs_filter_mask
- * Sums are held in float32; each logit is rounded once. A row's result depends on its
- * own hidden state, logits and adapter alone; an infinity among them gives what the
- * formula does, but one in up only a logit that is not finite (infinite or NaN). The
- * same call gives the same bits. Made for the 1 to 64 rows of a decode step; more rows
- * read each used adapter about once per 64 rows that use it. Two kernel launches on
- * `stream`; nothing is allocated. */
+ * Sums and the coordinates u are held in float32 (of a u below 2^-110 what lies below
+ * 2^-133 is lost); each logit is rounded once. A row's result depends on its own hidden
+ * state, logits and adapter alone; an infinity among them gives what the formula does,
+ * but one in up only a logit that is not finite (infinite or NaN). The same call gives
+ * the same bits, a row the same in any batch. Made for the 1 to 64 rows of a decode
+ * step, which read each used up factor once. More rows are put in the order of their
+ * adapters, 4096 at a time, and each 64 in that order read the up factors of theirs once.
+ * Down factors are read for every row, those that rows share from the L2. Two kernel
+ * launches on `stream`; nothing is allocated. */
 QS_API size_t qs_adapters_workspace_bytes(int64_t B, int64_t rank);
 QS_API int qs_apply_adapters(const void* logits, int dtype, int64_t B, int64_t V,
                       int64_t row_stride, const void* hidden, int64_t K,

@@ -268,6 +268,28 @@ def test_largest_coordinates(qs, rank, sign):
     check(z, "f32", x, down, up, None, index, got)
 
 
+@pytest.mark.parametrize("rank", [8, 16, 32, 40])
+@pytest.mark.parametrize("e", [-110, -117, -125, -134])
+def test_smallest_coordinates(qs, rank, e):
+    """Coordinates around 2^e, with factors that make them count: three truncated bf16 terms
+    leave less than one's least step, 2^-133, of each."""
+    B, V, K, count = 3, 40, 16, 1
+    z, x, down, up, _, index = inputs(9, B, V, K, rank, count)
+    z[:] = 0
+    down = half(down * 2.0 ** e)
+    up = half(up * 2.0 ** 100)
+    index[:] = 0
+    got, _ = run(qs, z, "f32", x, down, up, None, index)
+    u = x.astype(np.float64) @ down[0].astype(np.float64).T
+    w = up[0].astype(np.float64)
+    want = u @ w.T
+    # sums and roundings as for other coordinates, whose own products may be subnormal:
+    # half a step of 2^-149 for each of K
+    e_u = U * (K / 16 + 18) * (np.abs(x) @ np.abs(down[0].astype(np.float64)).T) + K * 2.0 ** -150
+    tol = (e_u + 2.0 ** -133) @ np.abs(w).T + U * (3 * rank + 8) * (np.abs(u) @ np.abs(w).T)
+    assert (np.abs(got.cpu().numpy() - want) <= 1.01 * tol).all()
+
+
 def test_same_bits(qs):
     """Twice the same call; and a row's bits whatever rows are beside it, how many there
     are, and where it stands among them."""

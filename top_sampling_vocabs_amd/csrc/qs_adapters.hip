@@ -1,11 +1,13 @@
 // Low-rank adapters of many requests beside a shared output projection: with a the
 // adapter of row b,
-//   y[b][v] = z[b][v] + scale[a] sum_r up[a][v][r] u[b][r],
-//   u[b][r] = sum_k down[a][r][k] x[b][k].
-// Two launches: the rows' low-rank coordinates scale * u, then their product with the
-// up factors on top of the logits. Every used adapter is read once per 64 rows that use
-// it, wherever they stand; what bounds the calls is reading the up factors, and the
-// logits read and written.
+//   y[b][v] = z[b][v] + sum_r up[a][v][r] u[b][r],
+//   u[b][r] = scale[a] sum_k down[a][r][k] x[b][k].
+// Two launches: the rows' low-rank coordinates u, then their product with the up factors
+// on top of the logits. Up to 64 rows read each used up factor once, wherever they stand;
+// more are taken in the order of their adapters (4096 to an order), 64 at a time, and each
+// 64 read the up factors of theirs once. Down factors are read for every row, from the L2
+// where rows share them. What bounds the calls is reading the up factors, and the logits
+// read and written.
 //
 // The second product runs on the matrix cores (16x16x32) with the factor's rows on one
 // side and 16 rows of the batch on the other. A product's column depends on its own
@@ -18,7 +20,8 @@
 // (64 rows of 151936 bf16 on 8 adapters in turn, of rank 16 20.0 us against 26.7 in the
 // batch's own order, of rank 8 17.7 against 26.4; on 16 of rank 32, fp32, 40 against 47).
 // The coordinates are float32; each is cut into three bf16 numbers of 8 bits, whose sum is
-// it, so that products are exact: three products cost nothing beside the factors' bytes
+// it (from 2^-110 up; below that bf16's least number, 2^-133, bounds what is left), so that
+// products are exact: three products cost nothing beside the factors' bytes
 // (one rounded to bf16 would cost the result 2^-8 of the adapter's share). Sums are held in
 // float32, and each logit is rounded once.
 //

@@ -8,7 +8,7 @@
 namespace qs {
 namespace adapters {
 
-constexpr int64_t kMaxB = (int64_t)1 << 18;  // a wave to each row and rank in one launch grid
+constexpr int64_t kMaxB = (int64_t)1 << 18;  // a row's number stands beside its adapter's in 31 bits
 constexpr int64_t kMaxV = (int64_t)1 << 24;
 constexpr int64_t kMaxK = 65536;
 constexpr int64_t kMaxRank = 128;
