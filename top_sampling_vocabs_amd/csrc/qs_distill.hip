@@ -206,6 +206,7 @@ __device__ __forceinline__ void finish_row(const Args& a, int r, int tid,
     if (i * THREADS >= a.K) continue;
     const bool live = (s.live >> i) & 1u;
     const bool at_m = live && s.z[i] == m, at_t = live && !a.rest && s.t[i] == tmax;
+    // by all lanes, also those whose own slot is empty: each holds the counts
     sum[1] += __popcll(ballot(at_m));
     sum[3] += __popcll(ballot(at_t));
     if (live) {
