@@ -1080,3 +1080,26 @@ def test_long_lists_of_any_row(qs, B, V, dtype, rest):
         ids[:, K - 1] = ids[:, 3]
         again = qs.distill_loss(lg, torch.from_numpy(ids).cuda(), t[1], rest=rest)
         assert bool((again["status"] == oracle.ROW_BAD_PARAM).all())
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [40, 3001, 70003])
+def test_smallest_temperatures(qs, V, dtype, rest):
+    """Temperatures down to subnormal ones, 1 / T past float32's largest value: equal maxima
+    share the row, the rest's or the listed tokens', and everything else has no weight."""
+    print(f"distill smallest temperatures V={V} {dtype} rest={rest}", flush=True)
+    T = np.repeat(np.array([2e-38, 1e-38, 3e-39, 1e-39, 1e-41, 1e-45], np.float32), 2)
+    rng = np.random.default_rng(V)
+    B = T.size
+    z = bf16(np.minimum(make(V, B, V, "normal"), 2.0))
+    ids, values = few_in_a_list(rng, B, V, 5, rest, 3.0)
+    for r in range(B):
+        others = np.setdiff1d(np.arange(V), ids[r])
+        z[r, rng.choice(others, 3, False)] = 2.5
+        if r % 2:
+            z[r, ids[r, :2]] = 2.5
+    _, _, _, out = run(qs, z, dtype, ids, values, T, None, rest)
+    check(z, ids, values, T, None, rest, out)
+    g = (T.astype(np.float64) * 1e6 * rng.uniform(1, 2, B)).astype(np.float32)
+    check_grad(qs, z, dtype, ids, values, T, None, rest, g)
